@@ -1,0 +1,22 @@
+// Arguments of the softmax-attention kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace kda {
+
+struct AttnArgs {
+    const uint16_t *q, *k, *v;   // k, v: [B, T, H_kv, D], or the caches [num_blocks, H_kv, block, D]
+    uint16_t *out;
+    float *lse;                  // NULL: not written
+    const int32_t *cu;           // NULL: B prompts of T tokens
+    const int32_t *table, *lens; // NULL: whole prompts
+    float scale;
+    int N, B, T, H_q, H_kv, D;
+    int num_blocks, block_log2, max_blocks;
+};
+
+cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream);
+
+}  // namespace kda

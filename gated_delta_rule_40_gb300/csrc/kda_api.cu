@@ -161,6 +161,11 @@ __global__ void selftest_wait_timeout_kernel(uint32_t limit) {
 
 namespace {
 thread_local int t_last_launches = 0;
+}  // namespace
+namespace kda {
+void set_last_launches(int n) { t_last_launches = n; }
+}  // namespace kda
+namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -203,6 +208,8 @@ const char *kda_status_string(int code) {
         case KDA_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait timed out";
         case KDA_ERR_BAD_SEQLENS: return "malformed cu_seqlens";
         case KDA_ERR_WORKSPACE: return "workspace missing, too small or misaligned";
+        case KDA_ERR_NO_BLOCKS: return "no free cache block left";
+        case KDA_ERR_BAD_PAGES: return "a block id or slot outside the cache";
         default: return "unknown status";
     }
 }

@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -27,6 +27,8 @@ KDA_ERR_CUDA = -3
 KDA_ERR_DEVICE_TIMEOUT = -4
 KDA_ERR_BAD_SEQLENS = -5
 KDA_ERR_WORKSPACE = -6
+KDA_ERR_NO_BLOCKS = -7
+KDA_ERR_BAD_PAGES = -8
 
 
 class KdaLibraryError(RuntimeError):
@@ -81,6 +83,14 @@ def load() -> ctypes.CDLL:
     lib.kda_la_fwd.restype = I
     lib.kda_la_decode.argtypes = [P, P, P, P, F, P, I, I, I, I, I, P, P]
     lib.kda_la_decode.restype = I
+    lib.kda_page_plan.argtypes = [P] * 5 + [I] * 5 + [P] * 5 + [P]
+    lib.kda_page_plan.restype = I
+    lib.kda_kv_write.argtypes = [P] * 5 + [I] * 5 + [P]
+    lib.kda_kv_write.restype = I
+    lib.kda_attn_fwd.argtypes = [P, P, P, F, P, I, I, I, I, I, I, P, P, P]
+    lib.kda_attn_fwd.restype = I
+    lib.kda_attn_paged.argtypes = [P, P, P, F, P, P, P] + [I] * 8 + [P, P, P]
+    lib.kda_attn_paged.restype = I
     lib.kda_status_string.argtypes = [I]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_get_status.argtypes = [P]
@@ -512,3 +522,120 @@ def kda_fwd_bf16_state(q, k, v, graw, b, A_log, scale: float, initial_state=None
                                 _ptr(out), _stream(stream))
     _raise(rc, "kda_fwd_bf16_state")
     return out, final_state
+
+
+class PagePlan(NamedTuple):
+    """What ``kda_page_plan`` writes besides the new block-table entries (all int32, on the device)."""
+    cu_seqlens: torch.Tensor   # [N+1]  packed offsets of the new tokens
+    seq_lens: torch.Tensor     # [N]    cached + new tokens
+    slots: torch.Tensor        # [T]    cache slot of each new token, -1 past the last
+    positions: torch.Tensor    # [T]    position of each new token in its request, -1 past the last
+    free_next: torch.Tensor    # [1]    first entry of free_blocks that was not taken
+
+
+def kda_page_plan(cached_lens, new_lens, free_blocks, free_start, block_table, block_size: int, num_tokens: int,
+                  stream=None) -> PagePlan:
+    """Block table, slot map and packed offsets of one serving step, from lengths
+    on the device: cached_lens, new_lens [N], free_blocks [F] (ids of unused
+    blocks), free_start [1] (the first of them to take) and block_table
+    [N,max_blocks] (new entries written in place), all int32.  ``num_tokens`` is
+    the size of the slot map: the number of new tokens, or more."""
+    lib = load()
+    i32 = torch.int32
+    N = cached_lens.numel()
+    _check(cached_lens, "cached_lens", i32, (N,))
+    _check(new_lens, "new_lens", i32, (N,))
+    _check(free_blocks, "free_blocks", i32, (free_blocks.numel(),))
+    _check(free_start, "free_start", i32, (1,))
+    _check(block_table, "block_table", i32, (N, block_table.shape[-1]))
+    if num_tokens < 0:
+        raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
+    # one allocation; every part starts on 16 bytes
+    n4, t4 = (N + 4) & ~3, (num_tokens + 3) & ~3
+    buf = torch.empty(2 * n4 + 2 * t4 + 4, dtype=i32, device=cached_lens.device)
+    cu, lens, slots, pos, nxt = buf.split((n4, n4, t4, t4, 4))
+    plan = PagePlan(cu[:N + 1], lens[:N], slots[:num_tokens], pos[:num_tokens], nxt[:1])
+    rc = lib.kda_page_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks), _ptr(free_start), _ptr(block_table), N,
+                           num_tokens, block_table.shape[1], block_size, free_blocks.numel(), _ptr(cu), _ptr(lens),
+                           _ptr(slots), _ptr(pos), _ptr(nxt), _stream(stream))
+    _raise(rc, "kda_page_plan")
+    return plan
+
+
+def kda_kv_write(k, v, slots, k_cache, v_cache, stream=None) -> None:
+    """Store k, v [T,H_kv,D] (bf16) in the caches [num_blocks,H_kv,block_size,D] at
+    ``slots`` [T] (int32, kda_page_plan's); a negative slot is left out."""
+    lib = load()
+    bf = torch.bfloat16
+    T, H_kv, D = k.shape
+    nb, _, bs, _ = k_cache.shape
+    _check(k, "k", bf, (T, H_kv, D))
+    _check(v, "v", bf, (T, H_kv, D))
+    _check(slots, "slots", torch.int32, (T,))
+    _check(k_cache, "k_cache", bf, (nb, H_kv, bs, D))
+    _check(v_cache, "v_cache", bf, (nb, H_kv, bs, D))
+    rc = lib.kda_kv_write(_ptr(k), _ptr(v), _ptr(slots), _ptr(k_cache), _ptr(v_cache), T, H_kv, D, nb, bs,
+                          _stream(stream))
+    _raise(rc, "kda_kv_write")
+
+
+def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, return_lse: bool = True,
+                 stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal softmax attention over whole prompts.  Shapes: q [B,T,H_q,D]; k, v
+    [B,T,H_kv,D] (bf16, D 64 or 128, H_q a multiple of H_kv); cu_seqlens int32
+    [N+1] (device, B = 1) or None.  Returns (out [B,T,H_q,D], lse [B,T,H_q] fp32
+    or None)."""
+    lib = load()
+    bf, f32 = torch.bfloat16, torch.float32
+    B, T, H_q, D = q.shape
+    H_kv = k.shape[2]
+    N = cu_seqlens.numel() - 1 if cu_seqlens is not None else B
+    _check(q, "q", bf, (B, T, H_q, D))
+    _check(k, "k", bf, (B, T, H_kv, D))
+    _check(v, "v", bf, (B, T, H_kv, D))
+    _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
+    if out is None:
+        out = torch.empty((B, T, H_q, D), dtype=bf, device=q.device)
+    else:
+        _check(out, "out", bf, (B, T, H_q, D))
+    if lse is not None:
+        _check(lse, "lse", f32, (B, T, H_q))
+    elif return_lse:
+        lse = torch.empty((B, T, H_q), dtype=f32, device=q.device)
+    rc = lib.kda_attn_fwd(_ptr(q), _ptr(k), _ptr(v), scale, _ptr(cu_seqlens), N, B, T, H_q, H_kv, D, _ptr(out),
+                          _ptr(lse), _stream(stream))
+    _raise(rc, "kda_attn_fwd")
+    return out, lse
+
+
+def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale: float, out=None, lse=None,
+                   return_lse: bool = True, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal softmax attention of new tokens (one or many per request) over the
+    paged cache that already holds them.  Shapes: q [T,H_q,D] (bf16, packed by
+    cu_seqlens [N+1]); k_cache, v_cache [num_blocks,H_kv,block_size,D] (bf16);
+    block_table [N,max_blocks], seq_lens [N] (int32; cached + new tokens).
+    Returns (out [T,H_q,D], lse [T,H_q] fp32 or None)."""
+    lib = load()
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    T, H_q, D = q.shape
+    nb, H_kv, bs, _ = k_cache.shape
+    N = seq_lens.numel()
+    _check(q, "q", bf, (T, H_q, D))
+    _check(k_cache, "k_cache", bf, (nb, H_kv, bs, D))
+    _check(v_cache, "v_cache", bf, (nb, H_kv, bs, D))
+    _check(block_table, "block_table", i32, (N, block_table.shape[-1]))
+    _check(seq_lens, "seq_lens", i32, (N,))
+    _check(cu_seqlens, "cu_seqlens", i32, (N + 1,))
+    if out is None:
+        out = torch.empty((T, H_q, D), dtype=bf, device=q.device)
+    else:
+        _check(out, "out", bf, (T, H_q, D))
+    if lse is not None:
+        _check(lse, "lse", f32, (T, H_q))
+    elif return_lse:
+        lse = torch.empty((T, H_q), dtype=f32, device=q.device)
+    rc = lib.kda_attn_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), scale, _ptr(block_table), _ptr(seq_lens),
+                            _ptr(cu_seqlens), N, T, H_q, H_kv, D, nb, bs, block_table.shape[1], _ptr(out), _ptr(lse),
+                            _stream(stream))
+    _raise(rc, "kda_attn_paged")
+    return out, lse

@@ -37,7 +37,8 @@
  *    Faults detected on the device (malformed cu_seqlens, a bounded wait that
  *    timed out) are recorded in a per-device status word read by
  *    kda_get_status.
- *  - K and V must both be 128 (KDA_ERR_UNSUPPORTED otherwise).
+ *  - K and V must both be 128 (KDA_ERR_UNSUPPORTED otherwise); the softmax-attention
+ *    calls take a head dimension D of 64 or 128 for both.
  */
 #ifndef KDA_H_
 #define KDA_H_
@@ -64,7 +65,9 @@ enum {
     KDA_ERR_CUDA = -3,           /* a CUDA runtime call or kernel launch failed */
     KDA_ERR_DEVICE_TIMEOUT = -4, /* (status word) a bounded device-side wait gave up */
     KDA_ERR_BAD_SEQLENS = -5,    /* (status word) cu_seqlens not 0 = c0 <= c1 <= ... <= cN = T */
-    KDA_ERR_WORKSPACE = -6       /* workspace NULL, too small or not 256-byte aligned */
+    KDA_ERR_WORKSPACE = -6,      /* workspace NULL, too small or not 256-byte aligned */
+    KDA_ERR_NO_BLOCKS = -7,      /* (status word) kda_page_plan ran out of free cache blocks */
+    KDA_ERR_BAD_PAGES = -8       /* (status word) a block id or slot outside the cache */
 };
 
 /*
@@ -319,6 +322,106 @@ int kda_la_fwd(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v, co
 int kda_la_decode(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v, const float *slope,
                   float scale, float *state, int B, int H_qk, int H_v, int K, int V, kda_bf16_t *out,
                   cudaStream_t stream);
+
+/*
+ * Softmax attention for the serving step of a hybrid model: the layers between
+ * its linear-attention layers, with their paged key/value cache.  Four calls:
+ * kda_page_plan lays a step's tokens out in the cache, kda_kv_write stores their
+ * keys and values, kda_attn_paged attends over the cache, and kda_attn_fwd attends
+ * over whole prompts without one.
+ *
+ * The cache.  k_cache and v_cache are [num_blocks, H_kv, block_size, D] bf16: a
+ * block holds block_size consecutive tokens of one request, head by head, so
+ * that the keys of one (block, head) are contiguous.  block_size is a power of
+ * two, 16 to 1024; num_blocks * block_size <= 2^31 - 1.  block_table
+ * [N, max_blocks] int32 names request n's blocks in order: token p of the request
+ * is row p % block_size of block block_table[n][p / block_size], and its slot is
+ * that block id * block_size + p % block_size.
+ */
+
+/*
+ * Block table, slot map and packed offsets of one serving step, from lengths that
+ * stay on the device.  Request n has cached_lens[n] tokens in the cache and adds
+ * new_lens[n]; it owns the first ceil(cached_lens[n] / block_size) entries of its
+ * table row and takes the further ones that it needs from free_blocks, requests in
+ * order, beginning at free_blocks[*free_start].
+ *
+ *   cached_lens, new_lens [N] int32       free_blocks [num_free] int32, distinct ids
+ *   free_start  [1] int32                 free_next   [1] int32: the first id not taken
+ *   block_table [N, max_blocks] int32     the new entries are written in place
+ *   cu_seqlens  [N + 1] int32             0 and the prefix sums of new_lens
+ *   seq_lens    [N] int32                 cached_lens + new_lens
+ *   slots, positions [T] int32            each new token's cache slot and its position in
+ *                                         its request; -1 past the last token
+ *
+ * T may exceed the number of new tokens (a captured step of fixed size).  The
+ * outputs must not overlap the inputs, except that block_table is both.  Errors in
+ * the status word: KDA_ERR_BAD_SEQLENS for a negative length (taken as 0), more than T new
+ * tokens (those past T get no slot) or a request longer than its table row, and
+ * KDA_ERR_NO_BLOCKS when free_blocks ends; tokens without a block get slot -1, which
+ * kda_kv_write leaves out.
+ */
+int kda_page_plan(const int32_t *cached_lens, const int32_t *new_lens, const int32_t *free_blocks,
+                  const int32_t *free_start, int32_t *block_table, int N, int T, int max_blocks,
+                  int block_size, int num_free, int32_t *cu_seqlens, int32_t *seq_lens,
+                  int32_t *slots, int32_t *positions, int32_t *free_next, cudaStream_t stream);
+
+/*
+ * Stores the keys and values of T tokens in the cache: row slots[t] of each head
+ * becomes k[t], v[t].
+ *
+ *   k, v [T, H_kv, D] bf16     slots [T] int32, distinct where not negative
+ *
+ * A negative slot is left out; one outside the cache is left out and sets
+ * KDA_ERR_BAD_PAGES in the status word.  D is 64 or 128.
+ */
+int kda_kv_write(const kda_bf16_t *k, const kda_bf16_t *v, const int32_t *slots,
+                 kda_bf16_t *k_cache, kda_bf16_t *v_cache, int T, int H_kv, int D, int num_blocks,
+                 int block_size, cudaStream_t stream);
+
+/*
+ * Causal softmax attention over whole prompts:
+ *
+ *   s_ij = scale q_i . k_j (j <= i),  lse_i = log sum_j exp s_ij,  o_i = sum_j exp(s_ij - lse_i) v_j
+ *
+ *   q, out [B, T, H_q, D] bf16     k, v [B, T, H_kv, D] bf16     lse [B, T, H_q] fp32 or NULL
+ *
+ * H_q is a multiple of H_kv, at most 128 times it; query head h reads key/value
+ * head h / (H_q / H_kv).  D is 64 or 128.  cu_seqlens as kda_fwd (B = 1, N packed
+ * prompts), else B prompts of T tokens.  A malformed cu_seqlens sets
+ * KDA_ERR_BAD_SEQLENS and writes nothing.  Scores, the softmax's statistics and the
+ * output sums are fp32; exp(s - max) enters the second product rounded to bf16.
+ * The values a query may not see are multiplied by an exact 0, so a NaN or infinity
+ * in v of a later token of the same prompt reaches earlier tokens, as it does in a masked matrix
+ * product; tokens of other prompts never do.
+ */
+int kda_attn_fwd(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v, float scale,
+                 const int32_t *cu_seqlens, int N, int B, int T, int H_q, int H_kv, int D,
+                 kda_bf16_t *out, float *lse, cudaStream_t stream);
+
+/*
+ * Causal softmax attention of new tokens over the paged cache, which already holds
+ * their keys and values (kda_kv_write).  Request n's new tokens are rows
+ * cu_seqlens[n] .. cu_seqlens[n+1]-1 of q, the last of its seq_lens[n] tokens: new
+ * token i stands at position seq_lens[n] - (new tokens) + i and sees the keys up to
+ * its own.  One token (decode), a few (verification of drafted ones) or a chunk of
+ * a prompt, in any mixture.
+ *
+ *   q, out [T, H_q, D] bf16     k_cache, v_cache as above     lse [T, H_q] fp32 or NULL
+ *   block_table [N, max_blocks], seq_lens [N], cu_seqlens [N + 1] int32 (kda_page_plan's)
+ *
+ * Heads, D and precision as kda_attn_fwd.  A token whose position is negative
+ * (seq_lens[n] below the number of new tokens) sees no key: out = 0, lse = -infinity.  Rows of
+ * out and lse past cu_seqlens[N] are not written.  Nothing past seq_lens[n] is read
+ * as a key or value, whatever the block holds there, nor any table entry past its blocks.
+ * Errors in the status word: KDA_ERR_BAD_SEQLENS for cu_seqlens not 0 = c0 <= ... <= cN <= T
+ * or seq_lens outside 0 .. max_blocks * block_size (nothing is written), and
+ * KDA_ERR_BAD_PAGES for a block id outside the cache (its keys and values count as zeros).
+ */
+int kda_attn_paged(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_bf16_t *v_cache,
+                   float scale, const int32_t *block_table, const int32_t *seq_lens,
+                   const int32_t *cu_seqlens, int N, int T, int H_q, int H_kv, int D, int num_blocks,
+                   int block_size, int max_blocks, kda_bf16_t *out, float *lse, cudaStream_t stream);
 
 /* Self-test of the device-side failure path: queues one tiny kernel whose bounded
  * wait on a barrier that nothing completes gives up, recording
