@@ -3,10 +3,12 @@
 Bounds, element by element, from the roundings the kernels make.  With A = sum_j p_j |v_j| (p the
 softmax weights):
 
-* out: exp(s - max) is rounded to bf16 before the second product (half an ulp: 2^-9 relative each, so
-  at most 2^-9 A in the sum), the result is rounded to bf16 (2^-9 |o|), and fp32 scores, exponentials
-  and sums add less than 2^-12 A (a score's error is at most D 2^-24 S, S below; with S <= 30 that is
-  2^-12).  |error| <= 2^-9 |o| + (2^-9 + 2^-12) A, all times 1 + 2^-8 for the products of roundings.
+* out: exp(s - max) is rounded to bf16 before the second product, the result once more.  bf16 holds 8
+  significant bits: the spacing above 1 is 2^-7, so rounding to nearest is off by at most 2^-8 relative
+  (1 + 2^-8 lies in the middle).  That makes 2^-8 A in the sum and 2^-8 |o| at the end; fp32 scores,
+  exponentials and sums add less than 2^-12 A (a score's error is at most D 2^-24 S, S below; with
+  S <= 30 that is 2^-12).  |error| <= 2^-8 |o| + (2^-8 + 2^-12) A, all times 1 + 2^-8 for the products
+  of roundings.
 * lse: the score's error, D 2^-24 S with S = scale max_j sum_d |q_d k_jd| and D <= 128, plus the
   exponential's, logarithm's and sum's, 2^-20 (1 + |lse|).
 """
@@ -36,7 +38,7 @@ def reference(q, k, v, scale, first=0):
     Aabs = torch.einsum("ahl,lhd->ahd", p, vv.abs())
     fin = torch.where(torch.isfinite(lse), lse, torch.zeros((), dtype=torch.float64))
     extra = torch.clamp(S / 30.0, min=1.0)[..., None]   # larger scores, larger errors in the exponent
-    tol_o = (2.0 ** -9 * out.abs() + (2.0 ** -9 + 2.0 ** -12 * extra) * Aabs) * (1 + 2.0 ** -8)
+    tol_o = (2.0 ** -8 * out.abs() + (2.0 ** -8 + 2.0 ** -12 * extra) * Aabs) * (1 + 2.0 ** -8)
     tol_l = 2.0 ** -17 * S + 2.0 ** -20 * (1 + fin.abs())
     return out, lse, tol_o, tol_l
 
