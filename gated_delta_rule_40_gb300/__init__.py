@@ -12,6 +12,7 @@ from .kda import (  # noqa: F401
     PagePlan,
     kda_attn_fwd,
     kda_attn_paged,
+    kda_attn_workspace_size,
     kda_bwd,
     kda_decode_step,
     kda_decode_tokens,

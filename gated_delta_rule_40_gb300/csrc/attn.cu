@@ -1,93 +1,720 @@
 // Causal softmax attention with grouped heads, over whole prompts (kda_attn_fwd) and over a paged
 // cache (kda_attn_paged): s = scale q.k, o = sum exp(s - lse) v over the keys up to the query's own.
-#include "kda_common.cuh"
+//
+// Work.  A tile of queries is 128 rows: 128 / G tokens (rounded down) times the G query heads that
+// share one key/value head, so that a key is read once for all of them and one decoded token with G
+// heads needs one pass over its cache.  A unit is one or two such tiles of one (request, key/value
+// head); it spans the tiles of 128 keys from the request's first to the last that its last token sees.
+// The key tiles of all units, in order, form one line that is cut into equal shares, one a CTA: a
+// share may begin or end inside a unit, whose pieces attn_join_kernel then joins from (maximum, sum,
+// unnormalised output).  So a long cache with few rows, ragged lengths and the triangle of a causal
+// prompt all divide evenly, without a schedule in memory: each CTA sums the requests' tiles itself.
+//
+// One CTA, 10 warps (an online softmax over key tiles, both products on the tensor cores):
+//   loader  TMA: the query tiles (two slots) and key / value tiles (a ring) into 128-byte-swizzled
+//           shared memory; with pages, one box a page
+//   issuer  S_i = Q_i K^T (M = 128, N = 128) into tensor memory, then O_i += P_i V (P_i from tensor
+//           memory, V MN-major); the two query tiles alternate, so that one's products run under the
+//           other's softmax
+//   2 x 4 softmax warps, a thread a row: s from tensor memory, row maximum, p = 2^(s c - m c) with
+//           c = scale log2(e), the sum of p in fp32, and p as bf16 back over s.  Tensor-core operands
+//           are bf16, so p is rounded to it: 2^-9 relative, like the output's own rounding.
+//           The reference maximum m moves only when the row's has grown by more than 2^8 (p then
+//           stays below 2^8, which costs no precision in floating point), so O is seldom rescaled.
+// Keys past a row's own position are masked in s.  Value rows past the unit's last key may hold
+// anything (another prompt, an unused part of a block), and 0 x NaN is NaN, so the issuer overwrites them
+// with zeros in shared memory.
+// Every wait is bounded; a timeout records KDA_ERR_DEVICE_TIMEOUT and all roles stop.
 #include "attn.h"
+#include "kda_common.cuh"
+#include "kda_tma.cuh"
 
 namespace kda {
 
-// One warp a (token, query head).  Lane l holds channels l, l + 32, ... of q and of the output; the
-// running maximum and sum of the softmax are rescaled when the maximum grows.
-template <int D, bool PAGED>
-__global__ __launch_bounds__(256) void attn_row_kernel(const AttnArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    // every warp checks the lengths, so that a malformed call writes nothing
-    const int nseq = a.cu ? a.N : a.B;
-    bool ok = true;
-    if (a.cu) {
-        for (int n = lane; n < a.N; n += 32) {
-            ok &= a.cu[n + 1] >= a.cu[n];
-            if (PAGED) ok &= a.lens[n] >= 0 && a.lens[n] <= ((long long)a.max_blocks << a.block_log2);
-        }
-        ok &= a.cu[0] == 0 && (PAGED ? a.cu[a.N] <= a.T : a.cu[a.N] == a.T);
+constexpr int AT_KEYS = 128;                 // keys a tile
+constexpr int AT_ROWS = 128;                 // rows a query tile
+constexpr long long AT_MAX_KEYS = 0x7fffff00;   // key positions, rounded up to a tile, stay below 2^31
+constexpr int AT_THREADS = 320;              // 8 softmax warps, loader, issuer
+constexpr int AT_LOADER = 8, AT_ISSUER = 9;  // warps
+constexpr float AT_SLACK = 8.0f;             // log2 of how far the row maximum may outgrow its reference
+
+template <int D>
+struct AttnLayout {
+    static constexpr uint32_t TILE = AT_KEYS * D * 2;          // bytes of a query, key or value tile
+    static constexpr int STAGES = D == 128 ? 5 : 8;            // key / value ring
+    static constexpr uint32_t HALF = AT_KEYS * 128;            // bytes of 64 channels of a tile
+    static constexpr uint32_t Q = STAGES * TILE, BAR = Q + 2 * TILE;
+    enum { QF = 0, QE = 2, SF = 4, PF = 6, PV = 8, OE = 10, KF = 12, KE = 12 + STAGES, COUNT = 12 + 2 * STAGES };
+    static constexpr uint32_t SLOT = BAR + 8 * COUNT, FLAG = SLOT + 4, BYTES = BAR + 512 + 1024;
+    static_assert(8 * COUNT + 8 <= 512 && BYTES <= 232448, "attention shared memory");
+};
+
+// A unit cut by a share's end: its rows, and how many CTAs from this one on hold a piece of it.
+struct JoinDesc {
+    int row0, tokens[2], hk, pieces;
+};
+
+struct AttnParams {
+    AttnArgs a;
+    JoinDesc *join;
+    float2 *ml;       // [CTA][2][256] reference maximum (in log2 units) and sum of a piece's rows
+    float *o;         // [CTA][2][D / 4][256][4] unnormalised outputs
+    float c;          // scale log2(e), not negative
+    int neg;          // the scale's sign
+    int G, tile_tokens, tiles;   // query heads a key/value head, tokens a tile, tiles a unit
+    int min_share;
+};
+
+// Sum of floor((a i + b) / m) over 0 <= i < n, for b >= 0 (Euclid's descent on the lattice points under
+// a line).
+__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long sum = 0;
+    while (n > 0) {
+        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const long long y = a * n + b;
+        n = y / m;
+        b = y % m;
+        const long long t = a;
+        a = m;
+        m = t;
+        if (m == 0) break;
     }
-    if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) set_status(KDA_ERR_BAD_SEQLENS);
-        return;
-    }
-    const long long tokens = (long long)a.B * a.T;
-    if (row >= tokens * a.H_q) return;
-    const long long t = row / a.H_q;
-    const int h = (int)(row - t * a.H_q), hk = h / (a.H_q / a.H_kv);
-    int n = 0;
-    long long first, keys;   // first key row (prompts), number of keys seen
-    if (a.cu) {
-        while (n < nseq && a.cu[n + 1] <= t) ++n;
-        if (n >= nseq) return;
-        first = a.cu[n];
-        keys = t - first + 1;
-        if (PAGED) keys += a.lens[n] - (a.cu[n + 1] - a.cu[n]);
-    } else {
-        n = (int)(t / a.T);
-        first = (long long)n * a.T;
-        keys = t - first + 1;
-    }
-    constexpr int R = D / 32;
-    float q[R], o[R], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        q[i] = bf16_to_f(a.q[row * D + lane + 32 * i]) * (a.scale * LOG2E);
-        o[i] = 0.f;
-    }
-    for (long long j = 0; j < keys; ++j) {
-        long long at;
-        bool real = true;
-        if (PAGED) {
-            const int id = a.table[(size_t)n * a.max_blocks + (j >> a.block_log2)];
-            real = id >= 0 && id < a.num_blocks;
-            if (!real && lane == 0) set_status(KDA_ERR_BAD_PAGES);
-            at = ((((long long)id * a.H_kv + hk) << a.block_log2) + (j & ((1 << a.block_log2) - 1))) * D;
-        } else {
-            at = ((first + j) * a.H_kv + hk) * D;
-        }
-        float s = 0.f;
-        if (real) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) s += q[i] * bf16_to_f(a.k[at + lane + 32 * i]);
-        }
-        s = warp_sum(s);
-        const float m2 = fmaxf(m, s), c = ex2(m - m2), e = ex2(s - m2);
-        l = l * c + e;
-#pragma unroll
-        for (int i = 0; i < R; ++i) o[i] = o[i] * c + (real ? e * bf16_to_f(a.v[at + lane + 32 * i]) : 0.f);
-        m = m2;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) a.out[row * D + lane + 32 * i] = f_to_bf16(o[i] * inv);
-    if (a.lse && lane == 0) a.lse[row] = l > 0.f ? (m + lg2(l)) * (1.f / LOG2E) : -INFINITY;
+    return sum;
 }
 
-cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream) {
-    const long long rows = (long long)a.B * a.T * a.H_q;
-    const unsigned grid = (unsigned)((rows + 7) / 8);
-    if (a.lens)
-        a.D == 64 ? attn_row_kernel<64, true><<<grid, 256, 0, stream>>>(a)
-                  : attn_row_kernel<128, true><<<grid, 256, 0, stream>>>(a);
-    else
-        a.D == 64 ? attn_row_kernel<64, false><<<grid, 256, 0, stream>>>(a)
-                  : attn_row_kernel<128, false><<<grid, 256, 0, stream>>>(a);
+// One request: its rows, keys and units
+struct Request {
+    int row0, fresh, keys, units;
+    __host__ __device__ void load(const AttnParams &p, int n) {
+        if (p.a.cu) {
+            row0 = p.a.cu[n];
+            fresh = p.a.cu[n + 1] - row0;
+            keys = p.a.lens ? p.a.lens[n] : fresh;
+        } else {
+            row0 = n * p.a.T;
+            fresh = keys = p.a.T;
+        }
+        const int w = p.tile_tokens * p.tiles;
+        units = (fresh + w - 1) / w;
+    }
+    // key tiles of the tokens up to (not including) token `end` of the request; at least one, for the
+    // rows that see nothing
+    __host__ __device__ int tiles_to(int end) const {
+        const int seen = keys - fresh + min(end, fresh);
+        return seen > AT_KEYS ? (seen + AT_KEYS - 1) / AT_KEYS : 1;
+    }
+    // key tiles of the first u units (u <= units) of w tokens each
+    __host__ __device__ long long prefix(int u, int w) const {
+        long long sum = 0, first = keys - fresh;   // units count max(1, ceil((first + (j + 1) w) / 128))
+        int full = u;
+        if (u > 0 && u == units) {
+            --full;
+            sum = tiles_to(fresh);
+        }
+        int j0 = 0;   // units that see nothing at all or no more than one tile through a negative start
+        if (first < 0) {
+            j0 = (int)min((long long)full, (-first) / w);
+            sum += j0;
+            first += (long long)j0 * w;
+            if (j0 < full && first < 0) {   // the unit that reaches the first key: its end is below w <= 128
+                sum += max(1ll, (first + w + AT_KEYS - 1) / AT_KEYS);
+                ++j0;
+                first += w;
+            }
+        }
+        return sum + floor_sum(full - j0, AT_KEYS, w, first + w + AT_KEYS - 1);
+    }
+};
+
+// The pieces of units in this CTA's share, in order
+struct Walk {
+    Request r;
+    int n, hk, unit, tile;
+    long long left, pos;
+    // the current piece
+    int a, b, all, token0, tokens[2], end[2];
+    __host__ __device__ void start(const AttnParams &p, int n_, int hk_, int unit_, int tile_, long long pos_, long long left_) {
+        n = n_; hk = hk_; unit = unit_; tile = tile_; pos = pos_; left = left_;
+        if (left > 0) r.load(p, n);
+    }
+    __host__ __device__ bool next(const AttnParams &p) {
+        if (left <= 0) return false;
+        if (unit >= r.units) {
+            unit = 0;
+            if (++hk == p.a.H_kv) {
+                hk = 0;
+                do r.load(p, ++n);
+                while (r.units == 0);
+            }
+        }
+        const int w = p.tile_tokens;
+        token0 = unit * w * p.tiles;
+        all = r.tiles_to(token0 + w * p.tiles);
+        a = tile;
+        b = (int)min((long long)all, tile + left);
+        pos += b - a;
+        left -= b - a;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            tokens[i] = i < p.tiles ? max(0, min(w, r.fresh - token0 - i * w)) : 0;
+            end[i] = tokens[i] ? min(b, r.tiles_to(token0 + i * w + tokens[i])) : 0;
+        }
+        tile = b;
+        if (b == all) {
+            tile = 0;
+            ++unit;
+        }
+        return true;
+    }
+    __host__ __device__ bool active(int i) const { return end[i] > a; }
+    // keys that the unit's last token sees
+    __host__ __device__ int keys(const AttnParams &p) const {
+        return max(0, r.keys - r.fresh + min(token0 + p.tile_tokens * p.tiles, r.fresh));
+    }
+};
+
+__device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+template <int D, bool PAGED>
+__global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_constant__ CUtensorMap tq,
+                                                             const __grid_constant__ CUtensorMap tk,
+                                                             const __grid_constant__ CUtensorMap tv,
+                                                             const __grid_constant__ AttnParams p) {
+    using L = AttnLayout<D>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = aligned_smem<1024>(smem_raw);
+    __shared__ long long s_warp[AT_THREADS / 32], s_base;
+    __shared__ int s_n, s_bad;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = smem_u32(sm), bar = sbase + L::BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::FLAG);
+    const int nseq = p.a.cu ? p.a.N : p.a.B;
+
+    // ---- this CTA's share: the tiles of all requests, then the request that holds the share's start
+    if (tid == 0) {
+        s_bad = 0;
+        p.join[blockIdx.x].pieces = 0;
+        if (p.a.cu && (p.a.cu[0] != 0 || (PAGED ? p.a.cu[p.a.N] > p.a.T : p.a.cu[p.a.N] != p.a.T))) s_bad = 1;
+    }
+    __syncthreads();
+    long long total = 0, mine = 0, before = 0;
+    auto group = [&](int n0) {   // tiles of requests n0 + tid: this thread's, the ones before it, all
+        const int n = n0 + tid;
+        mine = 0;
+        if (n < nseq) {
+            Request r;
+            r.load(p, n);
+            bool bad = p.a.cu && p.a.cu[n + 1] < p.a.cu[n];
+            if (PAGED) bad |= r.keys < 0 || r.keys > min((long long)p.a.max_blocks << p.a.block_log2, AT_MAX_KEYS);
+            if (bad) s_bad = 1;
+            else mine = r.prefix(r.units, p.tile_tokens * p.tiles) * p.a.H_kv;
+        }
+        long long x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        long long sum = 0;
+        before = x - mine;
+        for (int w = 0; w < AT_THREADS / 32; ++w) {
+            if (w < warp) before += s_warp[w];
+            sum += s_warp[w];
+        }
+        __syncthreads();
+        return sum;
+    };
+    for (int n0 = 0; n0 < nseq; n0 += AT_THREADS) total += group(n0);
+    if (s_bad) {
+        if (tid == 0) set_status(KDA_ERR_BAD_SEQLENS);
+        return;
+    }
+    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
+    const long long start = share * blockIdx.x, left = min(share, total - start);
+    if (left <= 0) return;
+    long long base = 0;
+    for (int n0 = 0; n0 < nseq; n0 += AT_THREADS) {
+        const long long sum = nseq <= AT_THREADS ? total : group(n0);
+        if (start < base + sum) {
+            if (start >= base + before && start < base + before + mine) {
+                s_n = n0 + tid;
+                s_base = base + before;
+            }
+            break;
+        }
+        base += sum;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < L::COUNT; ++i)
+            mbar_init(bar + 8 * i, i >= L::PF && i < L::PF + 2 || i >= L::OE && i < L::OE + 2 ? 4 : 1);
+        mbar_fence_init();
+        *abort_flag = 0;
+    }
+    if (warp == AT_ISSUER) tmem_alloc(sbase + L::SLOT, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::SLOT);
+    const uint32_t tS = tmem, tO = tmem + 256;
+
+    Walk w;
+    {
+        Request r;
+        r.load(p, s_n);
+        const int wt = p.tile_tokens * p.tiles;
+        const long long per_head = r.prefix(r.units, wt);
+        long long x = start - s_base;
+        const int hk = (int)(x / per_head);
+        x -= hk * per_head;
+        int lo = 0, hi = r.units;   // the unit whose tiles hold x: prefix(lo) <= x < prefix(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (r.prefix(mid, wt) <= x) lo = mid;
+            else hi = mid;
+        }
+        w.start(p, s_n, hk, lo, (int)(x - r.prefix(lo, wt)), start, left);
+    }
+
+    bool ok = true;
+    auto wait = [&](int b, uint32_t parity) {
+        for (int i = 0; ok && !mbar_wait(bar + 8 * b, parity, 1u << 14); ++i)
+            if (*abort_flag || i >= 256) ok = false;
+        return ok = __all_sync(0xffffffffu, ok);
+    };
+
+    if (warp == AT_LOADER) {
+        // ------------------------------------------------------------ loader
+        uint32_t kv = 0, qu = 0;
+        constexpr int HALVES = D / 64;
+        // with pages: a tile is `boxes` boxes of `box` keys
+        const int box = PAGED ? min(AT_KEYS, 1 << p.a.block_log2) : AT_KEYS, boxes = AT_KEYS / box;
+        const int my_box = lane % boxes, my_half = lane / boxes;
+        while (ok && w.next(p)) {
+            const int keys = w.keys(p);
+            auto page = [&](int t) {
+                if (!PAGED) return 0;
+                const int key = t * AT_KEYS + my_box * box;
+                if (key >= keys || my_half >= HALVES || t >= w.b) return 0;
+                const int id = p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)];
+                if (id >= 0 && id < p.a.num_blocks) return id;
+                set_status(KDA_ERR_BAD_PAGES);
+                return p.a.num_blocks;   // past the tensor: zeros
+            };
+            int id = page(w.a);
+            for (int t = w.a; ok && t < w.b; ++t) {
+                const int next_id = page(t + 1);
+                const int n_box = PAGED ? max(0, min(boxes, (keys - t * AT_KEYS + box - 1) / box)) : 1;
+                for (int part = 0; part < 2; ++part, ++kv) {
+                    const uint32_t s = kv % L::STAGES, use = kv / L::STAGES;
+                    if (use > 0 && !wait(L::KE + s, (use - 1) & 1)) break;
+                    const uint32_t f = bar + 8 * (L::KF + s);
+                    if (lane == 0) mbar_expect_tx(f, (uint32_t)(n_box * box * 128 * HALVES));
+                    __syncwarp();
+                    const CUtensorMap *m = part ? &tv : &tk;
+                    const uint32_t dst = sbase + s * L::TILE;
+                    if (PAGED) {
+                        const int off = (t * AT_KEYS + my_box * box) & ((1 << p.a.block_log2) - 1);
+                        if (my_box < n_box && my_half < HALVES)
+                            tma_load_3d(dst + my_half * L::HALF + my_box * box * 128, m, my_half * 64, off,
+                                        id * p.a.H_kv + w.hk, f);
+                    } else if (lane < HALVES) {
+                        tma_load_3d(dst + lane * L::HALF, m, lane * 64, w.r.row0 + t * AT_KEYS, w.hk, f);
+                    }
+                    // the queries follow the first key tile, so that they wait for their slot under its load
+                    if (t == w.a && part == 0) {
+                        for (int i = 0; i < 2; ++i) {
+                            if (!w.active(i)) continue;
+                            const uint32_t slot = qu & 1, u = qu >> 1;
+                            ++qu;
+                            if (u > 0 && !wait(L::QE + slot, (u - 1) & 1)) break;
+                            if (lane == 0) {
+                                const uint32_t qf = bar + 8 * (L::QF + slot);
+                                mbar_expect_tx(qf, (uint32_t)(p.G * p.tile_tokens * 128 * HALVES));
+                                for (int h = 0; h < HALVES; ++h)
+                                    tma_load_3d(sbase + L::Q + slot * L::TILE + h * L::HALF, &tq, h * 64, w.hk * p.G,
+                                                w.r.row0 + w.token0 + i * p.tile_tokens, qf);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
+                id = next_id;
+            }
+        }
+    } else if (warp == AT_ISSUER) {
+        // ------------------------------------------------------------ issuer
+        const uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, D) | (1u << 16);
+        uint32_t kv = 0, qu = 0, np[2] = {0, 0}, no[2] = {0, 0};
+        while (ok && w.next(p)) {
+            uint32_t slot[2];
+            for (int i = 0; i < 2; ++i)
+                if (w.active(i)) {
+                    slot[i] = qu & 1;
+                    if (!wait(L::QF + slot[i], (qu >> 1) & 1)) break;
+                    ++qu;
+                }
+            const int keys = w.keys(p);
+            // S_i of tile t from ring entry x
+            auto scores = [&](int i, int t, uint32_t x) {
+                if (lane == 0) {
+                    const uint64_t dq = umma_desc(sbase + L::Q + slot[i] * L::TILE, 16, 1024);
+                    const uint64_t dk = umma_desc(sbase + (x % L::STAGES) * L::TILE, 16, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint64_t o = (uint64_t)(((ks >> 2) * L::HALF + (ks & 3) * 32) >> 4);
+                        umma_bf16(tS + 128 * i, dq + o, dk + o, id_s, ks > 0 ? 1u : 0u);
+                    }
+                    umma_commit(bar + 8 * (L::SF + i));
+                    if (t + 1 == w.end[i]) umma_commit(bar + 8 * (L::QE + slot[i]));
+                }
+            };
+            auto release = [&](uint32_t x) {
+                if (lane == 0) umma_commit(bar + 8 * (L::KE + x % L::STAGES));
+            };
+            if (!ok || !wait(L::KF + kv % L::STAGES, (kv / L::STAGES) & 1)) break;
+            tc_fence_after();
+            for (int i = 0; i < 2; ++i)
+                if (w.active(i)) scores(i, w.a, kv);
+            release(kv);
+            for (int t = w.a; ok && t < w.b; ++t) {
+                const uint32_t xv = kv + 1, xk = kv + 2;
+                if (!wait(L::KF + xv % L::STAGES, (xv / L::STAGES) & 1)) break;
+                const uint32_t vt = sbase + (xv % L::STAGES) * L::TILE;
+                const int valid = keys - t * AT_KEYS;
+                if (valid < AT_KEYS) {
+                    unsigned char *v = sm + (xv % L::STAGES) * L::TILE;
+                    for (int u = max(valid, 0) * 8 + lane; u < AT_KEYS * 8; u += 32)
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            *reinterpret_cast<uint4 *>(v + h * L::HALF + u * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                const int last = w.end[1] > t ? 1 : 0;   // the last query tile that uses this value tile
+                for (int i = 0; ok && i < 2; ++i) {
+                    if (t < w.end[i]) {
+                        if (t == w.a && no[i] > 0 && !wait(L::OE + i, (no[i] - 1) & 1)) break;
+                        if (!wait(L::PF + i, np[i] & 1)) break;
+                        ++np[i];
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint64_t dv = umma_desc(vt, L::HALF, 1024);
+#pragma unroll
+                            for (int ks = 0; ks < AT_KEYS / 16; ++ks)
+                                umma_bf16_ta(tO + D * i, tS + 128 * i + 8 * ks, dv + (uint64_t)(ks * (2048 >> 4)), id_o,
+                                             t > w.a || ks > 0 ? 1u : 0u);
+                            umma_commit(bar + 8 * (L::PV + i));
+                        }
+                    }
+                    if (i == last) release(xv);
+                    if (t + 1 < w.end[i]) {
+                        if (!wait(L::KF + xk % L::STAGES, (xk / L::STAGES) & 1)) break;
+                        tc_fence_after();
+                        scores(i, t + 1, xk);
+                    }
+                }
+                if (t + 1 < w.b) release(xk);
+                kv += 2;
+            }
+            for (int i = 0; i < 2; ++i)
+                if (w.active(i)) ++no[i];
+        }
+        if (lane == 0 && (!ok || *abort_flag)) {
+            *abort_flag = 1;
+            // let what is in flight land before the CTA releases tensor memory (bounded)
+            for (int i = 0; i < L::COUNT; ++i)
+                for (uint32_t pp = 0; pp < 2; ++pp) mbar_wait(bar + 8 * i, pp, 1u << 12);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax of query tile i
+        const int i = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tS + 128 * i + lane_off, o_at = tO + D * i + lane_off;
+        uint32_t ns = 0;   // tiles so far: phase of S and PV
+        const float c = p.c;
+        while (ok && w.next(p)) {
+            const bool closed = w.a == 0 && w.b == w.all;
+            if (tid == 0 && w.a == 0 && !closed) {
+                JoinDesc d;
+                d.row0 = w.r.row0 + w.token0;
+                d.tokens[0] = w.tokens[0];
+                d.tokens[1] = w.tokens[1];
+                d.hk = w.hk;
+                d.pieces = 1 + (int)((w.all - w.b + share - 1) / share);
+                p.join[blockIdx.x] = d;
+            }
+            const int tok = row / p.G, g = row - tok * p.G;
+            const bool real = tok < w.tokens[i];
+            const bool warp_real = __any_sync(0xffffffffu, real);
+            // keys this row sees; rows that stand for nothing see all, so that they need no mask
+            const int limit = real ? w.r.keys - w.r.fresh + w.token0 + i * p.tile_tokens + tok + 1 : 0x7fffffff;
+            float m = -INFINITY, l = 0.f;   // reference maximum of s, sum of p
+            for (int t = w.a; ok && t < w.end[i]; ++t, ++ns) {
+                if (!wait(L::SF + i, ns & 1)) break;
+                if (warp_real) {
+                    tc_fence_after();
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) tmem_ld32_nowait(s_at + 32 * b, x[b]);
+                    tmem_wait_ld();
+                    if (p.neg) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[b][j] ^= 0x80000000u;
+                    }
+                    const int seen = limit - t * AT_KEYS;   // columns of this tile that the row sees
+                    if (__any_sync(0xffffffffu, seen < AT_KEYS)) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (32 * b + j >= seen) x[b][j] = 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        mx[b] = fmaxf(__uint_as_float(x[b][0]), __uint_as_float(x[b][1]));
+#pragma unroll
+                        for (int j = 2; j < 32; j += 2)
+                            mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(x[b][j])), __uint_as_float(x[b][j + 1]));
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool grow = (top - m) * c > AT_SLACK;   // the first tile's m is -infinity
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? ex2((m - top) * c) : 1.f;
+                        if (grow) m = top;
+                        l *= f;
+                        if (t > w.a) {
+                            if (!wait(L::PV + i, (ns - 1) & 1)) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int b = 0; b < D / 16; ++b) {
+                                uint32_t y[16];
+                                tmem_ld16_nowait(o_at + 16 * b, y);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                                tmem_st16(o_at + 16 * b, y);
+                            }
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m * c;
+                    const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[b][j]), __uint_as_float(x[b][j + 1])), c2, b2);
+                            e.x = ex2(e.x);
+                            e.y = ex2(e.y);
+                            sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], e);
+                            pk[j >> 1] = pack_bf16x2(e.x, e.y);
+                        }
+                        tmem_st16(s_at + 16 * b, pk);
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + 8 * (L::PF + i));
+            }
+            if (!ok) break;
+            // ---- the piece's rows: final ones go out, others to the workspace
+            if (w.active(i)) {
+                if (!wait(L::PV + i, (ns - 1) & 1)) break;
+                tc_fence_after();
+            }
+            if (w.tokens[i] && warp_real) {
+                const long long out_row = ((long long)w.r.row0 + w.token0 + i * p.tile_tokens + tok) * p.a.H_q + w.hk * p.G + g;
+                const int piece = 2 * blockIdx.x + (w.a > 0 ? 0 : 1), prow = i * AT_ROWS + row;
+                const bool any = w.active(i);
+                const float inv = closed ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+                const float base = m == -INFINITY ? 0.f : m * c;
+#pragma unroll 1
+                for (int b = 0; b < D / 32; ++b) {
+                    uint32_t y[32];
+                    if (any) {
+                        tmem_ld32_nowait(o_at + 32 * b, y);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) y[j] = 0;
+                    }
+                    if (!real) continue;
+                    if (closed) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            o[j] = l != 0.f ? pack_bf16x2(__uint_as_float(y[2 * j]) * inv, __uint_as_float(y[2 * j + 1]) * inv) : 0u;
+                        uint16_t *dst = p.a.out + out_row * D + 32 * b;
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(o[8], o[9], o[10], o[11]);
+                        *reinterpret_cast<uint4 *>(dst + 24) = make_uint4(o[12], o[13], o[14], o[15]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4 *>(p.o + (((size_t)piece * (D / 4) + 8 * b + j) * 256 + prow) * 4) =
+                                make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                    }
+                }
+                if (real) {
+                    if (!closed) p.ml[(size_t)piece * 256 + prow] = make_float2(l != 0.f ? base : -INFINITY, l);
+                    else if (p.a.lse) p.a.lse[out_row] = l != 0.f ? (base + lg2(l)) * (1.f / LOG2E) : -INFINITY;
+                }
+            }
+            if (w.active(i)) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + 8 * (L::OE + i));
+            }
+        }
+    }
+    if (!ok) {
+        set_status(KDA_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == AT_ISSUER) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of a unit that several CTAs worked on: with M the largest reference maximum,
+// o = sum 2^(m - M) O / sum 2^(m - M) l.  Piece 0 is the opening CTA's second slot, the following ones the
+// first slots of the CTAs after it, always in that order.  A thread takes 8 channels of one row; the pieces are laid
+// out with rows innermost, so a warp's loads are whole lines.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p) {
+    const int cta = blockIdx.x;
+    const JoinDesc d = p.join[cta];
+    if (d.pieces == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int prow = blockIdx.y * 32 + lane, i = prow / AT_ROWS, row = prow % AT_ROWS;
+    const int tok = row / p.G, g = row - tok * p.G;
+    if (tok >= d.tokens[i]) return;
+    auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
+    float M = -INFINITY;
+    for (int k = 0; k < d.pieces; ++k) M = fmaxf(M, p.ml[slot(k) * 256 + prow].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    const long long out_row = ((long long)d.row0 + i * p.tile_tokens + tok) * p.a.H_q + d.hk * p.G + g;
+    for (int c8 = warp; c8 < D / 8; c8 += 8) {
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
+        for (int k = 0; k < d.pieces; ++k) {
+            const float2 ml = p.ml[slot(k) * 256 + prow];
+            const float f = ex2(ml.x - ref);
+            l += f * ml.y;
+            const float4 *src = reinterpret_cast<const float4 *>(p.o) + (slot(k) * (D / 4) + 2 * c8) * 256 + prow;
+            const float4 u = src[0], v = src[256];
+            o[0] += f * u.x; o[1] += f * u.y; o[2] += f * u.z; o[3] += f * u.w;
+            o[4] += f * v.x; o[5] += f * v.y; o[6] += f * v.z; o[7] += f * v.w;
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        *reinterpret_cast<uint4 *>(p.a.out + out_row * D + 8 * c8) =
+            make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                       pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+        if (c8 == 0 && p.a.lse) p.a.lse[out_row] = l != 0.f ? (ref + lg2(l)) * (1.f / LOG2E) : -INFINITY;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+namespace {
+constexpr int AT_MAX_CTAS = 160;
+
+int sm_count() {
+    static int count[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (!count[dev]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        count[dev] = n < AT_MAX_CTAS ? n : AT_MAX_CTAS;
+    }
+    return count[dev];
+}
+
+// A 3-D bf16 tensor (channel, y, z) with the given strides in elements; boxes of 64 channels, 128-byte swizzle
+cudaError_t map_3d(CUtensorMap *m, const void *base, int D, long long y, long long z, long long y_stride,
+                   long long z_stride, int box_y, int box_z) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    const cudaError_t e = tma_encoder(&enc);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)y, (cuuint64_t)z};
+    const cuuint64_t strides[2] = {(cuuint64_t)y_stride * 2, (cuuint64_t)z_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_y, (cuuint32_t)box_z};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+size_t align256_at(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int D, bool PAGED>
+cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
+    using L = AttnLayout<D>;
+    const AttnArgs &a = p.a;
+    const long long rows = (long long)a.B * a.T;
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = map_3d(&mq, a.q, D, a.H_q, rows, D, (long long)a.H_q * D, p.G, p.tile_tokens);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < 2; ++i) {
+        const void *base = i ? a.v : a.k;
+        CUtensorMap *m = i ? &mv : &mk;
+        if (PAGED) {
+            const int bs = 1 << a.block_log2;
+            e = map_3d(m, base, D, bs, (long long)a.num_blocks * a.H_kv, D, (long long)bs * D, bs < AT_KEYS ? bs : AT_KEYS, 1);
+        } else {
+            e = map_3d(m, base, D, rows, a.H_kv, (long long)a.H_kv * D, D, AT_KEYS, 1);
+        }
+        if (e != cudaSuccess) return e;
+    }
+    e = cudaFuncSetAttribute(attn_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
+    if (e != cudaSuccess) return e;
+    attn_kernel<D, PAGED><<<grid, AT_THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
+    attn_join_kernel<D><<<dim3(grid, 4 * p.tiles), 256, 0, stream>>>(p);
     return cudaGetLastError();
+}
+}  // namespace
+
+size_t attn_workspace_bytes(int D) {
+    return align256_at(sizeof(JoinDesc) * AT_MAX_CTAS) + align256_at(sizeof(float2) * 256 * 2 * AT_MAX_CTAS) +
+           sizeof(float) * 256 * D * 2 * AT_MAX_CTAS;
+}
+
+cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches) {
+    const int sms = sm_count();
+    if (sms == 0) return cudaErrorInvalidDevice;
+    AttnParams p;
+    p.a = a;
+    char *base = static_cast<char *>(ws);
+    p.join = reinterpret_cast<JoinDesc *>(base);
+    base += align256_at(sizeof(JoinDesc) * AT_MAX_CTAS);
+    p.ml = reinterpret_cast<float2 *>(base);
+    base += align256_at(sizeof(float2) * 256 * 2 * AT_MAX_CTAS);
+    p.o = reinterpret_cast<float *>(base);
+    p.neg = a.scale < 0.f;
+    // a scale of 0 keeps a vanishing factor instead: the masked scores' -infinity x 0 would be NaN
+    p.c = fmaxf(fabsf(a.scale) * LOG2E, 1e-36f);
+    p.G = a.H_q / a.H_kv;
+    p.tile_tokens = AT_ROWS / p.G;
+    p.tiles = 2;
+    p.min_share = 2;
+    *launches = 2;
+    if (a.lens) return a.D == 64 ? run<64, true>(p, sms, stream) : run<128, true>(p, sms, stream);
+    return a.D == 64 ? run<64, false>(p, sms, stream) : run<128, false>(p, sms, stream);
 }
 
 }  // namespace kda

@@ -1,6 +1,7 @@
 // Arguments of the softmax-attention kernels.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -11,12 +12,14 @@ struct AttnArgs {
     uint16_t *out;
     float *lse;                  // NULL: not written
     const int32_t *cu;           // NULL: B prompts of T tokens
-    const int32_t *table, *lens; // NULL: whole prompts
+    const int32_t *table, *lens; // lens NULL: whole prompts
     float scale;
     int N, B, T, H_q, H_kv, D;
     int num_blocks, block_log2, max_blocks;
 };
 
-cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream);
+// Device workspace of one attention call, for any lengths.
+size_t attn_workspace_bytes(int D);
+cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches);
 
 }  // namespace kda

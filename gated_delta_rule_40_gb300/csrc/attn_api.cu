@@ -12,6 +12,8 @@ cudaError_t launch_kv_write(const uint16_t *k, const uint16_t *v, const int32_t 
                             uint16_t *v_cache, int T, int H_kv, int D, int num_blocks, int block_log2,
                             cudaStream_t stream);
 void set_last_launches(int n);
+cudaError_t ws_alloc(void **p, size_t bytes, cudaStream_t stream);
+cudaError_t ws_free(void *p, cudaStream_t stream);
 void timing_begin(cudaStream_t s);
 void timing_mark(const char *name, cudaStream_t s);
 }  // namespace kda
@@ -52,6 +54,55 @@ int validate_attn(const kda::AttnArgs &a) {
         return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
+
+// Runs the kernels in the given workspace, or in one from the library's pool
+int attend(const kda::AttnArgs &a, bool own_ws, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    const size_t need = kda::attn_workspace_bytes(a.D);
+    if (own_ws) {
+        if (kda::ws_alloc(&ws, need, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    } else if (!ws || !aligned(ws, 256) || ws_bytes < need) {
+        return KDA_ERR_WORKSPACE;
+    }
+    int launches = 0;
+    kda::timing_begin(stream);
+    const cudaError_t e = kda::launch_attn(a, ws, stream, &launches);
+    int rc = finish(e, "attn_kernel", stream);
+    if (rc == KDA_OK) kda::set_last_launches(launches);
+    if (own_ws && kda::ws_free(ws, stream) != cudaSuccess && rc == KDA_OK) rc = KDA_ERR_CUDA;
+    return rc;
+}
+
+int prompt(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v, float scale, const int32_t *cu_seqlens, int N,
+           int B, int T, int H_q, int H_kv, int D, kda_bf16_t *out, float *lse, bool own_ws, void *ws, size_t ws_bytes,
+           cudaStream_t stream) {
+    kda::AttnArgs a = {};
+    a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.cu = cu_seqlens; a.scale = scale;
+    a.N = cu_seqlens ? N : 0; a.B = B; a.T = T; a.H_q = H_q; a.H_kv = H_kv; a.D = D;
+    const int rc = validate_attn(a);
+    if (rc != KDA_OK) return rc;
+    if (cu_seqlens && B != 1) return KDA_ERR_INVALID_ARG;
+    if ((long long)B * T == 0) return nothing_to_do();
+    return attend(a, own_ws, ws, ws_bytes, stream);
+}
+
+int paged(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_bf16_t *v_cache, float scale,
+          const int32_t *block_table, const int32_t *seq_lens, const int32_t *cu_seqlens, int N, int T, int H_q,
+          int H_kv, int D, int num_blocks, int block_size, int max_blocks, kda_bf16_t *out, float *lse, bool own_ws,
+          void *ws, size_t ws_bytes, cudaStream_t stream) {
+    kda::AttnArgs a = {};
+    a.q = q; a.k = k_cache; a.v = v_cache; a.out = out; a.lse = lse; a.cu = cu_seqlens; a.scale = scale;
+    a.table = block_table; a.lens = seq_lens;
+    a.N = N; a.B = 1; a.T = T; a.H_q = H_q; a.H_kv = H_kv; a.D = D;
+    a.num_blocks = num_blocks; a.block_log2 = block_log2(block_size); a.max_blocks = max_blocks;
+    if (a.block_log2 < 0) return KDA_ERR_UNSUPPORTED;
+    const int rc = validate_attn(a);
+    if (rc != KDA_OK) return rc;
+    if (!cache_ok(num_blocks, a.block_log2) || (long long)num_blocks * H_kv > 0x7ffffffeLL || max_blocks < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (T == 0 || N == 0) return nothing_to_do();
+    if ((!block_table && max_blocks > 0) || !seq_lens || !cu_seqlens || num_blocks == 0) return KDA_ERR_INVALID_ARG;
+    return attend(a, own_ws, ws, ws_bytes, stream);
+}
 }  // namespace
 
 extern "C" {
@@ -87,37 +138,34 @@ int kda_kv_write(const kda_bf16_t *k, const kda_bf16_t *v, const int32_t *slots,
                   "kv_write_kernel", stream);
 }
 
+size_t kda_attn_workspace_size(int D) { return D == 64 || D == 128 ? kda::attn_workspace_bytes(D) : 0; }
+
 int kda_attn_fwd(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v, float scale,
                  const int32_t *cu_seqlens, int N, int B, int T, int H_q, int H_kv, int D, kda_bf16_t *out, float *lse,
                  cudaStream_t stream) {
-    kda::AttnArgs a = {};
-    a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.cu = cu_seqlens; a.scale = scale;
-    a.N = cu_seqlens ? N : 0; a.B = B; a.T = T; a.H_q = H_q; a.H_kv = H_kv; a.D = D;
-    const int rc = validate_attn(a);
-    if (rc != KDA_OK) return rc;
-    if (cu_seqlens && B != 1) return KDA_ERR_INVALID_ARG;
-    if ((long long)B * T == 0) return nothing_to_do();
-    kda::timing_begin(stream);
-    return finish(kda::launch_attn(a, stream), "attn_kernel", stream);
+    return prompt(q, k, v, scale, cu_seqlens, N, B, T, H_q, H_kv, D, out, lse, true, nullptr, 0, stream);
+}
+
+int kda_attn_fwd_ws(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v, float scale,
+                    const int32_t *cu_seqlens, int N, int B, int T, int H_q, int H_kv, int D, kda_bf16_t *out,
+                    float *lse, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return prompt(q, k, v, scale, cu_seqlens, N, B, T, H_q, H_kv, D, out, lse, false, ws, ws_bytes, stream);
 }
 
 int kda_attn_paged(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_bf16_t *v_cache, float scale,
                    const int32_t *block_table, const int32_t *seq_lens, const int32_t *cu_seqlens, int N, int T,
                    int H_q, int H_kv, int D, int num_blocks, int block_size, int max_blocks, kda_bf16_t *out,
                    float *lse, cudaStream_t stream) {
-    kda::AttnArgs a = {};
-    a.q = q; a.k = k_cache; a.v = v_cache; a.out = out; a.lse = lse; a.cu = cu_seqlens; a.scale = scale;
-    a.table = block_table; a.lens = seq_lens;
-    a.N = N; a.B = 1; a.T = T; a.H_q = H_q; a.H_kv = H_kv; a.D = D;
-    a.num_blocks = num_blocks; a.block_log2 = block_log2(block_size); a.max_blocks = max_blocks;
-    if (a.block_log2 < 0) return KDA_ERR_UNSUPPORTED;
-    const int rc = validate_attn(a);
-    if (rc != KDA_OK) return rc;
-    if (!cache_ok(num_blocks, a.block_log2) || max_blocks < 0) return KDA_ERR_INVALID_ARG;
-    if (T == 0 || N == 0) return nothing_to_do();
-    if ((!block_table && max_blocks > 0) || !seq_lens || !cu_seqlens) return KDA_ERR_INVALID_ARG;
-    kda::timing_begin(stream);
-    return finish(kda::launch_attn(a, stream), "attn_kernel", stream);
+    return paged(q, k_cache, v_cache, scale, block_table, seq_lens, cu_seqlens, N, T, H_q, H_kv, D, num_blocks,
+                 block_size, max_blocks, out, lse, true, nullptr, 0, stream);
+}
+
+int kda_attn_paged_ws(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_bf16_t *v_cache, float scale,
+                      const int32_t *block_table, const int32_t *seq_lens, const int32_t *cu_seqlens, int N, int T,
+                      int H_q, int H_kv, int D, int num_blocks, int block_size, int max_blocks, kda_bf16_t *out,
+                      float *lse, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return paged(q, k_cache, v_cache, scale, block_table, seq_lens, cu_seqlens, N, T, H_q, H_kv, D, num_blocks,
+                 block_size, max_blocks, out, lse, false, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -87,10 +87,18 @@ def load() -> ctypes.CDLL:
     lib.kda_page_plan.restype = I
     lib.kda_kv_write.argtypes = [P] * 5 + [I] * 5 + [P]
     lib.kda_kv_write.restype = I
-    lib.kda_attn_fwd.argtypes = [P, P, P, F, P, I, I, I, I, I, I, P, P, P]
+    attn_args = [P, P, P, F, P, I, I, I, I, I, I, P, P]
+    lib.kda_attn_fwd.argtypes = attn_args + [P]
     lib.kda_attn_fwd.restype = I
-    lib.kda_attn_paged.argtypes = [P, P, P, F, P, P, P] + [I] * 8 + [P, P, P]
+    lib.kda_attn_fwd_ws.argtypes = attn_args + [P, Z, P]
+    lib.kda_attn_fwd_ws.restype = I
+    paged_args = [P, P, P, F, P, P, P] + [I] * 8 + [P, P]
+    lib.kda_attn_paged.argtypes = paged_args + [P]
     lib.kda_attn_paged.restype = I
+    lib.kda_attn_paged_ws.argtypes = paged_args + [P, Z, P]
+    lib.kda_attn_paged_ws.restype = I
+    lib.kda_attn_workspace_size.argtypes = [I]
+    lib.kda_attn_workspace_size.restype = Z
     lib.kda_status_string.argtypes = [I]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_get_status.argtypes = [P]
@@ -579,13 +587,36 @@ def kda_kv_write(k, v, slots, k_cache, v_cache, stream=None) -> None:
     _raise(rc, "kda_kv_write")
 
 
+def kda_attn_workspace_size(D: int = 128) -> int:
+    return int(load().kda_attn_workspace_size(D))
+
+
+def _attend(name: str, args, D: int, device, workspace, stream, fresh):
+    """Calls kda_attn_fwd / kda_attn_paged.  On the current stream the workspace comes from torch's caching
+    allocator; on a stream of the caller's, which that allocator knows nothing of, from the library's pool on
+    that stream, and the outputs made here (``fresh``) are kept until it has passed."""
+    lib = load()
+    if workspace is None and stream is None:
+        workspace = torch.empty(lib.kda_attn_workspace_size(D), dtype=torch.uint8, device=device)
+    elif workspace is not None:
+        _check(workspace, "workspace", torch.uint8)
+    if workspace is None:
+        rc = getattr(lib, name)(*args, _stream(stream))
+    else:
+        name += "_ws"
+        rc = getattr(lib, name)(*args, _ptr(workspace), workspace.numel(), _stream(stream))
+    _raise(rc, name)
+    if stream is not None:
+        for t in fresh:
+            t.record_stream(stream)
+
+
 def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, return_lse: bool = True,
-                 stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                 workspace=None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Causal softmax attention over whole prompts.  Shapes: q [B,T,H_q,D]; k, v
     [B,T,H_kv,D] (bf16, D 64 or 128, H_q a multiple of H_kv); cu_seqlens int32
-    [N+1] (device, B = 1) or None.  Returns (out [B,T,H_q,D], lse [B,T,H_q] fp32
-    or None)."""
-    lib = load()
+    [N+1] (device, B = 1) or None; workspace uint8 (kda_attn_workspace_size(D)
+    bytes) or None.  Returns (out [B,T,H_q,D], lse [B,T,H_q] fp32 or None)."""
     bf, f32 = torch.bfloat16, torch.float32
     B, T, H_q, D = q.shape
     H_kv = k.shape[2]
@@ -594,28 +625,31 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, ret
     _check(k, "k", bf, (B, T, H_kv, D))
     _check(v, "v", bf, (B, T, H_kv, D))
     _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
+    fresh = []
     if out is None:
         out = torch.empty((B, T, H_q, D), dtype=bf, device=q.device)
+        fresh.append(out)
     else:
         _check(out, "out", bf, (B, T, H_q, D))
     if lse is not None:
         _check(lse, "lse", f32, (B, T, H_q))
     elif return_lse:
         lse = torch.empty((B, T, H_q), dtype=f32, device=q.device)
-    rc = lib.kda_attn_fwd(_ptr(q), _ptr(k), _ptr(v), scale, _ptr(cu_seqlens), N, B, T, H_q, H_kv, D, _ptr(out),
-                          _ptr(lse), _stream(stream))
-    _raise(rc, "kda_attn_fwd")
+        fresh.append(lse)
+    _attend("kda_attn_fwd", (_ptr(q), _ptr(k), _ptr(v), scale, _ptr(cu_seqlens), N, B, T, H_q, H_kv, D, _ptr(out),
+                             _ptr(lse)), D, q.device, workspace, stream, fresh)
     return out, lse
 
 
 def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale: float, out=None, lse=None,
-                   return_lse: bool = True, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                   return_lse: bool = True, workspace=None,
+                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Causal softmax attention of new tokens (one or many per request) over the
     paged cache that already holds them.  Shapes: q [T,H_q,D] (bf16, packed by
     cu_seqlens [N+1]); k_cache, v_cache [num_blocks,H_kv,block_size,D] (bf16);
-    block_table [N,max_blocks], seq_lens [N] (int32; cached + new tokens).
-    Returns (out [T,H_q,D], lse [T,H_q] fp32 or None)."""
-    lib = load()
+    block_table [N,max_blocks], seq_lens [N] (int32; cached + new tokens);
+    workspace as ``kda_attn_fwd``.  Returns (out [T,H_q,D], lse [T,H_q] fp32 or
+    None)."""
     bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     T, H_q, D = q.shape
     nb, H_kv, bs, _ = k_cache.shape
@@ -626,16 +660,18 @@ def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale
     _check(block_table, "block_table", i32, (N, block_table.shape[-1]))
     _check(seq_lens, "seq_lens", i32, (N,))
     _check(cu_seqlens, "cu_seqlens", i32, (N + 1,))
+    fresh = []
     if out is None:
         out = torch.empty((T, H_q, D), dtype=bf, device=q.device)
+        fresh.append(out)
     else:
         _check(out, "out", bf, (T, H_q, D))
     if lse is not None:
         _check(lse, "lse", f32, (T, H_q))
     elif return_lse:
         lse = torch.empty((T, H_q), dtype=f32, device=q.device)
-    rc = lib.kda_attn_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), scale, _ptr(block_table), _ptr(seq_lens),
-                            _ptr(cu_seqlens), N, T, H_q, H_kv, D, nb, bs, block_table.shape[1], _ptr(out), _ptr(lse),
-                            _stream(stream))
-    _raise(rc, "kda_attn_paged")
+        fresh.append(lse)
+    _attend("kda_attn_paged", (_ptr(q), _ptr(k_cache), _ptr(v_cache), scale, _ptr(block_table), _ptr(seq_lens),
+                               _ptr(cu_seqlens), N, T, H_q, H_kv, D, nb, bs, block_table.shape[1], _ptr(out),
+                               _ptr(lse)), D, q.device, workspace, stream, fresh)
     return out, lse

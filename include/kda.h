@@ -423,6 +423,19 @@ int kda_attn_paged(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_bf1
                    const int32_t *cu_seqlens, int N, int T, int H_q, int H_kv, int D, int num_blocks,
                    int block_size, int max_blocks, kda_bf16_t *out, float *lse, cudaStream_t stream);
 
+/* kda_attn_fwd and kda_attn_paged with a caller-owned workspace of at least
+ * kda_attn_workspace_size(D) bytes (whatever the lengths; 0 for an unsupported D), on the
+ * terms of kda_fwd_ws.  The calls without it take one from the library's pool. */
+size_t kda_attn_workspace_size(int D);
+int kda_attn_fwd_ws(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v, float scale,
+                    const int32_t *cu_seqlens, int N, int B, int T, int H_q, int H_kv, int D,
+                    kda_bf16_t *out, float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+int kda_attn_paged_ws(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_bf16_t *v_cache,
+                      float scale, const int32_t *block_table, const int32_t *seq_lens,
+                      const int32_t *cu_seqlens, int N, int T, int H_q, int H_kv, int D,
+                      int num_blocks, int block_size, int max_blocks, kda_bf16_t *out, float *lse,
+                      void *ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Self-test of the device-side failure path: queues one tiny kernel whose bounded
  * wait on a barrier that nothing completes gives up, recording
  * KDA_ERR_DEVICE_TIMEOUT in the status word (read it with kda_get_status); the
