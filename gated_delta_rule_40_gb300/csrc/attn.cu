@@ -10,19 +10,22 @@
 // unnormalised output).  So a long cache with few rows, ragged lengths and the triangle of a causal
 // prompt all divide evenly, without a schedule in memory: each CTA sums the requests' tiles itself.
 //
-// One CTA, 10 warps (an online softmax over key tiles, both products on the tensor cores):
-//   loader  TMA: the query tiles (two slots) and key / value tiles (a ring) into 128-byte-swizzled
-//           shared memory; with pages, one box a page
-//   issuer  S_i = Q_i K^T (M = 128, N = 128) into tensor memory, then O_i += P_i V (P_i from tensor
-//           memory, V MN-major); the two query tiles alternate, so that one's products run under the
-//           other's softmax
-//   2 x 4 softmax warps, a thread a row: s from tensor memory, row maximum, p = 2^(s c - m c) with
-//           c = scale log2(e), the sum of p in fp32, and p as bf16 back over s.  Tensor-core operands
-//           are bf16, so p is rounded to it: 2^-9 relative, like the output's own rounding.
-//           The reference maximum m moves only when the row's has grown by more than 2^8 (p then
-//           stays below 2^8, which costs no precision in floating point), so O is seldom rescaled.
+// One CTA, 11 warps (an online softmax over steps of 64 keys, both products on the tensor cores):
+//   loader    TMA: the query tiles (two slots) and key / value tiles of 128 keys (a ring) into
+//             128-byte-swizzled shared memory; with pages, one box a page
+//   2 engines, each an issuer warp and four softmax warps on one query tile at a time (the two tiles of a
+//             unit, or units of one tile in turn):
+//     issuer  S = Q K^T (M = 128, N = 64) into one of two tensor-memory buffers, then O += P V (P from
+//             tensor memory, V MN-major).  The scores of a step are ready two steps ahead, so that neither
+//             the tensor cores nor the softmax wait for the other's latency; a step of 128 keys would leave
+//             tensor memory for one buffer only (2 x 128 columns of S beside 2 x 128 of O).
+//     softmax a thread a row: s from tensor memory, row maximum, p = 2^(s c - m c) with c = scale log2(e),
+//             the sum of p in fp32, and p as bf16 back over s.  Tensor-core operands are bf16, so p is
+//             rounded to it: 2^-8 relative, like the output's own rounding.  The reference maximum m moves
+//             only when the row's has grown by more than 2^8 (p then stays below 2^8, which costs no
+//             precision in floating point), so O is seldom rescaled.
 // Keys past a row's own position are masked in s.  Value rows past the unit's last key may hold
-// anything (another prompt, an unused part of a block), and 0 x NaN is NaN, so the issuer overwrites them
+// anything (another prompt, an unused part of a block), and 0 x NaN is NaN, so the issuers overwrite them
 // with zeros in shared memory.
 // Every wait is bounded; a timeout records KDA_ERR_DEVICE_TIMEOUT and all roles stop.
 #include "attn.h"
@@ -34,8 +37,9 @@ namespace kda {
 constexpr int AT_KEYS = 128;                 // keys a tile
 constexpr int AT_ROWS = 128;                 // rows a query tile
 constexpr long long AT_MAX_KEYS = 0x7fffff00;   // key positions, rounded up to a tile, stay below 2^31
-constexpr int AT_THREADS = 320;              // 8 softmax warps, loader, issuer
-constexpr int AT_LOADER = 8, AT_ISSUER = 9;  // warps
+constexpr int AT_THREADS = 352;              // 8 softmax warps, 2 issuers, loader
+constexpr int AT_ISSUER = 8, AT_LOADER = 10; // warps
+constexpr int AT_STEP = 64;                  // keys a softmax step
 constexpr float AT_SLACK = 8.0f;             // log2 of how far the row maximum may outgrow its reference
 
 template <int D>
@@ -44,7 +48,11 @@ struct AttnLayout {
     static constexpr int STAGES = D == 128 ? 5 : 8;            // key / value ring
     static constexpr uint32_t HALF = AT_KEYS * 128;            // bytes of 64 channels of a tile
     static constexpr uint32_t Q = STAGES * TILE, BAR = Q + 2 * TILE;
-    enum { QF = 0, QE = 2, SF = 4, PF = 6, PV = 8, OE = 10, KF = 12, KE = 12 + STAGES, COUNT = 12 + 2 * STAGES };
+    // barriers: query tile loaded / free [slot]; scores ready, weights ready, output product done
+    // [engine][buffer]; output read [engine]; key / value tile loaded / free [stage].  A step's scores are
+    // ready only after the output product two steps before it, so that with one barrier a buffer no wait can
+    // take an earlier phase for its own.
+    enum { QF = 0, QE = 2, SF = 4, PF = 8, PV = 12, OE = 16, KF = 18, KE = 18 + STAGES, COUNT = 18 + 2 * STAGES };
     static constexpr uint32_t SLOT = BAR + 8 * COUNT, FLAG = SLOT + 4, BYTES = BAR + 512 + 1024;
     static_assert(8 * COUNT + 8 <= 512 && BYTES <= 232448, "attention shared memory");
 };
@@ -65,21 +73,25 @@ struct AttnParams {
     int min_share;
 };
 
-// Sum of floor((a i + b) / m) over 0 <= i < n, for b >= 0 (Euclid's descent on the lattice points under
-// a line).
-__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
-    long long sum = 0;
+// Sum of floor((a i + b) / m) over 0 <= i < n, a, m >= 1 (Euclid's descent on the lattice points under a
+// line).  a n + b stays below 2^31 here: n <= 2^24 units, as a call has at most 2^31 rows, and after its
+// reduction a < 128.
+__host__ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t a, long long b0) {
+    long long sum = (long long)n * (b0 / m);
+    uint32_t b = (uint32_t)(b0 % m);
     while (n > 0) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+        sum += (long long)n * (n - 1) / 2 * (a / m);
         a %= m;
-        b %= m;
-        const long long y = a * n + b;
+        const uint32_t y = a * n + b;
         n = y / m;
         b = y % m;
-        const long long t = a;
+        const uint32_t t = a;
         a = m;
         m = t;
-        if (m == 0) break;
+        if (n > 0) {
+            sum += (long long)n * (b / m);
+            b %= m;
+        }
     }
     return sum;
 }
@@ -124,7 +136,7 @@ struct Request {
                 first += w;
             }
         }
-        return sum + floor_sum(full - j0, AT_KEYS, w, first + w + AT_KEYS - 1);
+        return full > j0 ? sum + floor_sum(full - j0, AT_KEYS, w, first + w + AT_KEYS - 1) : sum;
     }
 };
 
@@ -132,11 +144,15 @@ struct Request {
 struct Walk {
     Request r;
     int n, hk, unit, tile;
-    long long left, pos;
+    long long left;
     // the current piece
-    int a, b, all, token0, tokens[2], end[2];
-    __host__ __device__ void start(const AttnParams &p, int n_, int hk_, int unit_, int tile_, long long pos_, long long left_) {
-        n = n_; hk = hk_; unit = unit_; tile = tile_; pos = pos_; left = left_;
+    int a, b, all, token0, tokens[2];
+    int end[2];      // steps of a query tile up to the piece's end
+    int engine;      // of the first query tile
+    __host__ __device__ void start(const AttnParams &p, int n_, int hk_, int unit_, int tile_, long long left_) {
+        engine = 1;
+        tokens[1] = 0;
+        n = n_; hk = hk_; unit = unit_; tile = tile_; left = left_;
         if (left > 0) r.load(p, n);
     }
     __host__ __device__ bool next(const AttnParams &p) {
@@ -154,13 +170,14 @@ struct Walk {
         all = r.tiles_to(token0 + w * p.tiles);
         a = tile;
         b = (int)min((long long)all, tile + left);
-        pos += b - a;
         left -= b - a;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             tokens[i] = i < p.tiles ? max(0, min(w, r.fresh - token0 - i * w)) : 0;
-            end[i] = tokens[i] ? min(b, r.tiles_to(token0 + i * w + tokens[i])) : 0;
+            const int seen = r.keys - r.fresh + token0 + i * w + tokens[i];
+            end[i] = tokens[i] ? min(2 * b, seen > AT_STEP ? (seen + AT_STEP - 1) / AT_STEP : 1) : 0;
         }
+        engine = tokens[1] ? 0 : engine ^ 1;
         tile = b;
         if (b == all) {
             tile = 0;
@@ -168,7 +185,9 @@ struct Walk {
         }
         return true;
     }
-    __host__ __device__ bool active(int i) const { return end[i] > a; }
+    __host__ __device__ bool active(int i) const { return end[i] > 2 * a; }
+    // the query tile that engine e works on, or -1
+    __host__ __device__ int tile_of(int e) const { return tokens[1] ? e : e == engine ? 0 : -1; }
     // keys that the unit's last token sees
     __host__ __device__ int keys(const AttnParams &p) const {
         return max(0, r.keys - r.fresh + min(token0 + p.tile_tokens * p.tiles, r.fresh));
@@ -189,8 +208,8 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     using L = AttnLayout<D>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = aligned_smem<1024>(smem_raw);
-    __shared__ long long s_warp[AT_THREADS / 32], s_base;
-    __shared__ int s_n, s_bad;
+    __shared__ long long s_warp[AT_THREADS / 32], s_x, s_head, s_at;
+    __shared__ int s_n, s_bad, s_unit;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(sm), bar = sbase + L::BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::FLAG);
@@ -246,7 +265,8 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         if (start < base + sum) {
             if (start >= base + before && start < base + before + mine) {
                 s_n = n0 + tid;
-                s_base = base + before;
+                s_x = start - (base + before);
+                s_head = mine / p.a.H_kv;
             }
             break;
         }
@@ -254,39 +274,53 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     }
     if (tid == 0) {
         for (int i = 0; i < L::COUNT; ++i)
-            mbar_init(bar + 8 * i, i >= L::PF && i < L::PF + 2 || i >= L::OE && i < L::OE + 2 ? 4 : 1);
+            mbar_init(bar + 8 * i, i >= L::KE ? 2 : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) ? 4 : 1);
         mbar_fence_init();
         *abort_flag = 0;
+        s_unit = 0;
     }
-    if (warp == AT_ISSUER) tmem_alloc(sbase + L::SLOT, 512);
+    if (warp == AT_LOADER) tmem_alloc(sbase + L::SLOT, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::SLOT);
     const uint32_t tS = tmem, tO = tmem + 256;
 
+    // the head and unit that hold tile s_x of request s_n: every thread tries one unit, the last that starts at
+    // or before the tile wins
     Walk w;
     {
         Request r;
         r.load(p, s_n);
         const int wt = p.tile_tokens * p.tiles;
-        const long long per_head = r.prefix(r.units, wt);
-        long long x = start - s_base;
-        const int hk = (int)(x / per_head);
-        x -= hk * per_head;
-        int lo = 0, hi = r.units;   // the unit whose tiles hold x: prefix(lo) <= x < prefix(hi)
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (r.prefix(mid, wt) <= x) lo = mid;
-            else hi = mid;
+        const int hk = (int)(s_x / s_head);
+        long long x = s_x - hk * s_head;
+        int unit = 0;
+        if (r.units > 1) {
+            const int step = (r.units + AT_THREADS - 1) / AT_THREADS, u = min(tid * step, r.units - 1);
+            const long long at = r.prefix(u, wt);
+            if (at <= x) atomicMax(&s_unit, u);
+            __syncthreads();
+            unit = s_unit;
+            if (unit == u) s_at = at;
+            __syncthreads();
+            x -= s_at;
+            for (int n; x >= (n = r.tiles_to((unit + 1) * wt)); ++unit) x -= n;
         }
-        w.start(p, s_n, hk, lo, (int)(x - r.prefix(lo, wt)), start, left);
+        w.start(p, s_n, hk, unit, (int)x, left);
     }
 
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
         for (int i = 0; ok && !mbar_wait(bar + 8 * b, parity, 1u << 14); ++i)
             if (*abort_flag || i >= 256) ok = false;
+        return ok = __all_sync(0xffffffffu, ok);
+    };
+
+    // for hand-offs on the critical path
+    auto spin = [&](int b, uint32_t parity) {
+        for (int i = 0; ok && !mbar_spin(bar + 8 * b, parity, 1u << 14); ++i)
+            if (*abort_flag || i >= 4096) ok = false;
         return ok = __all_sync(0xffffffffu, ok);
     };
 
@@ -349,83 +383,89 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 id = next_id;
             }
         }
-    } else if (warp == AT_ISSUER) {
-        // ------------------------------------------------------------ issuer
-        const uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, D) | (1u << 16);
-        uint32_t kv = 0, qu = 0, np[2] = {0, 0}, no[2] = {0, 0};
+    } else if (warp >= AT_ISSUER) {
+        // ------------------------------------------------------------ issuer of engine e
+        const int e = warp - AT_ISSUER;
+        const uint32_t id_s = idesc_bf16(128, AT_STEP), id_o = idesc_bf16(128, D) | (1u << 16);
+        const uint32_t s_at = tS + 128 * e, o_at = tO + D * e;
+        uint32_t kv = 0, qu = 0, steps = 0, jobs = 0;   // ring entries, query tiles, this engine's steps and jobs so far
         while (ok && w.next(p)) {
-            uint32_t slot[2];
-            for (int i = 0; i < 2; ++i)
-                if (w.active(i)) {
-                    slot[i] = qu & 1;
-                    if (!wait(L::QF + slot[i], (qu >> 1) & 1)) break;
+            const int i = w.tile_of(e);
+            const bool mine = i >= 0 && w.active(i);
+            uint32_t slot = 0;
+            for (int k = 0; k < 2; ++k)
+                if (w.active(k)) {
+                    if (mine && k == i) {
+                        slot = qu & 1;
+                        wait(L::QF + slot, (qu >> 1) & 1);
+                    }
                     ++qu;
                 }
-            const int keys = w.keys(p);
-            // S_i of tile t from ring entry x
-            auto scores = [&](int i, int t, uint32_t x) {
-                if (lane == 0) {
-                    const uint64_t dq = umma_desc(sbase + L::Q + slot[i] * L::TILE, 16, 1024);
-                    const uint64_t dk = umma_desc(sbase + (x % L::STAGES) * L::TILE, 16, 1024);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint64_t o = (uint64_t)(((ks >> 2) * L::HALF + (ks & 3) * 32) >> 4);
-                        umma_bf16(tS + 128 * i, dq + o, dk + o, id_s, ks > 0 ? 1u : 0u);
-                    }
-                    umma_commit(bar + 8 * (L::SF + i));
-                    if (t + 1 == w.end[i]) umma_commit(bar + 8 * (L::QE + slot[i]));
-                }
-            };
+            if (!ok) break;
+            const int keys = w.keys(p), s0 = 2 * w.a, s1 = mine ? w.end[i] : s0;
+            const uint64_t dq = umma_desc(sbase + L::Q + slot * L::TILE, 16, 1024);
+            auto entry = [&](int s, int part) { return kv + 2 * (uint32_t)((s >> 1) - w.a) + part; };
+            auto loaded = [&](uint32_t x) { return spin(L::KF + x % L::STAGES, (x / L::STAGES) & 1); };
             auto release = [&](uint32_t x) {
                 if (lane == 0) umma_commit(bar + 8 * (L::KE + x % L::STAGES));
             };
-            if (!ok || !wait(L::KF + kv % L::STAGES, (kv / L::STAGES) & 1)) break;
-            tc_fence_after();
-            for (int i = 0; i < 2; ++i)
-                if (w.active(i)) scores(i, w.a, kv);
-            release(kv);
-            for (int t = w.a; ok && t < w.b; ++t) {
-                const uint32_t xv = kv + 1, xk = kv + 2;
-                if (!wait(L::KF + xv % L::STAGES, (xv / L::STAGES) & 1)) break;
-                const uint32_t vt = sbase + (xv % L::STAGES) * L::TILE;
-                const int valid = keys - t * AT_KEYS;
-                if (valid < AT_KEYS) {
-                    unsigned char *v = sm + (xv % L::STAGES) * L::TILE;
-                    for (int u = max(valid, 0) * 8 + lane; u < AT_KEYS * 8; u += 32)
+            // scores of step s
+            auto scores = [&](int s) {
+                const uint32_t x = entry(s, 0), buf = (steps + (s - s0)) & 1;
+                if ((s & 1) == 0 && !loaded(x)) return;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t dk = umma_desc(sbase + (x % L::STAGES) * L::TILE + (s & 1) * AT_STEP * 128, 16, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint64_t o = (uint64_t)(((ks >> 2) * L::HALF + (ks & 3) * 32) >> 4);
+                        umma_bf16(s_at + AT_STEP * buf, dq + o, dk + o, id_s, ks > 0 ? 1u : 0u);
+                    }
+                    umma_commit(bar + 8 * (L::SF + 2 * e + buf));
+                    if (s + 1 == s1) umma_commit(bar + 8 * (L::QE + slot));
+                }
+                if ((s & 1) || s + 1 == s1) release(x);
+            };
+            if (s0 < s1) scores(s0);
+            if (ok && s0 + 1 < s1) scores(s0 + 1);
+            for (int s = s0; ok && s < s1; ++s) {
+                const uint32_t x = entry(s, 1), n = steps + (s - s0), buf = n & 1;
+                if ((s & 1) == 0 && !loaded(x)) break;
+                const uint32_t stage = x % L::STAGES;
+                const int valid = keys - s * AT_STEP;
+                if (valid < AT_STEP) {
+                    unsigned char *v = sm + stage * L::TILE + (s & 1) * AT_STEP * 128;
+                    for (int u = max(valid, 0) * 8 + lane; u < AT_STEP * 8; u += 32)
 #pragma unroll
                         for (int h = 0; h < D / 64; ++h)
                             *reinterpret_cast<uint4 *>(v + h * L::HALF + u * 16) = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
                     __syncwarp();
                 }
-                const int last = w.end[1] > t ? 1 : 0;   // the last query tile that uses this value tile
-                for (int i = 0; ok && i < 2; ++i) {
-                    if (t < w.end[i]) {
-                        if (t == w.a && no[i] > 0 && !wait(L::OE + i, (no[i] - 1) & 1)) break;
-                        if (!wait(L::PF + i, np[i] & 1)) break;
-                        ++np[i];
-                        tc_fence_after();
-                        if (lane == 0) {
-                            const uint64_t dv = umma_desc(vt, L::HALF, 1024);
+                if (s == s0 && jobs > 0 && !wait(L::OE + e, (jobs - 1) & 1)) break;
+                if (!spin(L::PF + 2 * e + buf, (n >> 1) & 1)) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t dv = umma_desc(sbase + stage * L::TILE + (s & 1) * AT_STEP * 128, L::HALF, 1024);
 #pragma unroll
-                            for (int ks = 0; ks < AT_KEYS / 16; ++ks)
-                                umma_bf16_ta(tO + D * i, tS + 128 * i + 8 * ks, dv + (uint64_t)(ks * (2048 >> 4)), id_o,
-                                             t > w.a || ks > 0 ? 1u : 0u);
-                            umma_commit(bar + 8 * (L::PV + i));
-                        }
-                    }
-                    if (i == last) release(xv);
-                    if (t + 1 < w.end[i]) {
-                        if (!wait(L::KF + xk % L::STAGES, (xk / L::STAGES) & 1)) break;
-                        tc_fence_after();
-                        scores(i, t + 1, xk);
-                    }
+                    for (int ks = 0; ks < AT_STEP / 16; ++ks)
+                        umma_bf16_ta(o_at, s_at + AT_STEP * buf + 8 * ks, dv + (uint64_t)(ks * (2048 >> 4)), id_o,
+                                     s > s0 || ks > 0 ? 1u : 0u);
+                    umma_commit(bar + 8 * (L::PV + 2 * e + buf));
                 }
-                if (t + 1 < w.b) release(xk);
-                kv += 2;
+                if ((s & 1) || s + 1 == s1) release(x);
+                if (s + 2 < s1) scores(s + 2);
             }
-            for (int i = 0; i < 2; ++i)
-                if (w.active(i)) ++no[i];
+            // tiles of the piece that this engine has no part in
+            for (int t = (s1 + 1) >> 1; ok && t < w.b; ++t)
+                for (int part = 0; part < 2; ++part) {
+                    const uint32_t x = entry(2 * t, part);
+                    if (!wait(L::KF + x % L::STAGES, (x / L::STAGES) & 1)) break;
+                    if (lane == 0) mbar_arrive(bar + 8 * (L::KE + x % L::STAGES));
+                }
+            kv += 2 * (uint32_t)(w.b - w.a);
+            steps += (uint32_t)(s1 - s0);
+            jobs += mine ? 1 : 0;
         }
         if (lane == 0 && (!ok || *abort_flag)) {
             *abort_flag = 1;
@@ -434,11 +474,11 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 for (uint32_t pp = 0; pp < 2; ++pp) mbar_wait(bar + 8 * i, pp, 1u << 12);
         }
     } else {
-        // ------------------------------------------------------------ softmax of query tile i
-        const int i = warp >> 2, row = (warp & 3) * 32 + lane;
+        // ------------------------------------------------------------ softmax of engine e
+        const int e = warp >> 2, row = (warp & 3) * 32 + lane, tok = row / p.G, g = row - tok * p.G;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tS + 128 * i + lane_off, o_at = tO + D * i + lane_off;
-        uint32_t ns = 0;   // tiles so far: phase of S and PV
+        const uint32_t s_at = tS + 128 * e + lane_off, o_at = tO + D * e + lane_off;
+        uint32_t ns = 0;   // steps so far: phases of S, P and PV
         const float c = p.c;
         while (ok && w.next(p)) {
             const bool closed = w.a == 0 && w.b == w.all;
@@ -451,30 +491,32 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 d.pieces = 1 + (int)((w.all - w.b + share - 1) / share);
                 p.join[blockIdx.x] = d;
             }
-            const int tok = row / p.G, g = row - tok * p.G;
+            const int i = w.tile_of(e);
+            if (i < 0) continue;
             const bool real = tok < w.tokens[i];
             const bool warp_real = __any_sync(0xffffffffu, real);
             // keys this row sees; rows that stand for nothing see all, so that they need no mask
             const int limit = real ? w.r.keys - w.r.fresh + w.token0 + i * p.tile_tokens + tok + 1 : 0x7fffffff;
             float m = -INFINITY, l = 0.f;   // reference maximum of s, sum of p
-            for (int t = w.a; ok && t < w.end[i]; ++t, ++ns) {
-                if (!wait(L::SF + i, ns & 1)) break;
+            for (int s = 2 * w.a; ok && s < w.end[i]; ++s, ++ns) {
+                const uint32_t buf = ns & 1;
+                if (!spin(L::SF + 2 * e + buf, (ns >> 1) & 1)) break;
                 if (warp_real) {
                     tc_fence_after();
-                    uint32_t x[4][32];
+                    uint32_t x[2][32];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) tmem_ld32_nowait(s_at + 32 * b, x[b]);
+                    for (int b = 0; b < 2; ++b) tmem_ld32_nowait(s_at + AT_STEP * buf + 32 * b, x[b]);
                     tmem_wait_ld();
                     if (p.neg) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
+                        for (int b = 0; b < 2; ++b)
 #pragma unroll
                             for (int j = 0; j < 32; ++j) x[b][j] ^= 0x80000000u;
                     }
-                    const int seen = limit - t * AT_KEYS;   // columns of this tile that the row sees
-                    if (__any_sync(0xffffffffu, seen < AT_KEYS)) {
+                    const int seen = limit - s * AT_STEP;   // columns of this step that the row sees
+                    if (__any_sync(0xffffffffu, seen < AT_STEP)) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
+                        for (int b = 0; b < 2; ++b)
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 if (32 * b + j >= seen) x[b][j] = 0xff800000u;
@@ -482,19 +524,20 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     float mx[4];
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        mx[b] = fmaxf(__uint_as_float(x[b][0]), __uint_as_float(x[b][1]));
+                        mx[b] = fmaxf(__uint_as_float(x[b >> 1][16 * (b & 1)]), __uint_as_float(x[b >> 1][16 * (b & 1) + 1]));
 #pragma unroll
-                        for (int j = 2; j < 32; j += 2)
-                            mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(x[b][j])), __uint_as_float(x[b][j + 1]));
+                        for (int j = 2; j < 16; j += 2)
+                            mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(x[b >> 1][16 * (b & 1) + j])),
+                                          __uint_as_float(x[b >> 1][16 * (b & 1) + j + 1]));
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    const bool grow = (top - m) * c > AT_SLACK;   // the first tile's m is -infinity
+                    const bool grow = (top - m) * c > AT_SLACK;   // the first step's m is -infinity
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? ex2((m - top) * c) : 1.f;
                         if (grow) m = top;
                         l *= f;
-                        if (t > w.a) {
-                            if (!wait(L::PV + i, (ns - 1) & 1)) break;
+                        if (s > 2 * w.a) {
+                            if (!wait(L::PV + 2 * e + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) break;
                             tc_fence_after();
 #pragma unroll 1
                             for (int b = 0; b < D / 16; ++b) {
@@ -511,29 +554,29 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
+                    for (int b = 0; b < 2; ++b) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
-                            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[b][j]), __uint_as_float(x[b][j + 1])), c2, b2);
-                            e.x = ex2(e.x);
-                            e.y = ex2(e.y);
-                            sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], e);
-                            pk[j >> 1] = pack_bf16x2(e.x, e.y);
+                            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[b][j]), __uint_as_float(x[b][j + 1])), c2, b2);
+                            y.x = ex2(y.x);
+                            y.y = ex2(y.y);
+                            sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], y);
+                            pk[j >> 1] = pack_bf16x2(y.x, y.y);
                         }
-                        tmem_st16(s_at + 16 * b, pk);
+                        tmem_st16(s_at + AT_STEP * buf + 16 * b, pk);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar + 8 * (L::PF + i));
+                if (lane == 0) mbar_arrive(bar + 8 * (L::PF + 2 * e + buf));
             }
             if (!ok) break;
             // ---- the piece's rows: final ones go out, others to the workspace
             if (w.active(i)) {
-                if (!wait(L::PV + i, (ns - 1) & 1)) break;
+                if (!wait(L::PV + 2 * e + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) break;
                 tc_fence_after();
             }
             if (w.tokens[i] && warp_real) {
@@ -578,7 +621,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             if (w.active(i)) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar + 8 * (L::OE + i));
+                if (lane == 0) mbar_arrive(bar + 8 * (L::OE + e));
             }
         }
     }
@@ -588,7 +631,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == AT_ISSUER) tmem_dealloc(tmem, 512);
+    if (warp == AT_LOADER) tmem_dealloc(tmem, 512);
 }
 
 // Joins the pieces of a unit that several CTAs worked on: with M the largest reference maximum,
@@ -598,6 +641,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p) {
     const int cta = blockIdx.x;
+    grid_dep_wait();   // launched while the pieces are still being computed
     const JoinDesc d = p.join[cta];
     if (d.pieces == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -605,26 +649,43 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p) {
     const int tok = row / p.G, g = row - tok * p.G;
     if (tok >= d.tokens[i]) return;
     auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
-    float M = -INFINITY;
-    for (int k = 0; k < d.pieces; ++k) M = fmaxf(M, p.ml[slot(k) * 256 + prow].x);
-    const float ref = M == -INFINITY ? 0.f : M;
     const long long out_row = ((long long)d.row0 + i * p.tile_tokens + tok) * p.a.H_q + d.hk * p.G + g;
     for (int c8 = warp; c8 < D / 8; c8 += 8) {
-        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
-        for (int k = 0; k < d.pieces; ++k) {
-            const float2 ml = p.ml[slot(k) * 256 + prow];
-            const float f = ex2(ml.x - ref);
-            l += f * ml.y;
-            const float4 *src = reinterpret_cast<const float4 *>(p.o) + (slot(k) * (D / 4) + 2 * c8) * 256 + prow;
-            const float4 u = src[0], v = src[256];
-            o[0] += f * u.x; o[1] += f * u.y; o[2] += f * u.z; o[3] += f * u.w;
-            o[4] += f * v.x; o[5] += f * v.y; o[6] += f * v.z; o[7] += f * v.w;
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f, M = -INFINITY;
+        // four pieces at a time, so that their loads are in flight together
+        for (int k0 = 0; k0 < d.pieces; k0 += 4) {
+            float2 ml[4];
+            float4 u[4], v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                u[k] = v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k < d.pieces) {
+                    ml[k] = p.ml[slot(k0 + k) * 256 + prow];
+                    const float4 *src = reinterpret_cast<const float4 *>(p.o) + (slot(k0 + k) * (D / 4) + 2 * c8) * 256 + prow;
+                    u[k] = src[0];
+                    v[k] = src[256];
+                }
+            }
+            const float top = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+            const float ref = top == -INFINITY ? 0.f : top, f0 = ex2(M - ref);
+            l *= f0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] *= f0;
+            M = top;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = ex2(ml[k].x - ref);
+                l += f * ml[k].y;
+                o[0] += f * u[k].x; o[1] += f * u[k].y; o[2] += f * u[k].z; o[3] += f * u[k].w;
+                o[4] += f * v[k].x; o[5] += f * v[k].y; o[6] += f * v[k].z; o[7] += f * v[k].w;
+            }
         }
         const float inv = l != 0.f ? 1.f / l : 0.f;
         *reinterpret_cast<uint4 *>(p.a.out + out_row * D + 8 * c8) =
             make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
                        pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
-        if (c8 == 0 && p.a.lse) p.a.lse[out_row] = l != 0.f ? (ref + lg2(l)) * (1.f / LOG2E) : -INFINITY;
+        if (c8 == 0 && p.a.lse) p.a.lse[out_row] = l != 0.f ? (M + lg2(l)) * (1.f / LOG2E) : -INFINITY;
     }
 }
 
@@ -683,9 +744,21 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
     }
     e = cudaFuncSetAttribute(attn_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
     if (e != cudaSuccess) return e;
+    // the same split of an SM's memory for both kernels, so that it is not rearranged between them
+    e = cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
     attn_kernel<D, PAGED><<<grid, AT_THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
-    attn_join_kernel<D><<<dim3(grid, 4 * p.tiles), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 4 * p.tiles);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p);
 }
 }  // namespace
 
