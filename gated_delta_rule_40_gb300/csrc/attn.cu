@@ -194,6 +194,15 @@ struct Walk {
     }
 };
 
+// One lane of a converged warp.  The tensor-core instructions take their operands from uniform registers:
+// under this predicate, and with a warp index that is uniform to the compiler too, an issue costs about
+// 65 cycles; under lane == 0 every operand is moved there first, about 100 cycles.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(w[0]), "r"(w[1]),
                  "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -210,7 +219,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     unsigned char *sm = aligned_smem<1024>(smem_raw);
     __shared__ long long s_warp[AT_THREADS / 32], s_x, s_head, s_at;
     __shared__ int s_n, s_bad, s_unit;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t sbase = smem_u32(sm), bar = sbase + L::BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::FLAG);
     const int nseq = p.a.cu ? p.a.N : p.a.B;
@@ -407,14 +416,14 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             auto entry = [&](int s, int part) { return kv + 2 * (uint32_t)((s >> 1) - w.a) + part; };
             auto loaded = [&](uint32_t x) { return spin(L::KF + x % L::STAGES, (x / L::STAGES) & 1); };
             auto release = [&](uint32_t x) {
-                if (lane == 0) umma_commit(bar + 8 * (L::KE + x % L::STAGES));
+                if (elect_lane()) umma_commit(bar + 8 * (L::KE + x % L::STAGES));
             };
             // scores of step s
             auto scores = [&](int s) {
                 const uint32_t x = entry(s, 0), buf = (steps + (s - s0)) & 1;
                 if ((s & 1) == 0 && !loaded(x)) return;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_lane()) {
                     const uint64_t dk = umma_desc(sbase + (x % L::STAGES) * L::TILE + (s & 1) * AT_STEP * 128, 16, 1024);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
@@ -445,7 +454,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 if (s == s0 && jobs > 0 && !wait(L::OE + e, (jobs - 1) & 1)) break;
                 if (!spin(L::PF + 2 * e + buf, (n >> 1) & 1)) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_lane()) {
                     const uint64_t dv = umma_desc(sbase + stage * L::TILE + (s & 1) * AT_STEP * 128, L::HALF, 1024);
 #pragma unroll
                     for (int ks = 0; ks < AT_STEP / 16; ++ks)
@@ -461,7 +470,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 for (int part = 0; part < 2; ++part) {
                     const uint32_t x = entry(2 * t, part);
                     if (!wait(L::KF + x % L::STAGES, (x / L::STAGES) & 1)) break;
-                    if (lane == 0) mbar_arrive(bar + 8 * (L::KE + x % L::STAGES));
+                    if (elect_lane()) mbar_arrive(bar + 8 * (L::KE + x % L::STAGES));
                 }
             kv += 2 * (uint32_t)(w.b - w.a);
             steps += (uint32_t)(s1 - s0);
