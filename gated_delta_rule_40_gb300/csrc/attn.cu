@@ -10,10 +10,12 @@
 // unnormalised output).  So a long cache with few rows, ragged lengths and the triangle of a causal
 // prompt all divide evenly, without a schedule in memory: each CTA sums the requests' tiles itself.
 //
-// One CTA, 11 warps (an online softmax over steps of 64 keys, both products on the tensor cores):
+// One CTA, 12 warps (an online softmax over steps of 64 keys, both products on the tensor cores):
 //   loader    TMA: the query tiles (two slots) and key / value tiles of 128 keys (a ring) into
 //             128-byte-swizzled shared memory; with pages, one box a page
-//   2 engines, each an issuer warp and four softmax warps on one query tile at a time (the two tiles of a
+//   cleaner   zeros in the value rows past a unit's last key, which may hold anything (another prompt, an
+//             unused part of a block): p is 0 there, and 0 x NaN would be NaN
+//   2 engines, each an issuing thread and four softmax warps on one query tile at a time (the two tiles of a
 //             unit, or units of one tile in turn):
 //     issuer  S = Q K^T (M = 128, N = 64) into one of two tensor-memory buffers, then O += P V (P from
 //             tensor memory, V MN-major).  The scores of a step are ready two steps ahead, so that neither
@@ -24,9 +26,7 @@
 //             rounded to it: 2^-8 relative, like the output's own rounding.  The reference maximum m moves
 //             only when the row's has grown by more than 2^8 (p then stays below 2^8, which costs no
 //             precision in floating point), so O is seldom rescaled.
-// Keys past a row's own position are masked in s.  Value rows past the unit's last key may hold
-// anything (another prompt, an unused part of a block), and 0 x NaN is NaN, so the issuers overwrite them
-// with zeros in shared memory.
+// Keys past a row's own position are masked in s.
 // Every wait is bounded; a timeout records KDA_ERR_DEVICE_TIMEOUT and all roles stop.
 #include "attn.h"
 #include "kda_common.cuh"
@@ -37,8 +37,8 @@ namespace kda {
 constexpr int AT_KEYS = 128;                 // keys a tile
 constexpr int AT_ROWS = 128;                 // rows a query tile
 constexpr long long AT_MAX_KEYS = 0x7fffff00;   // key positions, rounded up to a tile, stay below 2^31
-constexpr int AT_THREADS = 352;              // 8 softmax warps, 2 issuers, loader
-constexpr int AT_ISSUER = 8, AT_LOADER = 10; // warps
+constexpr int AT_THREADS = 384;              // 8 softmax warps, 2 issuers, loader, cleaner
+constexpr int AT_ISSUER = 8, AT_LOADER = 10, AT_CLEANER = 11;   // warps
 constexpr int AT_STEP = 64;                  // keys a softmax step
 constexpr float AT_SLACK = 8.0f;             // log2 of how far the row maximum may outgrow its reference
 
@@ -49,10 +49,12 @@ struct AttnLayout {
     static constexpr uint32_t HALF = AT_KEYS * 128;            // bytes of 64 channels of a tile
     static constexpr uint32_t Q = STAGES * TILE, BAR = Q + 2 * TILE;
     // barriers: query tile loaded / free [slot]; scores ready, weights ready, output product done
-    // [engine][buffer]; output read [engine]; key / value tile loaded / free [stage].  A step's scores are
+    // [engine][buffer]; output read [engine]; key / value tile loaded / free, value tile to be cleaned loaded
+    // [stage].  A step's scores are
     // ready only after the output product two steps before it, so that with one barrier a buffer no wait can
     // take an earlier phase for its own.
-    enum { QF = 0, QE = 2, SF = 4, PF = 8, PV = 12, OE = 16, KF = 18, KE = 18 + STAGES, COUNT = 18 + 2 * STAGES };
+    enum { QF = 0, QE = 2, SF = 4, PF = 8, PV = 12, OE = 16, KF = 18, KE = 18 + STAGES, VL = 18 + 2 * STAGES,
+           COUNT = 18 + 3 * STAGES };
     static constexpr uint32_t SLOT = BAR + 8 * COUNT, FLAG = SLOT + 4, BYTES = BAR + 512 + 1024;
     static_assert(8 * COUNT + 8 <= 512 && BYTES <= 232448, "attention shared memory");
 };
@@ -188,6 +190,8 @@ struct Walk {
     __host__ __device__ bool active(int i) const { return end[i] > 2 * a; }
     // the query tile that engine e works on, or -1
     __host__ __device__ int tile_of(int e) const { return tokens[1] ? e : e == engine ? 0 : -1; }
+    // whether the value rows of tile t do not end with it
+    __host__ __device__ bool dirty(const AttnParams &p, int t) const { return keys(p) < (t + 1) * AT_KEYS; }
     // keys that the unit's last token sees
     __host__ __device__ int keys(const AttnParams &p) const {
         return max(0, r.keys - r.fresh + min(token0 + p.tile_tokens * p.tiles, r.fresh));
@@ -201,6 +205,14 @@ __device__ __forceinline__ bool elect_lane() {
     uint32_t p;
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
+}
+
+// One probe of a barrier's phase (the thread may sleep in it for a while)
+__device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done) : "r"(mbar), "r"(parity) : "memory");
+    return done != 0;
 }
 
 __device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w) {
@@ -283,7 +295,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     }
     if (tid == 0) {
         for (int i = 0; i < L::COUNT; ++i)
-            mbar_init(bar + 8 * i, i >= L::KE ? 2 : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) ? 4 : 1);
+            mbar_init(bar + 8 * i, i >= L::KE && i < L::VL ? 2 : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) ? 4 : 1);
         mbar_fence_init();
         *abort_flag = 0;
         s_unit = 0;
@@ -319,18 +331,25 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         w.start(p, s_n, hk, unit, (int)x, left);
     }
 
+    // Bounded waits, of one thread or of a whole warp (whose lanes give up together).  The first probe is on its
+    // own: for a phase that is complete already, which is the rule, it is all that runs.
     bool ok = true;
-    auto wait = [&](int b, uint32_t parity) {
-        for (int i = 0; ok && !mbar_wait(bar + 8 * b, parity, 1u << 14); ++i)
-            if (*abort_flag || i >= 256) ok = false;
-        return ok = __all_sync(0xffffffffu, ok);
+    constexpr uint32_t LIMIT = 1u << 20;
+    auto wait_one = [&](int b, uint32_t parity) {
+        if (mbar_try(bar + 8 * b, parity)) return true;
+        for (uint32_t i = 0; i < LIMIT; ++i) {
+            if (mbar_try(bar + 8 * b, parity)) return true;
+            if ((i & 63) == 63 && *abort_flag) break;
+        }
+        return ok = false;
     };
-
-    // for hand-offs on the critical path
-    auto spin = [&](int b, uint32_t parity) {
-        for (int i = 0; ok && !mbar_spin(bar + 8 * b, parity, 1u << 14); ++i)
-            if (*abort_flag || i >= 4096) ok = false;
-        return ok = __all_sync(0xffffffffu, ok);
+    auto wait = [&](int b, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try(bar + 8 * b, parity))) return true;
+        for (uint32_t i = 0; i < LIMIT; ++i) {
+            if (__all_sync(0xffffffffu, mbar_try(bar + 8 * b, parity))) return true;
+            if ((i & 63) == 63 && __any_sync(0xffffffffu, *abort_flag)) break;
+        }
+        return ok = false;
     };
 
     if (warp == AT_LOADER) {
@@ -358,7 +377,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 for (int part = 0; part < 2; ++part, ++kv) {
                     const uint32_t s = kv % L::STAGES, use = kv / L::STAGES;
                     if (use > 0 && !wait(L::KE + s, (use - 1) & 1)) break;
-                    const uint32_t f = bar + 8 * (L::KF + s);
+                    const uint32_t f = bar + 8 * ((part && w.dirty(p, t) ? L::VL : L::KF) + s);
                     if (lane == 0) mbar_expect_tx(f, (uint32_t)(n_box * box * 128 * HALVES));
                     __syncwarp();
                     const CUtensorMap *m = part ? &tv : &tk;
@@ -392,96 +411,114 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 id = next_id;
             }
         }
-    } else if (warp >= AT_ISSUER) {
-        // ------------------------------------------------------------ issuer of engine e
-        const int e = warp - AT_ISSUER;
-        const uint32_t id_s = idesc_bf16(128, AT_STEP), id_o = idesc_bf16(128, D) | (1u << 16);
-        const uint32_t s_at = tS + 128 * e, o_at = tO + D * e;
-        uint32_t kv = 0, qu = 0, steps = 0, jobs = 0;   // ring entries, query tiles, this engine's steps and jobs so far
+    } else if (warp == AT_CLEANER) {
+        // ------------------------------------------------------------ cleaner
+        uint32_t kv = 0, uses = 0;   // ring entries so far; per stage, the parity of its value tiles cleaned
         while (ok && w.next(p)) {
-            const int i = w.tile_of(e);
-            const bool mine = i >= 0 && w.active(i);
-            uint32_t slot = 0;
-            for (int k = 0; k < 2; ++k)
-                if (w.active(k)) {
-                    if (mine && k == i) {
-                        slot = qu & 1;
-                        wait(L::QF + slot, (qu >> 1) & 1);
-                    }
-                    ++qu;
-                }
-            if (!ok) break;
-            const int keys = w.keys(p), s0 = 2 * w.a, s1 = mine ? w.end[i] : s0;
-            const uint64_t dq = umma_desc(sbase + L::Q + slot * L::TILE, 16, 1024);
-            auto entry = [&](int s, int part) { return kv + 2 * (uint32_t)((s >> 1) - w.a) + part; };
-            auto loaded = [&](uint32_t x) { return spin(L::KF + x % L::STAGES, (x / L::STAGES) & 1); };
-            auto release = [&](uint32_t x) {
-                if (elect_lane()) umma_commit(bar + 8 * (L::KE + x % L::STAGES));
-            };
-            // scores of step s
-            auto scores = [&](int s) {
-                const uint32_t x = entry(s, 0), buf = (steps + (s - s0)) & 1;
-                if ((s & 1) == 0 && !loaded(x)) return;
-                tc_fence_after();
-                if (elect_lane()) {
-                    const uint64_t dk = umma_desc(sbase + (x % L::STAGES) * L::TILE + (s & 1) * AT_STEP * 128, 16, 1024);
+            const int t = w.b - 1;
+            kv += 2 * (uint32_t)(w.b - w.a);
+            if (!w.dirty(p, t)) continue;
+            const uint32_t stage = (kv - 1) % L::STAGES;
+            if (!wait(L::VL + stage, (uses >> stage) & 1)) break;
+            uses ^= 1u << stage;
+            unsigned char *v = sm + stage * L::TILE;
+            for (int u = max(w.keys(p) - t * AT_KEYS, 0) * 8 + lane; u < AT_KEYS * 8; u += 32)
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint64_t o = (uint64_t)(((ks >> 2) * L::HALF + (ks & 3) * 32) >> 4);
-                        umma_bf16(s_at + AT_STEP * buf, dq + o, dk + o, id_s, ks > 0 ? 1u : 0u);
+                for (int h = 0; h < D / 64; ++h)
+                    *reinterpret_cast<uint4 *>(v + h * L::HALF + u * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + 8 * (L::KF + stage));
+        }
+    } else if (warp >= AT_ISSUER) {
+        // ------------------------------------------------------------ issuing thread of engine e
+        const int e = warp - AT_ISSUER;
+        if (elect_lane()) {
+            constexpr uint32_t id_s = idesc_bf16(128, AT_STEP), id_o = idesc_bf16(128, D) | (1u << 16);
+            constexpr uint32_t HALF_STEP = AT_STEP * 128;   // bytes between a tile's two steps
+            const uint32_t s_at = tS + 128 * e, o_at = tO + D * e;
+            // ring positions of the next key and value tile
+            uint32_t ks = 0, kp = 0, vs = 1, vp = 0;
+            auto advance = [](uint32_t &stage, uint32_t &phase) {
+                stage += 2;
+                if (stage >= L::STAGES) {
+                    stage -= L::STAGES;
+                    phase ^= 1;
+                }
+            };
+            uint32_t qu = 0, steps = 0, jobs = 0;   // query tiles of both engines, this engine's steps and jobs so far
+            while (ok && w.next(p)) {
+                const int i = w.tile_of(e);
+                const bool mine = i >= 0 && w.active(i);
+                uint32_t slot = 0;
+                for (int k = 0; k < 2; ++k)
+                    if (w.active(k)) {
+                        if (mine && k == i) {
+                            slot = qu & 1;
+                            wait_one(L::QF + slot, (qu >> 1) & 1);
+                        }
+                        ++qu;
+                    }
+                const int s0 = 2 * w.a, s1 = mine ? w.end[i] : s0;
+                const uint64_t dq = umma_desc(sbase + L::Q + slot * L::TILE, 16, 1024);
+                // scores of step s
+                auto scores = [&](int s) {
+                    const uint32_t buf = (steps + (s - s0)) & 1;
+                    if ((s & 1) == 0 && !wait_one(L::KF + ks, kp)) return;
+                    tc_fence_after();
+                    const uint64_t dk = umma_desc(sbase + ks * L::TILE + (s & 1) * HALF_STEP, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t o = (uint64_t)(((k >> 2) * L::HALF + (k & 3) * 32) >> 4);
+                        umma_bf16(s_at + AT_STEP * buf, dq + o, dk + o, id_s, k > 0 ? 1u : 0u);
                     }
                     umma_commit(bar + 8 * (L::SF + 2 * e + buf));
                     if (s + 1 == s1) umma_commit(bar + 8 * (L::QE + slot));
-                }
-                if ((s & 1) || s + 1 == s1) release(x);
-            };
-            if (s0 < s1) scores(s0);
-            if (ok && s0 + 1 < s1) scores(s0 + 1);
-            for (int s = s0; ok && s < s1; ++s) {
-                const uint32_t x = entry(s, 1), n = steps + (s - s0), buf = n & 1;
-                if ((s & 1) == 0 && !loaded(x)) break;
-                const uint32_t stage = x % L::STAGES;
-                const int valid = keys - s * AT_STEP;
-                if (valid < AT_STEP) {
-                    unsigned char *v = sm + stage * L::TILE + (s & 1) * AT_STEP * 128;
-                    for (int u = max(valid, 0) * 8 + lane; u < AT_STEP * 8; u += 32)
+                    if ((s & 1) || s + 1 == s1) {
+                        umma_commit(bar + 8 * (L::KE + ks));
+                        advance(ks, kp);
+                    }
+                };
+                if (ok && s0 < s1) scores(s0);
+                if (ok && s0 + 1 < s1) scores(s0 + 1);
+                for (int s = s0; ok && s < s1; ++s) {
+                    const uint32_t n = steps + (s - s0), buf = n & 1;
+                    if ((s & 1) == 0 && !wait_one(L::KF + vs, vp)) break;
+                    if (s == s0 && jobs > 0 && !wait_one(L::OE + e, (jobs - 1) & 1)) break;
+                    if (!wait_one(L::PF + 2 * e + buf, (n >> 1) & 1)) break;
+                    tc_fence_after();
+                    const uint64_t dv = umma_desc(sbase + vs * L::TILE + (s & 1) * HALF_STEP, L::HALF, 1024);
 #pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            *reinterpret_cast<uint4 *>(v + h * L::HALF + u * 16) = make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                if (s == s0 && jobs > 0 && !wait(L::OE + e, (jobs - 1) & 1)) break;
-                if (!spin(L::PF + 2 * e + buf, (n >> 1) & 1)) break;
-                tc_fence_after();
-                if (elect_lane()) {
-                    const uint64_t dv = umma_desc(sbase + stage * L::TILE + (s & 1) * AT_STEP * 128, L::HALF, 1024);
-#pragma unroll
-                    for (int ks = 0; ks < AT_STEP / 16; ++ks)
-                        umma_bf16_ta(o_at, s_at + AT_STEP * buf + 8 * ks, dv + (uint64_t)(ks * (2048 >> 4)), id_o,
-                                     s > s0 || ks > 0 ? 1u : 0u);
+                    for (int k = 0; k < AT_STEP / 16; ++k)
+                        umma_bf16_ta(o_at, s_at + AT_STEP * buf + 8 * k, dv + (uint64_t)(k * (2048 >> 4)), id_o,
+                                     s > s0 || k > 0 ? 1u : 0u);
                     umma_commit(bar + 8 * (L::PV + 2 * e + buf));
+                    if ((s & 1) || s + 1 == s1) {
+                        umma_commit(bar + 8 * (L::KE + vs));
+                        advance(vs, vp);
+                    }
+                    if (s + 2 < s1) scores(s + 2);
                 }
-                if ((s & 1) || s + 1 == s1) release(x);
-                if (s + 2 < s1) scores(s + 2);
+                // tiles of the piece that this engine has no part in
+                for (int t = (s1 + 1) >> 1; ok && t < w.b; ++t) {
+                    if (!wait_one(L::KF + ks, kp)) break;
+                    mbar_arrive(bar + 8 * (L::KE + ks));
+                    advance(ks, kp);
+                    if (!wait_one(L::KF + vs, vp)) break;
+                    mbar_arrive(bar + 8 * (L::KE + vs));
+                    advance(vs, vp);
+                }
+                steps += (uint32_t)(s1 - s0);
+                jobs += mine ? 1 : 0;
             }
-            // tiles of the piece that this engine has no part in
-            for (int t = (s1 + 1) >> 1; ok && t < w.b; ++t)
-                for (int part = 0; part < 2; ++part) {
-                    const uint32_t x = entry(2 * t, part);
-                    if (!wait(L::KF + x % L::STAGES, (x / L::STAGES) & 1)) break;
-                    if (elect_lane()) mbar_arrive(bar + 8 * (L::KE + x % L::STAGES));
-                }
-            kv += 2 * (uint32_t)(w.b - w.a);
-            steps += (uint32_t)(s1 - s0);
-            jobs += mine ? 1 : 0;
+            if (!ok || *abort_flag) {
+                *abort_flag = 1;
+                // let what is in flight land before the CTA releases tensor memory (bounded)
+                for (int i = 0; i < L::COUNT; ++i)
+                    for (uint32_t pp = 0; pp < 2; ++pp) mbar_wait(bar + 8 * i, pp, 1u << 12);
+            }
         }
-        if (lane == 0 && (!ok || *abort_flag)) {
-            *abort_flag = 1;
-            // let what is in flight land before the CTA releases tensor memory (bounded)
-            for (int i = 0; i < L::COUNT; ++i)
-                for (uint32_t pp = 0; pp < 2; ++pp) mbar_wait(bar + 8 * i, pp, 1u << 12);
-        }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax of engine e
         const int e = warp >> 2, row = (warp & 3) * 32 + lane, tok = row / p.G, g = row - tok * p.G;
@@ -509,7 +546,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             float m = -INFINITY, l = 0.f;   // reference maximum of s, sum of p
             for (int s = 2 * w.a; ok && s < w.end[i]; ++s, ++ns) {
                 const uint32_t buf = ns & 1;
-                if (!spin(L::SF + 2 * e + buf, (ns >> 1) & 1)) break;
+                if (!wait(L::SF + 2 * e + buf, (ns >> 1) & 1)) break;
                 if (warp_real) {
                     tc_fence_after();
                     uint32_t x[2][32];
