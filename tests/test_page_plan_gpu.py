@@ -189,5 +189,6 @@ def test_write_past_32_bit_offsets():
     s = 0.1 * torch.einsum("hd,hld->hl", q[0].double(), kk)
     p = torch.softmax(s, -1)
     want = torch.einsum("hl,hld->hd", p, vv)
-    bound = 2.0 ** -9 * want.abs() + (2.0 ** -9 + 2.0 ** -12) * torch.einsum("hl,hld->hd", p, vv.abs())
+    # bf16 rounds to within 2^-8 (attn_testutil): the softmax weights once, the result once
+    bound = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * torch.einsum("hl,hld->hd", p, vv.abs())
     assert ((out[0].double() - want).abs() <= bound * (1 + 2.0 ** -8)).all()
