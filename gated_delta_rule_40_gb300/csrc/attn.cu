@@ -788,11 +788,17 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
         }
         if (e != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(attn_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
-    if (e != cudaSuccess) return e;
-    // the same split of an SM's memory for both kernels, so that it is not rearranged between them
-    e = cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    if (e != cudaSuccess) return e;
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    static bool ready[64] = {false};   // by device: the attributes are set once
+    if (!ready[dev & 63]) {
+        e = cudaFuncSetAttribute(attn_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
+        if (e != cudaSuccess) return e;
+        // the same split of an SM's memory for both kernels, so that it is not rearranged between them
+        e = cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e != cudaSuccess) return e;
+        ready[dev & 63] = true;
+    }
     attn_kernel<D, PAGED><<<grid, AT_THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

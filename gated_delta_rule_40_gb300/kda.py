@@ -140,6 +140,13 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(stream) -> int:
+    """``_stream`` as a plain number, which ctypes takes too; the current stream without a Stream object."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _stream(stream).value or 0
+
+
 def _check(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional=False, device: str = "cuda"):
     if t is None:
         if optional:
@@ -158,6 +165,16 @@ def _check(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional=Fal
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _arg(t, name: str, dtype, shape, device: int) -> int:
+    """Address of a required tensor after ``_check``'s checks, which for a tensor that passes are made here in
+    a quarter of the time: a call of one decoding step costs the host more than the GPU.  ``device`` is the
+    current one, or -2, which no tensor is on."""
+    if t is not None and t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, dtype, shape)
+    return t.data_ptr()
 
 
 def _raise(rc: int, where: str):
@@ -548,42 +565,43 @@ def kda_page_plan(cached_lens, new_lens, free_blocks, free_start, block_table, b
     blocks), free_start [1] (the first of them to take) and block_table
     [N,max_blocks] (new entries written in place), all int32.  ``num_tokens`` is
     the size of the slot map: the number of new tokens, or more."""
-    lib = load()
-    i32 = torch.int32
-    N = cached_lens.numel()
-    _check(cached_lens, "cached_lens", i32, (N,))
-    _check(new_lens, "new_lens", i32, (N,))
-    _check(free_blocks, "free_blocks", i32, (free_blocks.numel(),))
-    _check(free_start, "free_start", i32, (1,))
-    _check(block_table, "block_table", i32, (N, block_table.shape[-1]))
+    lib = _lib or load()
+    i32, dev = torch.int32, torch.cuda.current_device() if cached_lens.is_cuda else -2
+    N, F, width = cached_lens.shape[0], free_blocks.shape[0], block_table.shape[-1]
+    pc = _arg(cached_lens, "cached_lens", i32, (N,), dev)
+    pn = _arg(new_lens, "new_lens", i32, (N,), dev)
+    pf = _arg(free_blocks, "free_blocks", i32, (F,), dev)
+    ps = _arg(free_start, "free_start", i32, (1,), dev)
+    pt = _arg(block_table, "block_table", i32, (N, width), dev)
     if num_tokens < 0:
         raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
-    # one allocation; every part starts on 16 bytes
-    n4, t4 = (N + 4) & ~3, (num_tokens + 3) & ~3
-    buf = torch.empty(2 * n4 + 2 * t4 + 4, dtype=i32, device=cached_lens.device)
-    cu, lens, slots, pos, nxt = buf.split((n4, n4, t4, t4, 4))
-    plan = PagePlan(cu[:N + 1], lens[:N], slots[:num_tokens], pos[:num_tokens], nxt[:1])
-    rc = lib.kda_page_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks), _ptr(free_start), _ptr(block_table), N,
-                           num_tokens, block_table.shape[1], block_size, free_blocks.numel(), _ptr(cu), _ptr(lens),
-                           _ptr(slots), _ptr(pos), _ptr(nxt), _stream(stream))
+    # one allocation for the five outputs
+    buf = cached_lens.new_empty(2 * N + 2 * num_tokens + 2)
+    plan = PagePlan(*buf.split_with_sizes((N + 1, N, num_tokens, num_tokens, 1)))
+    at = buf.data_ptr()
+    lens = at + 4 * (N + 1)
+    slots = lens + 4 * N
+    pos = slots + 4 * num_tokens
+    rc = lib.kda_page_plan(pc, pn, pf, ps, pt, N, num_tokens, width, block_size, F, at, lens, slots, pos,
+                           pos + 4 * num_tokens, _raw_stream(stream))
     _raise(rc, "kda_page_plan")
+    if stream is not None:
+        buf.record_stream(stream)
     return plan
 
 
 def kda_kv_write(k, v, slots, k_cache, v_cache, stream=None) -> None:
     """Store k, v [T,H_kv,D] (bf16) in the caches [num_blocks,H_kv,block_size,D] at
     ``slots`` [T] (int32, kda_page_plan's); a negative slot is left out."""
-    lib = load()
-    bf = torch.bfloat16
+    lib = _lib or load()
+    bf, dev = torch.bfloat16, torch.cuda.current_device() if k.is_cuda else -2
     T, H_kv, D = k.shape
     nb, _, bs, _ = k_cache.shape
-    _check(k, "k", bf, (T, H_kv, D))
-    _check(v, "v", bf, (T, H_kv, D))
-    _check(slots, "slots", torch.int32, (T,))
-    _check(k_cache, "k_cache", bf, (nb, H_kv, bs, D))
-    _check(v_cache, "v_cache", bf, (nb, H_kv, bs, D))
-    rc = lib.kda_kv_write(_ptr(k), _ptr(v), _ptr(slots), _ptr(k_cache), _ptr(v_cache), T, H_kv, D, nb, bs,
-                          _stream(stream))
+    rc = lib.kda_kv_write(_arg(k, "k", bf, (T, H_kv, D), dev), _arg(v, "v", bf, (T, H_kv, D), dev),
+                          _arg(slots, "slots", torch.int32, (T,), dev),
+                          _arg(k_cache, "k_cache", bf, (nb, H_kv, bs, D), dev),
+                          _arg(v_cache, "v_cache", bf, (nb, H_kv, bs, D), dev), T, H_kv, D, nb, bs,
+                          _raw_stream(stream))
     _raise(rc, "kda_kv_write")
 
 
@@ -591,24 +609,46 @@ def kda_attn_workspace_size(D: int = 128) -> int:
     return int(load().kda_attn_workspace_size(D))
 
 
-def _attend(name: str, args, D: int, device, workspace, stream, fresh):
-    """Calls kda_attn_fwd / kda_attn_paged.  On the current stream the workspace comes from torch's caching
-    allocator; on a stream of the caller's, which that allocator knows nothing of, from the library's pool on
-    that stream, and the outputs made here (``fresh``) are kept until it has passed."""
-    lib = load()
-    if workspace is None and stream is None:
-        workspace = torch.empty(lib.kda_attn_workspace_size(D), dtype=torch.uint8, device=device)
-    elif workspace is not None:
-        _check(workspace, "workspace", torch.uint8)
-    if workspace is None:
-        rc = getattr(lib, name)(*args, _stream(stream))
+_attn_ws_bytes: dict = {}   # by head dimension
+
+
+def _attend(name: str, args, q, heads, out, lse, return_lse: bool, workspace, stream, dev: int):
+    """Outputs, workspace and call of kda_attn_fwd / kda_attn_paged.  On the current stream the workspace comes
+    from torch's caching allocator; on a stream of the caller's, which that allocator knows nothing of, from the
+    library's pool on that stream, and the outputs made here are kept until it has passed."""
+    made = []
+    if out is None:
+        out = torch.empty_like(q)
+        made.append(out)
+        p_out = out.data_ptr()
     else:
-        name += "_ws"
-        rc = getattr(lib, name)(*args, _ptr(workspace), workspace.numel(), _stream(stream))
-    _raise(rc, name)
+        p_out = _arg(out, "out", torch.bfloat16, q.shape, dev)
+    if lse is not None:
+        p_lse = _arg(lse, "lse", torch.float32, heads, dev)
+    elif return_lse:
+        lse = torch.empty(heads, dtype=torch.float32, device=q.device)
+        made.append(lse)
+        p_lse = lse.data_ptr()
+    else:
+        p_lse = None
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8)
+    elif stream is None:
+        D = q.shape[-1]
+        if D not in _attn_ws_bytes:
+            _attn_ws_bytes[D] = kda_attn_workspace_size(D)
+        workspace = torch.empty(_attn_ws_bytes[D], dtype=torch.uint8, device=q.device)
+    s = _raw_stream(stream)
+    if workspace is None:
+        rc = getattr(_lib, name)(*args, p_out, p_lse, s)
+    else:
+        rc = getattr(_lib, name + "_ws")(*args, p_out, p_lse, workspace.data_ptr(), workspace.numel(), s)
+    if rc:
+        _raise(rc, name)
     if stream is not None:
-        for t in fresh:
+        for t in made:
             t.record_stream(stream)
+    return out, lse
 
 
 def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, return_lse: bool = True,
@@ -617,28 +657,17 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, ret
     [B,T,H_kv,D] (bf16, D 64 or 128, H_q a multiple of H_kv); cu_seqlens int32
     [N+1] (device, B = 1) or None; workspace uint8 (kda_attn_workspace_size(D)
     bytes) or None.  Returns (out [B,T,H_q,D], lse [B,T,H_q] fp32 or None)."""
-    bf, f32 = torch.bfloat16, torch.float32
+    load()
+    bf, dev = torch.bfloat16, torch.cuda.current_device() if q.is_cuda else -2
     B, T, H_q, D = q.shape
     H_kv = k.shape[2]
-    N = cu_seqlens.numel() - 1 if cu_seqlens is not None else B
-    _check(q, "q", bf, (B, T, H_q, D))
-    _check(k, "k", bf, (B, T, H_kv, D))
-    _check(v, "v", bf, (B, T, H_kv, D))
-    _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
-    fresh = []
-    if out is None:
-        out = torch.empty((B, T, H_q, D), dtype=bf, device=q.device)
-        fresh.append(out)
-    else:
-        _check(out, "out", bf, (B, T, H_q, D))
-    if lse is not None:
-        _check(lse, "lse", f32, (B, T, H_q))
-    elif return_lse:
-        lse = torch.empty((B, T, H_q), dtype=f32, device=q.device)
-        fresh.append(lse)
-    _attend("kda_attn_fwd", (_ptr(q), _ptr(k), _ptr(v), scale, _ptr(cu_seqlens), N, B, T, H_q, H_kv, D, _ptr(out),
-                             _ptr(lse)), D, q.device, workspace, stream, fresh)
-    return out, lse
+    N, pcu = B, None
+    if cu_seqlens is not None:
+        N = cu_seqlens.shape[0] - 1
+        pcu = _arg(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    args = (_arg(q, "q", bf, (B, T, H_q, D), dev), _arg(k, "k", bf, (B, T, H_kv, D), dev),
+            _arg(v, "v", bf, (B, T, H_kv, D), dev), scale, pcu, N, B, T, H_q, H_kv, D)
+    return _attend("kda_attn_fwd", args, q, (B, T, H_q), out, lse, return_lse, workspace, stream, dev)
 
 
 def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale: float, out=None, lse=None,
@@ -650,28 +679,13 @@ def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale
     block_table [N,max_blocks], seq_lens [N] (int32; cached + new tokens);
     workspace as ``kda_attn_fwd``.  Returns (out [T,H_q,D], lse [T,H_q] fp32 or
     None)."""
-    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    load()
+    bf, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device() if q.is_cuda else -2
     T, H_q, D = q.shape
     nb, H_kv, bs, _ = k_cache.shape
-    N = seq_lens.numel()
-    _check(q, "q", bf, (T, H_q, D))
-    _check(k_cache, "k_cache", bf, (nb, H_kv, bs, D))
-    _check(v_cache, "v_cache", bf, (nb, H_kv, bs, D))
-    _check(block_table, "block_table", i32, (N, block_table.shape[-1]))
-    _check(seq_lens, "seq_lens", i32, (N,))
-    _check(cu_seqlens, "cu_seqlens", i32, (N + 1,))
-    fresh = []
-    if out is None:
-        out = torch.empty((T, H_q, D), dtype=bf, device=q.device)
-        fresh.append(out)
-    else:
-        _check(out, "out", bf, (T, H_q, D))
-    if lse is not None:
-        _check(lse, "lse", f32, (T, H_q))
-    elif return_lse:
-        lse = torch.empty((T, H_q), dtype=f32, device=q.device)
-        fresh.append(lse)
-    _attend("kda_attn_paged", (_ptr(q), _ptr(k_cache), _ptr(v_cache), scale, _ptr(block_table), _ptr(seq_lens),
-                               _ptr(cu_seqlens), N, T, H_q, H_kv, D, nb, bs, block_table.shape[1], _ptr(out),
-                               _ptr(lse)), D, q.device, workspace, stream, fresh)
-    return out, lse
+    N, width = seq_lens.shape[0], block_table.shape[-1]
+    args = (_arg(q, "q", bf, (T, H_q, D), dev), _arg(k_cache, "k_cache", bf, (nb, H_kv, bs, D), dev),
+            _arg(v_cache, "v_cache", bf, (nb, H_kv, bs, D), dev), scale,
+            _arg(block_table, "block_table", i32, (N, width), dev), _arg(seq_lens, "seq_lens", i32, (N,), dev),
+            _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,), dev), N, T, H_q, H_kv, D, nb, bs, width)
+    return _attend("kda_attn_paged", args, q, (T, H_q), out, lse, return_lse, workspace, stream, dev)
