@@ -21,11 +21,12 @@
 //             tensor memory, V MN-major).  The scores of a step are ready two steps ahead, so that neither
 //             the tensor cores nor the softmax wait for the other's latency; a step of 128 keys would leave
 //             tensor memory for one buffer only (2 x 128 columns of S beside 2 x 128 of O).
-//     softmax a thread a row: s from tensor memory, row maximum, p = 2^(s c - m c) with c = scale log2(e),
-//             the sum of p in fp32, and p as bf16 back over s.  Tensor-core operands are bf16, so p is
-//             rounded to it: 2^-8 relative, like the output's own rounding.  The reference maximum m moves
-//             only when the row's has grown by more than 2^8 (p then stays below 2^8, which costs no
-//             precision in floating point), so O is seldom rescaled.
+//     softmax a thread a row: s from tensor memory, p = 2^(s c - m c) with c = scale log2(e), the sum of p
+//             in fp32, and p as bf16.  Tensor-core operands are bf16, so p is rounded to it: 2^-8 relative,
+//             like the output's own rounding.  The reference m is the maximum of the row's first 64 keys
+//             and moves only when a step's sum of p passes 2^16: a larger p costs no precision in floating
+//             point, a common factor cancels in o, and neither the maximum nor a rescaling of O is needed
+//             in most steps.
 // Keys past a row's own position are masked in s.
 // Every wait is bounded; a timeout records KDA_ERR_DEVICE_TIMEOUT and all roles stop.
 #include "attn.h"
@@ -40,7 +41,10 @@ constexpr long long AT_MAX_KEYS = 0x7fffff00;   // key positions, rounded up to 
 constexpr int AT_THREADS = 384;              // 8 softmax warps, 2 issuers, loader, cleaner
 constexpr int AT_ISSUER = 8, AT_LOADER = 10, AT_CLEANER = 11;   // warps
 constexpr int AT_STEP = 64;                  // keys a softmax step
-constexpr float AT_SLACK = 8.0f;             // log2 of how far the row maximum may outgrow its reference
+constexpr int AT_UNIT = 2;                   // what a unit of two query tiles costs beside its key tiles, in tiles
+constexpr float AT_SLACK = 8.0f;             // log2 of how far a row's maximum may outgrow its reference in a step that
+                                             // looks at it
+constexpr float AT_MOST = 65536.0f;          // sum of a step's p that makes it look
 
 template <int D>
 struct AttnLayout {
@@ -71,6 +75,7 @@ struct AttnParams {
     float *o;         // [CTA][2][D / 4][256][4] unnormalised outputs
     float c;          // scale log2(e), not negative
     int neg;          // the scale's sign
+    bool whole;       // out is aligned to 32 bytes
     int G, tile_tokens, tiles;   // query heads a key/value head, tokens a tile, tiles a unit
     int min_share;
 };
@@ -100,7 +105,7 @@ __host__ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 
 // One request: its rows, keys and units
 struct Request {
-    int row0, fresh, keys, units;
+    int row0, fresh, keys, units, cost;   // cost: of a unit, beside its tiles
     __host__ __device__ void load(const AttnParams &p, int n) {
         if (p.a.cu) {
             row0 = p.a.cu[n];
@@ -112,6 +117,7 @@ struct Request {
         }
         const int w = p.tile_tokens * p.tiles;
         units = (fresh + w - 1) / w;
+        cost = fresh > p.tile_tokens ? AT_UNIT : 0;
     }
     // key tiles of the tokens up to (not including) token `end` of the request; at least one, for the
     // rows that see nothing
@@ -119,13 +125,13 @@ struct Request {
         const int seen = keys - fresh + min(end, fresh);
         return seen > AT_KEYS ? (seen + AT_KEYS - 1) / AT_KEYS : 1;
     }
-    // key tiles of the first u units (u <= units) of w tokens each
+    // length of the first u units (u <= units) of w tokens each: their key tiles and their costs
     __host__ __device__ long long prefix(int u, int w) const {
-        long long sum = 0, first = keys - fresh;   // units count max(1, ceil((first + (j + 1) w) / 128))
+        long long sum = (long long)u * cost, first = keys - fresh;   // a unit has max(1, ceil((first + (j + 1) w) / 128)) tiles
         int full = u;
         if (u > 0 && u == units) {
             --full;
-            sum = tiles_to(fresh);
+            sum += tiles_to(fresh);
         }
         int j0 = 0;   // units that see nothing at all or no more than one tile through a negative start
         if (first < 0) {
@@ -145,34 +151,44 @@ struct Request {
 // The pieces of units in this CTA's share, in order
 struct Walk {
     Request r;
-    int n, hk, unit, tile;
+    int n, hk, unit, at;
     long long left;
     // the current piece
     int a, b, all, token0, tokens[2];
     int end[2];      // steps of a query tile up to the piece's end
     int engine;      // of the first query tile
-    __host__ __device__ void start(const AttnParams &p, int n_, int hk_, int unit_, int tile_, long long left_) {
+    __host__ __device__ void start(const AttnParams &p, int n_, int hk_, int unit_, int at_, long long left_) {
         engine = 1;
         tokens[1] = 0;
-        n = n_; hk = hk_; unit = unit_; tile = tile_; left = left_;
+        n = n_; hk = hk_; unit = unit_; at = at_; left = left_;
         if (left > 0) r.load(p, n);
     }
     __host__ __device__ bool next(const AttnParams &p) {
-        if (left <= 0) return false;
-        if (unit >= r.units) {
-            unit = 0;
-            if (++hk == p.a.H_kv) {
-                hk = 0;
-                do r.load(p, ++n);
-                while (r.units == 0);
+        for (;;) {
+            if (left <= 0) return false;
+            if (unit >= r.units) {
+                unit = 0;
+                if (++hk == p.a.H_kv) {
+                    hk = 0;
+                    do r.load(p, ++n);
+                    while (r.units == 0);
+                }
             }
+            token0 = unit * p.tile_tokens * p.tiles;
+            all = r.tiles_to(token0 + p.tile_tokens * p.tiles);
+            // from place `at` of the unit's cost + all
+            const int stop = (int)min((long long)all + r.cost, at + left);
+            a = max(at - r.cost, 0);
+            b = max(stop - r.cost, 0);
+            left -= stop - at;
+            at = stop;
+            if (at == all + r.cost) {
+                at = 0;
+                ++unit;
+            }
+            if (b > a) break;   // a share may end before a unit's first tile
         }
         const int w = p.tile_tokens;
-        token0 = unit * w * p.tiles;
-        all = r.tiles_to(token0 + w * p.tiles);
-        a = tile;
-        b = (int)min((long long)all, tile + left);
-        left -= b - a;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             tokens[i] = i < p.tiles ? max(0, min(w, r.fresh - token0 - i * w)) : 0;
@@ -180,11 +196,6 @@ struct Walk {
             end[i] = tokens[i] ? min(2 * b, seen > AT_STEP ? (seen + AT_STEP - 1) / AT_STEP : 1) : 0;
         }
         engine = tokens[1] ? 0 : engine ^ 1;
-        tile = b;
-        if (b == all) {
-            tile = 0;
-            ++unit;
-        }
         return true;
     }
     __host__ __device__ bool active(int i) const { return end[i] > 2 * a; }
@@ -215,10 +226,16 @@ __device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
     return done != 0;
 }
 
-__device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+// 32 bytes to one place: a whole sector where the place is aligned to it
+__device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w, bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 template <int D, bool PAGED>
@@ -236,7 +253,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::FLAG);
     const int nseq = p.a.cu ? p.a.N : p.a.B;
 
-    // ---- this CTA's share: the tiles of all requests, then the request that holds the share's start
+    // ---- this CTA's share: the length of all requests, then the request that holds the share's start
     if (tid == 0) {
         s_bad = 0;
         p.join[blockIdx.x].pieces = 0;
@@ -244,7 +261,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     }
     __syncthreads();
     long long total = 0, mine = 0, before = 0;
-    auto group = [&](int n0) {   // tiles of requests n0 + tid: this thread's, the ones before it, all
+    auto group = [&](int n0) {   // lengths of requests n0 + tid: this thread's, the ones before it, all
         const int n = n0 + tid;
         mine = 0;
         if (n < nseq) {
@@ -307,8 +324,8 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::SLOT);
     const uint32_t tS = tmem, tO = tmem + 256;
 
-    // the head and unit that hold tile s_x of request s_n: every thread tries one unit, the last that starts at
-    // or before the tile wins
+    // the head and unit that hold place s_x of request s_n: every thread tries one unit, the last that starts at
+    // or before it wins
     Walk w;
     {
         Request r;
@@ -326,7 +343,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             if (unit == u) s_at = at;
             __syncthreads();
             x -= s_at;
-            for (int n; x >= (n = r.tiles_to((unit + 1) * wt)); ++unit) x -= n;
+            for (int n; x >= (n = r.tiles_to((unit + 1) * wt) + r.cost); ++unit) x -= n;
         }
         w.start(p, s_n, hk, unit, (int)x, left);
     }
@@ -549,7 +566,8 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 if (!wait(L::SF + 2 * e + buf, (ns >> 1) & 1)) break;
                 if (warp_real) {
                     tc_fence_after();
-                    uint32_t x[2][32];
+                    uint32_t x[2][32], pk[2][16];
+                    float2 sum;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) tmem_ld32_nowait(s_at + AT_STEP * buf + 32 * b, x[b]);
                     tmem_wait_ld();
@@ -567,52 +585,62 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                             for (int j = 0; j < 32; ++j)
                                 if (32 * b + j >= seen) x[b][j] = 0xff800000u;
                     }
-                    float mx[4];
+                    auto weights = [&]() {
+                        const float base = m == -INFINITY ? 0.f : m * c;
+                        const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        mx[b] = fmaxf(__uint_as_float(x[b >> 1][16 * (b & 1)]), __uint_as_float(x[b >> 1][16 * (b & 1) + 1]));
+                        for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int j = 2; j < 16; j += 2)
-                            mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(x[b >> 1][16 * (b & 1) + j])),
-                                          __uint_as_float(x[b >> 1][16 * (b & 1) + j + 1]));
+                            for (int j = 0; j < 32; j += 2) {
+                                float2 y = __ffma2_rn(make_float2(__uint_as_float(x[b][j]), __uint_as_float(x[b][j + 1])), c2, b2);
+                                y.x = ex2(y.x);
+                                y.y = ex2(y.y);
+                                part[(j >> 1) & 1] = __fadd2_rn(part[(j >> 1) & 1], y);
+                                pk[b][j >> 1] = pack_bf16x2(y.x, y.y);
+                            }
+                        sum = __fadd2_rn(part[0], part[1]);
+                    };
+                    bool look = __any_sync(0xffffffffu, m == -INFINITY);
+                    if (!look) {
+                        weights();
+                        look = __any_sync(0xffffffffu, !(sum.x + sum.y <= AT_MOST));
                     }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    const bool grow = (top - m) * c > AT_SLACK;   // the first step's m is -infinity
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float f = grow ? ex2((m - top) * c) : 1.f;
-                        if (grow) m = top;
-                        l *= f;
-                        if (s > 2 * w.a) {
-                            if (!wait(L::PV + 2 * e + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) break;
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int b = 0; b < D / 16; ++b) {
-                                uint32_t y[16];
-                                tmem_ld16_nowait(o_at + 16 * b, y);
-                                tmem_wait_ld();
+                    if (look) {
+                        float mx[4];
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                                tmem_st16(o_at + 16 * b, y);
+                        for (int b = 0; b < 4; ++b) {
+                            mx[b] = fmaxf(__uint_as_float(x[b >> 1][16 * (b & 1)]), __uint_as_float(x[b >> 1][16 * (b & 1) + 1]));
+#pragma unroll
+                            for (int j = 2; j < 16; j += 2)
+                                mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(x[b >> 1][16 * (b & 1) + j])),
+                                              __uint_as_float(x[b >> 1][16 * (b & 1) + j + 1]));
+                        }
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        const bool grow = (top - m) * c > AT_SLACK;   // the first step's m is -infinity
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float f = grow ? ex2((m - top) * c) : 1.f;
+                            if (grow) m = top;
+                            l *= f;
+                            if (s > 2 * w.a) {
+                                if (!wait(L::PV + 2 * e + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) break;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int b = 0; b < D / 16; ++b) {
+                                    uint32_t y[16];
+                                    tmem_ld16_nowait(o_at + 16 * b, y);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                                    tmem_st16(o_at + 16 * b, y);
+                                }
                             }
                         }
+                        weights();
                     }
-                    const float base = m == -INFINITY ? 0.f : m * c;
-                    const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[b][j]), __uint_as_float(x[b][j + 1])), c2, b2);
-                            y.x = ex2(y.x);
-                            y.y = ex2(y.y);
-                            sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], y);
-                            pk[j >> 1] = pack_bf16x2(y.x, y.y);
-                        }
-                        tmem_st16(s_at + AT_STEP * buf + 16 * b, pk);
-                    }
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    for (int b = 0; b < 2; ++b) tmem_st16(s_at + AT_STEP * buf + 16 * b, pk[b]);
+                    l += sum.x + sum.y;
                     tmem_wait_st();
                     tc_fence_before();
                 }
@@ -629,34 +657,33 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 const long long out_row = ((long long)w.r.row0 + w.token0 + i * p.tile_tokens + tok) * p.a.H_q + w.hk * p.G + g;
                 const int piece = 2 * blockIdx.x + (w.a > 0 ? 0 : 1), prow = i * AT_ROWS + row;
                 const bool any = w.active(i);
-                const float inv = closed ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+                const float inv = l != 0.f ? 1.f / l : 0.f;
                 const float base = m == -INFINITY ? 0.f : m * c;
-#pragma unroll 1
-                for (int b = 0; b < D / 32; ++b) {
-                    uint32_t y[32];
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) {
+                    uint32_t y[2][32];
                     if (any) {
-                        tmem_ld32_nowait(o_at + 32 * b, y);
+                        tmem_ld32_nowait(o_at + 64 * b, y[0]);
+                        tmem_ld32_nowait(o_at + 64 * b + 32, y[1]);
                         tmem_wait_ld();
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) y[j] = 0;
+                        for (int j = 0; j < 64; ++j) y[j >> 5][j & 31] = 0;
                     }
-                    if (!real) continue;
-                    if (closed) {
-                        uint32_t o[16];
+                    if (real && closed) {
+                        uint32_t o[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = l != 0.f ? pack_bf16x2(__uint_as_float(y[j >> 4][(2 * j) & 31]) * inv,
+                                                          __uint_as_float(y[j >> 4][(2 * j + 1) & 31]) * inv) : 0u;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) store_32_bytes(p.a.out + out_row * D + 64 * b + 16 * j, o + 8 * j, p.whole);
+                    } else if (real) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            o[j] = l != 0.f ? pack_bf16x2(__uint_as_float(y[2 * j]) * inv, __uint_as_float(y[2 * j + 1]) * inv) : 0u;
-                        uint16_t *dst = p.a.out + out_row * D + 32 * b;
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                        *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(o[8], o[9], o[10], o[11]);
-                        *reinterpret_cast<uint4 *>(dst + 24) = make_uint4(o[12], o[13], o[14], o[15]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4 *>(p.o + (((size_t)piece * (D / 4) + 8 * b + j) * 256 + prow) * 4) =
-                                make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                            *reinterpret_cast<uint4 *>(p.o + (((size_t)piece * (D / 4) + 16 * b + j) * 256 + prow) * 4) =
+                                make_uint4(y[j >> 3][(4 * j) & 31], y[j >> 3][(4 * j + 1) & 31], y[j >> 3][(4 * j + 2) & 31],
+                                           y[j >> 3][(4 * j + 3) & 31]);
                     }
                 }
                 if (real) {
@@ -831,6 +858,7 @@ cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *l
     base += align256_at(sizeof(float2) * 256 * 2 * AT_MAX_CTAS);
     p.o = reinterpret_cast<float *>(base);
     p.neg = a.scale < 0.f;
+    p.whole = ((uintptr_t)a.out & 31u) == 0;
     // a scale of 0 keeps a vanishing factor instead: the masked scores' -infinity x 0 would be NaN
     p.c = fmaxf(fabsf(a.scale) * LOG2E, 1e-36f);
     p.G = a.H_q / a.H_kv;
