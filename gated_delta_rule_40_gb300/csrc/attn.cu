@@ -41,7 +41,6 @@ constexpr long long AT_MAX_KEYS = 0x7fffff00;   // key positions, rounded up to 
 constexpr int AT_THREADS = 384;              // 8 softmax warps, 2 issuers, loader, cleaner
 constexpr int AT_ISSUER = 8, AT_LOADER = 10, AT_CLEANER = 11;   // warps
 constexpr int AT_STEP = 64;                  // keys a softmax step
-constexpr int AT_UNIT = 2;                   // what a unit of two query tiles costs beside its key tiles, in tiles
 constexpr float AT_SLACK = 8.0f;             // log2 of how far a row's maximum may outgrow its reference in a step that
                                              // looks at it
 constexpr float AT_MOST = 65536.0f;          // sum of a step's p that makes it look
@@ -78,6 +77,7 @@ struct AttnParams {
     bool whole;       // out is aligned to 32 bytes
     int G, tile_tokens, tiles;   // query heads a key/value head, tokens a tile, tiles a unit
     int min_share;
+    int unit_cost;    // of a unit with two query tiles, in key tiles
 };
 
 // Sum of floor((a i + b) / m) over 0 <= i < n, a, m >= 1 (Euclid's descent on the lattice points under a
@@ -117,7 +117,7 @@ struct Request {
         }
         const int w = p.tile_tokens * p.tiles;
         units = (fresh + w - 1) / w;
-        cost = fresh > p.tile_tokens ? AT_UNIT : 0;
+        cost = fresh > p.tile_tokens ? p.unit_cost : 0;
     }
     // key tiles of the tokens up to (not including) token `end` of the request; at least one, for the
     // rows that see nothing
@@ -378,18 +378,20 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         const int my_box = lane % boxes, my_half = lane / boxes;
         while (ok && w.next(p)) {
             const int keys = w.keys(p);
+            // block id of this lane's box of tile t; looked at only when the tile is loaded, a tile later
             auto page = [&](int t) {
                 if (!PAGED) return 0;
                 const int key = t * AT_KEYS + my_box * box;
                 if (key >= keys || my_half >= HALVES || t >= w.b) return 0;
-                const int id = p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)];
-                if (id >= 0 && id < p.a.num_blocks) return id;
-                set_status(KDA_ERR_BAD_PAGES);
-                return p.a.num_blocks;   // past the tensor: zeros
+                return p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)];
             };
             int id = page(w.a);
             for (int t = w.a; ok && t < w.b; ++t) {
                 const int next_id = page(t + 1);
+                if (PAGED && (id < 0 || id >= p.a.num_blocks)) {
+                    set_status(KDA_ERR_BAD_PAGES);
+                    id = p.a.num_blocks;   // past the tensor: zeros
+                }
                 const int n_box = PAGED ? max(0, min(boxes, (keys - t * AT_KEYS + box - 1) / box)) : 1;
                 for (int part = 0; part < 2; ++part, ++kv) {
                     const uint32_t s = kv % L::STAGES, use = kv / L::STAGES;
@@ -604,6 +606,9 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     bool look = __any_sync(0xffffffffu, m == -INFINITY);
                     if (!look) {
                         weights();
+                        // written on trust: the check's latency runs under the store's
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) tmem_st16(s_at + AT_STEP * buf + 16 * b, pk[b]);
                         look = __any_sync(0xffffffffu, !(sum.x + sum.y <= AT_MOST));
                     }
                     if (look) {
@@ -637,9 +642,10 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                             }
                         }
                         weights();
-                    }
+                        tmem_wait_st();
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) tmem_st16(s_at + AT_STEP * buf + 16 * b, pk[b]);
+                        for (int b = 0; b < 2; ++b) tmem_st16(s_at + AT_STEP * buf + 16 * b, pk[b]);
+                    }
                     l += sum.x + sum.y;
                     tmem_wait_st();
                     tc_fence_before();
@@ -865,6 +871,7 @@ cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *l
     p.tile_tokens = AT_ROWS / p.G;
     p.tiles = 2;
     p.min_share = 2;
+    p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
     *launches = 2;
     if (a.lens) return a.D == 64 ? run<64, true>(p, sms, stream) : run<128, true>(p, sms, stream);
     return a.D == 64 ? run<64, false>(p, sms, stream) : run<128, false>(p, sms, stream);
