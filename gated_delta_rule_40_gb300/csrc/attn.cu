@@ -41,15 +41,21 @@ constexpr long long AT_MAX_KEYS = 0x7fffff00;   // key positions, rounded up to 
 constexpr int AT_THREADS = 384;              // 8 softmax warps, 2 issuers, loader, cleaner
 constexpr int AT_ISSUER = 8, AT_LOADER = 10, AT_CLEANER = 11;   // warps
 constexpr int AT_STEP = 64;                  // keys a softmax step
+constexpr int AT_LEAST = 3;                  // tiles of a piece of a unit of two query tiles, at least
 constexpr float AT_SLACK = 8.0f;             // log2 of how far a row's maximum may outgrow its reference in a step that
                                              // looks at it
 constexpr float AT_MOST = 65536.0f;          // sum of a step's p that makes it look
 
-template <int D>
+template <int D, bool PAGED>
 struct AttnLayout {
     static constexpr uint32_t TILE = AT_KEYS * D * 2;          // bytes of a query, key or value tile
     static constexpr int STAGES = D == 128 ? 5 : 8;            // key / value ring
-    static constexpr uint32_t HALF = AT_KEYS * 128;            // bytes of 64 channels of a tile
+    // A tile is made of 8-row x 64-channel swizzled blocks of 1 KiB.  A query tile, and a key or value tile of a
+    // prompt, holds 64 channels of all rows, then the others; with pages, all channels of 8 rows, then the next
+    // 8, so that a page, whatever its length, is one box.
+    static constexpr uint32_t Q_HALF = AT_ROWS * 128;
+    static constexpr uint32_t HALF = PAGED ? 1024 : AT_KEYS * 128;   // from a block to the other 64 channels'
+    static constexpr uint32_t GROUP = PAGED ? 16 * D : 1024;         // from a block to the next 8 rows'
     static constexpr uint32_t Q = STAGES * TILE, BAR = Q + 2 * TILE;
     // barriers: query tile loaded / free [slot]; scores ready, weights ready, output product done
     // [engine][buffer]; output read [engine]; key / value tile loaded / free, value tile to be cleaned loaded
@@ -105,7 +111,8 @@ __host__ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 
 // One request: its rows, keys and units
 struct Request {
-    int row0, fresh, keys, units, cost;   // cost: of a unit, beside its tiles
+    int row0, fresh, keys, units;
+    int cost, least;   // of a unit: its cost beside its tiles, the fewest tiles of a piece
     __host__ __device__ void load(const AttnParams &p, int n) {
         if (p.a.cu) {
             row0 = p.a.cu[n];
@@ -118,12 +125,18 @@ struct Request {
         const int w = p.tile_tokens * p.tiles;
         units = (fresh + w - 1) / w;
         cost = fresh > p.tile_tokens ? p.unit_cost : 0;
+        least = fresh > p.tile_tokens ? AT_LEAST : 1;
     }
     // key tiles of the tokens up to (not including) token `end` of the request; at least one, for the
     // rows that see nothing
     __host__ __device__ int tiles_to(int end) const {
         const int seen = keys - fresh + min(end, fresh);
         return seen > AT_KEYS ? (seen + AT_KEYS - 1) / AT_KEYS : 1;
+    }
+    // A cut of a unit of n tiles at place x of its cost + n: there, or at its start or end where a piece would be
+    // too short to be worth its joining
+    __host__ __device__ int cut(int x, int n) const {
+        return x - cost < least ? 0 : cost + n - x < least ? cost + n : x;
     }
     // length of the first u units (u <= units) of w tokens each: their key tiles and their costs
     __host__ __device__ long long prefix(int u, int w) const {
@@ -157,6 +170,7 @@ struct Walk {
     int a, b, all, token0, tokens[2];
     int end[2];      // steps of a query tile up to the piece's end
     int engine;      // of the first query tile
+    long long line_end;   // place of the share's end in the unit's line
     __host__ __device__ void start(const AttnParams &p, int n_, int hk_, int unit_, int at_, long long left_) {
         engine = 1;
         tokens[1] = 0;
@@ -177,16 +191,14 @@ struct Walk {
             token0 = unit * p.tile_tokens * p.tiles;
             all = r.tiles_to(token0 + p.tile_tokens * p.tiles);
             // from place `at` of the unit's cost + all
-            const int stop = (int)min((long long)all + r.cost, at + left);
-            a = max(at - r.cost, 0);
-            b = max(stop - r.cost, 0);
-            left -= stop - at;
-            at = stop;
-            if (at == all + r.cost) {
-                at = 0;
-                ++unit;
-            }
-            if (b > a) break;   // a share may end before a unit's first tile
+            const int whole = all + r.cost, from = r.cut(at, all), to = at + left >= whole ? whole : r.cut((int)(at + left), all);
+            line_end = at + left;
+            left = at + left >= whole ? at + left - whole : 0;
+            a = max(from - r.cost, 0);
+            b = max(to - r.cost, 0);
+            at = 0;
+            ++unit;
+            if (b > a) break;   // nothing of this unit is left to the share
         }
         const int w = p.tile_tokens;
 #pragma unroll
@@ -218,6 +230,25 @@ __device__ __forceinline__ bool elect_lane() {
     return p != 0;
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];\n" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, int v,
+                                            uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];\n" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(mbar)
+        : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // One probe of a barrier's phase (the thread may sleep in it for a while)
 __device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
     uint32_t done;
@@ -243,23 +274,37 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                                                              const __grid_constant__ CUtensorMap tk,
                                                              const __grid_constant__ CUtensorMap tv,
                                                              const __grid_constant__ AttnParams p) {
-    using L = AttnLayout<D>;
+    using L = AttnLayout<D, PAGED>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = aligned_smem<1024>(smem_raw);
     __shared__ long long s_warp[AT_THREADS / 32], s_x, s_head, s_at;
-    __shared__ int s_n, s_bad, s_unit;
+    __shared__ int s_n, s_unit;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t sbase = smem_u32(sm), bar = sbase + L::BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::FLAG);
     const int nseq = p.a.cu ? p.a.N : p.a.B;
+    grid_dep_launch();   // the joining kernel may come as soon as CTAs leave
+
+    // barriers and tensor memory, under the latency of the lengths' loads
+    bool bad = false;
+    if (tid == 0) {
+        p.join[blockIdx.x].pieces = 0;
+        bad = p.a.cu && (p.a.cu[0] != 0 || (PAGED ? p.a.cu[p.a.N] > p.a.T : p.a.cu[p.a.N] != p.a.T));
+    } else if (tid == 32) {
+        for (int i = 0; i < L::COUNT; ++i)
+            mbar_init(bar + 8 * i, i >= L::KE && i < L::VL ? 2 : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) ? 4 : 1);
+        mbar_fence_init();
+        *abort_flag = 0;
+        s_unit = 0;
+    } else if (tid >= 64 && tid < 67) {
+        prefetch_map(tid == 64 ? &tq : tid == 65 ? &tk : &tv);
+    }
+    if (warp == AT_LOADER) tmem_alloc(sbase + L::SLOT, 512);
+    auto leave = [&]() {
+        if (warp == AT_LOADER) tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(sm + L::SLOT), 512);
+    };
 
     // ---- this CTA's share: the length of all requests, then the request that holds the share's start
-    if (tid == 0) {
-        s_bad = 0;
-        p.join[blockIdx.x].pieces = 0;
-        if (p.a.cu && (p.a.cu[0] != 0 || (PAGED ? p.a.cu[p.a.N] > p.a.T : p.a.cu[p.a.N] != p.a.T))) s_bad = 1;
-    }
-    __syncthreads();
     long long total = 0, mine = 0, before = 0;
     auto group = [&](int n0) {   // lengths of requests n0 + tid: this thread's, the ones before it, all
         const int n = n0 + tid;
@@ -267,10 +312,10 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         if (n < nseq) {
             Request r;
             r.load(p, n);
-            bool bad = p.a.cu && p.a.cu[n + 1] < p.a.cu[n];
-            if (PAGED) bad |= r.keys < 0 || r.keys > min((long long)p.a.max_blocks << p.a.block_log2, AT_MAX_KEYS);
-            if (bad) s_bad = 1;
-            else mine = r.prefix(r.units, p.tile_tokens * p.tiles) * p.a.H_kv;
+            bool wrong = p.a.cu && p.a.cu[n + 1] < p.a.cu[n];
+            if (PAGED) wrong |= r.keys < 0 || r.keys > min((long long)p.a.max_blocks << p.a.block_log2, AT_MAX_KEYS);
+            bad |= wrong;
+            if (!wrong) mine = r.prefix(r.units, p.tile_tokens * p.tiles) * p.a.H_kv;
         }
         long long x = mine;
 #pragma unroll
@@ -278,25 +323,37 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             const long long y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
+        if (nseq > AT_THREADS) __syncthreads();   // the last group's sums have been read
         if (lane == 31) s_warp[warp] = x;
-        __syncthreads();
+        bad = __syncthreads_or(bad);
         long long sum = 0;
         before = x - mine;
+#pragma unroll
         for (int w = 0; w < AT_THREADS / 32; ++w) {
             if (w < warp) before += s_warp[w];
             sum += s_warp[w];
         }
-        __syncthreads();
         return sum;
     };
-    for (int n0 = 0; n0 < nseq; n0 += AT_THREADS) total += group(n0);
-    if (s_bad) {
+    tc_fence_before();
+    total = group(0);
+    tc_fence_after();
+    for (int n0 = AT_THREADS; n0 < nseq; n0 += AT_THREADS) total += group(n0);
+    if (bad) {
         if (tid == 0) set_status(KDA_ERR_BAD_SEQLENS);
+        leave();
         return;
     }
-    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
+    // 32-bit divisions wherever they do
+    auto divide = [](long long a, long long b) {
+        return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+    };
+    const long long share = max(divide(total + gridDim.x - 1, gridDim.x), (long long)p.min_share);
     const long long start = share * blockIdx.x, left = min(share, total - start);
-    if (left <= 0) return;
+    if (left <= 0) {
+        leave();
+        return;
+    }
     long long base = 0;
     for (int n0 = 0; n0 < nseq; n0 += AT_THREADS) {
         const long long sum = nseq <= AT_THREADS ? total : group(n0);
@@ -304,23 +361,13 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             if (start >= base + before && start < base + before + mine) {
                 s_n = n0 + tid;
                 s_x = start - (base + before);
-                s_head = mine / p.a.H_kv;
+                s_head = divide(mine, p.a.H_kv);
             }
             break;
         }
         base += sum;
     }
-    if (tid == 0) {
-        for (int i = 0; i < L::COUNT; ++i)
-            mbar_init(bar + 8 * i, i >= L::KE && i < L::VL ? 2 : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) ? 4 : 1);
-        mbar_fence_init();
-        *abort_flag = 0;
-        s_unit = 0;
-    }
-    if (warp == AT_LOADER) tmem_alloc(sbase + L::SLOT, 512);
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::SLOT);
     const uint32_t tS = tmem, tO = tmem + 256;
 
@@ -331,7 +378,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         Request r;
         r.load(p, s_n);
         const int wt = p.tile_tokens * p.tiles;
-        const int hk = (int)(s_x / s_head);
+        const int hk = (int)divide(s_x, s_head);
         long long x = s_x - hk * s_head;
         int unit = 0;
         if (r.units > 1) {
@@ -375,17 +422,36 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         constexpr int HALVES = D / 64;
         // with pages: a tile is `boxes` boxes of `box` keys
         const int box = PAGED ? min(AT_KEYS, 1 << p.a.block_log2) : AT_KEYS, boxes = AT_KEYS / box;
-        const int my_box = lane % boxes, my_half = lane / boxes;
         while (ok && w.next(p)) {
             const int keys = w.keys(p);
             // block id of this lane's box of tile t; looked at only when the tile is loaded, a tile later
             auto page = [&](int t) {
                 if (!PAGED) return 0;
-                const int key = t * AT_KEYS + my_box * box;
-                if (key >= keys || my_half >= HALVES || t >= w.b) return 0;
+                const int key = t * AT_KEYS + lane * box;
+                if (lane >= boxes || key >= keys || t >= w.b) return 0;
                 return p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)];
             };
             int id = page(w.a);
+            auto queries = [&]() {
+                for (int i = 0; i < 2; ++i) {
+                    if (!w.active(i)) continue;
+                    const uint32_t slot = qu & 1, u = qu >> 1;
+                    ++qu;
+                    if (u > 0 && !wait(L::QE + slot, (u - 1) & 1)) break;
+                    if (lane == 0) {
+                        const uint32_t qf = bar + 8 * (L::QF + slot);
+                        mbar_expect_tx(qf, (uint32_t)(p.G * p.tile_tokens * 128 * HALVES));
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_load_3d(sbase + L::Q + slot * L::TILE + h * L::Q_HALF, &tq, h * 64, w.hk * p.G,
+                                        w.r.row0 + w.token0 + i * p.tile_tokens, qf);
+                    }
+                    __syncwarp();
+                }
+            };
+            // the first queries go out at once; later ones follow the piece's first key tile, so that they wait
+            // for their slot under its load
+            const bool early = qu == 0;
+            if (early) queries();
             for (int t = w.a; ok && t < w.b; ++t) {
                 const int next_id = page(t + 1);
                 if (PAGED && (id < 0 || id >= p.a.num_blocks)) {
@@ -402,30 +468,13 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     const CUtensorMap *m = part ? &tv : &tk;
                     const uint32_t dst = sbase + s * L::TILE;
                     if (PAGED) {
-                        const int off = (t * AT_KEYS + my_box * box) & ((1 << p.a.block_log2) - 1);
-                        if (my_box < n_box && my_half < HALVES)
-                            tma_load_3d(dst + my_half * L::HALF + my_box * box * 128, m, my_half * 64, off,
-                                        id * p.a.H_kv + w.hk, f);
-                    } else if (lane < HALVES) {
-                        tma_load_3d(dst + lane * L::HALF, m, lane * 64, w.r.row0 + t * AT_KEYS, w.hk, f);
+                        const int off = (t * AT_KEYS + lane * box) & ((1 << p.a.block_log2) - 1);
+                        if (lane < n_box)
+                            tma_load_5d(dst + lane * (box / 8) * L::GROUP, m, 0, 0, 0, off / 8, id * p.a.H_kv + w.hk, f);
+                    } else if (lane == 0) {
+                        tma_load_4d(dst, m, 0, w.r.row0 + t * AT_KEYS, 0, w.hk, f);
                     }
-                    // the queries follow the first key tile, so that they wait for their slot under its load
-                    if (t == w.a && part == 0) {
-                        for (int i = 0; i < 2; ++i) {
-                            if (!w.active(i)) continue;
-                            const uint32_t slot = qu & 1, u = qu >> 1;
-                            ++qu;
-                            if (u > 0 && !wait(L::QE + slot, (u - 1) & 1)) break;
-                            if (lane == 0) {
-                                const uint32_t qf = bar + 8 * (L::QF + slot);
-                                mbar_expect_tx(qf, (uint32_t)(p.G * p.tile_tokens * 128 * HALVES));
-                                for (int h = 0; h < HALVES; ++h)
-                                    tma_load_3d(sbase + L::Q + slot * L::TILE + h * L::HALF, &tq, h * 64, w.hk * p.G,
-                                                w.r.row0 + w.token0 + i * p.tile_tokens, qf);
-                            }
-                            __syncwarp();
-                        }
-                    }
+                    if (t == w.a && part == 0 && !early) queries();
                 }
                 id = next_id;
             }
@@ -444,7 +493,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             for (int u = max(w.keys(p) - t * AT_KEYS, 0) * 8 + lane; u < AT_KEYS * 8; u += 32)
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
-                    *reinterpret_cast<uint4 *>(v + h * L::HALF + u * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(v + (u >> 6) * L::GROUP + h * L::HALF + (u & 63) * 16) = make_uint4(0, 0, 0, 0);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + 8 * (L::KF + stage));
@@ -454,7 +503,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         const int e = warp - AT_ISSUER;
         if (elect_lane()) {
             constexpr uint32_t id_s = idesc_bf16(128, AT_STEP), id_o = idesc_bf16(128, D) | (1u << 16);
-            constexpr uint32_t HALF_STEP = AT_STEP * 128;   // bytes between a tile's two steps
+            constexpr uint32_t HALF_STEP = AT_STEP / 8 * L::GROUP;   // bytes between a tile's two steps
             const uint32_t s_at = tS + 128 * e, o_at = tO + D * e;
             // ring positions of the next key and value tile
             uint32_t ks = 0, kp = 0, vs = 1, vp = 0;
@@ -485,11 +534,12 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     const uint32_t buf = (steps + (s - s0)) & 1;
                     if ((s & 1) == 0 && !wait_one(L::KF + ks, kp)) return;
                     tc_fence_after();
-                    const uint64_t dk = umma_desc(sbase + ks * L::TILE + (s & 1) * HALF_STEP, 16, 1024);
+                    const uint64_t dk = umma_desc(sbase + ks * L::TILE + (s & 1) * HALF_STEP, 16, L::GROUP);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t o = (uint64_t)(((k >> 2) * L::HALF + (k & 3) * 32) >> 4);
-                        umma_bf16(s_at + AT_STEP * buf, dq + o, dk + o, id_s, k > 0 ? 1u : 0u);
+                        const uint64_t to_q = (uint64_t)(((k >> 2) * L::Q_HALF + (k & 3) * 32) >> 4);
+                        const uint64_t to_k = (uint64_t)(((k >> 2) * L::HALF + (k & 3) * 32) >> 4);
+                        umma_bf16(s_at + AT_STEP * buf, dq + to_q, dk + to_k, id_s, k > 0 ? 1u : 0u);
                     }
                     umma_commit(bar + 8 * (L::SF + 2 * e + buf));
                     if (s + 1 == s1) umma_commit(bar + 8 * (L::QE + slot));
@@ -506,10 +556,10 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     if (s == s0 && jobs > 0 && !wait_one(L::OE + e, (jobs - 1) & 1)) break;
                     if (!wait_one(L::PF + 2 * e + buf, (n >> 1) & 1)) break;
                     tc_fence_after();
-                    const uint64_t dv = umma_desc(sbase + vs * L::TILE + (s & 1) * HALF_STEP, L::HALF, 1024);
+                    const uint64_t dv = umma_desc(sbase + vs * L::TILE + (s & 1) * HALF_STEP, L::HALF, L::GROUP);
 #pragma unroll
                     for (int k = 0; k < AT_STEP / 16; ++k)
-                        umma_bf16_ta(o_at, s_at + AT_STEP * buf + 8 * k, dv + (uint64_t)(k * (2048 >> 4)), id_o,
+                        umma_bf16_ta(o_at, s_at + AT_STEP * buf + 8 * k, dv + (uint64_t)(k * (2 * L::GROUP >> 4)), id_o,
                                      s > s0 || k > 0 ? 1u : 0u);
                     umma_commit(bar + 8 * (L::PV + 2 * e + buf));
                     if ((s & 1) || s + 1 == s1) {
@@ -553,7 +603,8 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 d.tokens[0] = w.tokens[0];
                 d.tokens[1] = w.tokens[1];
                 d.hk = w.hk;
-                d.pieces = 1 + (int)((w.all - w.b + share - 1) / share);
+                // the shares' ends in the rest of the unit, the first of them this one's, that cut it
+                d.pieces = 2 + (int)((w.all + w.r.cost - w.r.least - w.line_end) / share);
                 p.join[blockIdx.x] = d;
             }
             const int i = w.tile_of(e);
@@ -718,7 +769,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
 // first slots of the CTAs after it, always in that order.  A thread takes 8 channels of one row; the pieces are laid
 // out with rows innermost, so a warp's loads are whole lines.
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p) {
+__global__ __launch_bounds__(256, 4) void attn_join_kernel(const AttnParams p) {
     const int cta = blockIdx.x;
     grid_dep_wait();   // launched while the pieces are still being computed
     const JoinDesc d = p.join[cta];
@@ -729,43 +780,44 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p) {
     if (tok >= d.tokens[i]) return;
     auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
     const long long out_row = ((long long)d.row0 + i * p.tile_tokens + tok) * p.a.H_q + d.hk * p.G + g;
-    for (int c8 = warp; c8 < D / 8; c8 += 8) {
-        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f, M = -INFINITY;
-        // four pieces at a time, so that their loads are in flight together
-        for (int k0 = 0; k0 < d.pieces; k0 += 4) {
-            float2 ml[4];
-            float4 u[4], v[4];
+    const int c8 = blockIdx.z * 8 + warp;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f, M = -INFINITY;
+    // four pieces at a time, so that their loads are in flight together
+    for (int k0 = 0; k0 < d.pieces; k0 += 4) {
+        float2 ml[4];
+        float4 u[4], v[4];
+        float top = M;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                ml[k] = make_float2(-INFINITY, 0.f);
-                u[k] = v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k0 + k < d.pieces) {
-                    ml[k] = p.ml[slot(k0 + k) * 256 + prow];
-                    const float4 *src = reinterpret_cast<const float4 *>(p.o) + (slot(k0 + k) * (D / 4) + 2 * c8) * 256 + prow;
-                    u[k] = src[0];
-                    v[k] = src[256];
-                }
-            }
-            const float top = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
-            const float ref = top == -INFINITY ? 0.f : top, f0 = ex2(M - ref);
-            l *= f0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] *= f0;
-            M = top;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float f = ex2(ml[k].x - ref);
-                l += f * ml[k].y;
-                o[0] += f * u[k].x; o[1] += f * u[k].y; o[2] += f * u[k].z; o[3] += f * u[k].w;
-                o[4] += f * v[k].x; o[5] += f * v[k].y; o[6] += f * v[k].z; o[7] += f * v[k].w;
+        for (int k = 0; k < 4; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            u[k] = v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k < d.pieces) {
+                ml[k] = p.ml[slot(k0 + k) * 256 + prow];
+                const float4 *src = reinterpret_cast<const float4 *>(p.o) + (slot(k0 + k) * (D / 4) + 2 * c8) * 256 + prow;
+                u[k] = src[0];
+                v[k] = src[256];
             }
         }
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        *reinterpret_cast<uint4 *>(p.a.out + out_row * D + 8 * c8) =
-            make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
-                       pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
-        if (c8 == 0 && p.a.lse) p.a.lse[out_row] = l != 0.f ? (M + lg2(l)) * (1.f / LOG2E) : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+        const float ref = top == -INFINITY ? 0.f : top, f0 = ex2(M - ref);
+        l *= f0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] *= f0;
+        M = top;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float f = ex2(ml[k].x - ref);
+            l += f * ml[k].y;
+            o[0] += f * u[k].x; o[1] += f * u[k].y; o[2] += f * u[k].z; o[3] += f * u[k].w;
+            o[4] += f * v[k].x; o[5] += f * v[k].y; o[6] += f * v[k].z; o[7] += f * v[k].w;
+        }
     }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    *reinterpret_cast<uint4 *>(p.a.out + out_row * D + 8 * c8) =
+        make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                   pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+    if (c8 == 0 && p.a.lse) p.a.lse[out_row] = l != 0.f ? (M + lg2(l)) * (1.f / LOG2E) : -INFINITY;
 }
 
 // ---------------------------------------------------------------- host side
@@ -784,17 +836,22 @@ int sm_count() {
     return count[dev];
 }
 
-// A 3-D bf16 tensor (channel, y, z) with the given strides in elements; boxes of 64 channels, 128-byte swizzle
-cudaError_t map_3d(CUtensorMap *m, const void *base, int D, long long y, long long z, long long y_stride,
-                   long long z_stride, int box_y, int box_z) {
+// A bf16 tensor of n dimensions, the first of channels, with the others' strides in elements, in 128-byte
+// swizzled boxes
+cudaError_t tensor_map(CUtensorMap *m, const void *base, int n, const long long *sizes, const long long *strides,
+                       const int *boxes) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     const cudaError_t e = tma_encoder(&enc);
     if (e != cudaSuccess) return e;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)y, (cuuint64_t)z};
-    const cuuint64_t strides[2] = {(cuuint64_t)y_stride * 2, (cuuint64_t)z_stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_y, (cuuint32_t)box_z};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+    cuuint64_t dims[5], bytes[4];
+    cuuint32_t box[5], one[5];
+    for (int i = 0; i < n; ++i) {
+        dims[i] = (cuuint64_t)sizes[i];
+        box[i] = (cuuint32_t)boxes[i];
+        one[i] = 1;
+        if (i > 0) bytes[i - 1] = (cuuint64_t)strides[i - 1] * 2;
+    }
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)n, const_cast<void *>(base), dims, bytes, box, one,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -804,20 +861,29 @@ size_t align256_at(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <int D, bool PAGED>
 cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
-    using L = AttnLayout<D>;
+    using L = AttnLayout<D, PAGED>;
     const AttnArgs &a = p.a;
     const long long rows = (long long)a.B * a.T;
     CUtensorMap mq, mk, mv;
-    cudaError_t e = map_3d(&mq, a.q, D, a.H_q, rows, D, (long long)a.H_q * D, p.G, p.tile_tokens);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    {   // (channel, head, row)
+        const long long size[3] = {D, a.H_q, rows}, stride[2] = {D, (long long)a.H_q * D};
+        const int box[3] = {64, p.G, p.tile_tokens};
+        if ((e = tensor_map(&mq, a.q, 3, size, stride, box)) != cudaSuccess) return e;
+    }
     for (int i = 0; i < 2; ++i) {
         const void *base = i ? a.v : a.k;
         CUtensorMap *m = i ? &mv : &mk;
-        if (PAGED) {
+        if (PAGED) {   // (64 channels, 8 rows, channel halves, groups of 8 rows in a block, block and head)
             const int bs = 1 << a.block_log2;
-            e = map_3d(m, base, D, bs, (long long)a.num_blocks * a.H_kv, D, (long long)bs * D, bs < AT_KEYS ? bs : AT_KEYS, 1);
-        } else {
-            e = map_3d(m, base, D, rows, a.H_kv, (long long)a.H_kv * D, D, AT_KEYS, 1);
+            const long long size[5] = {64, 8, D / 64, bs / 8, (long long)a.num_blocks * a.H_kv};
+            const long long stride[4] = {D, 64, 8 * D, (long long)bs * D};
+            const int box[5] = {64, 8, D / 64, (bs < AT_KEYS ? bs : AT_KEYS) / 8, 1};
+            e = tensor_map(m, base, 5, size, stride, box);
+        } else {   // (64 channels, row, channel halves, head)
+            const long long size[4] = {64, rows, D / 64, a.H_kv}, stride[3] = {(long long)a.H_kv * D, 64, D};
+            const int box[4] = {64, AT_KEYS, D / 64, 1};
+            e = tensor_map(m, base, 4, size, stride, box);
         }
         if (e != cudaSuccess) return e;
     }
@@ -835,7 +901,10 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
     attn_kernel<D, PAGED><<<grid, AT_THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 4 * p.tiles);
+    // rows that a unit can have: a tile's, and those of the next one behind it
+    const int tokens = a.T < p.tile_tokens * p.tiles ? a.T : p.tile_tokens * p.tiles;
+    const int unit_rows = tokens <= p.tile_tokens ? tokens * p.G : AT_ROWS + (tokens - p.tile_tokens) * p.G;
+    cfg.gridDim = dim3(grid, (unit_rows + 31) / 32, D / 64);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
