@@ -654,13 +654,14 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                             }
                         sum = __fadd2_rn(part[0], part[1]);
                     };
-                    bool look = __any_sync(0xffffffffu, m == -INFINITY);
+                    // (rows that stand for nothing hold what was in shared memory, and have no say)
+                    bool look = __any_sync(0xffffffffu, real && m == -INFINITY);
                     if (!look) {
                         weights();
                         // written on trust: the check's latency runs under the store's
 #pragma unroll
                         for (int b = 0; b < 2; ++b) tmem_st16(s_at + AT_STEP * buf + 16 * b, pk[b]);
-                        look = __any_sync(0xffffffffu, !(sum.x + sum.y <= AT_MOST));
+                        look = __any_sync(0xffffffffu, real && !(sum.x + sum.y <= AT_MOST));
                     }
                     if (look) {
                         float mx[4];
@@ -673,7 +674,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                                               __uint_as_float(x[b >> 1][16 * (b & 1) + j + 1]));
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        const bool grow = (top - m) * c > AT_SLACK;   // the first step's m is -infinity
+                        const bool grow = real && (top - m) * c > AT_SLACK;   // the first step's m is -infinity
                         if (__any_sync(0xffffffffu, grow)) {
                             const float f = grow ? ex2((m - top) * c) : 1.f;
                             if (grow) m = top;
