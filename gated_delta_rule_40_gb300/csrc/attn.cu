@@ -17,10 +17,11 @@
 //             unused part of a block): p is 0 there, and 0 x NaN would be NaN
 //   2 engines, each an issuing thread and four softmax warps on one query tile at a time (the two tiles of a
 //             unit, or units of one tile in turn):
-//     issuer  S = Q K^T (M = 128, N = 64) into one of two tensor-memory buffers, then O += P V (P from
-//             tensor memory, V MN-major).  The scores of a step are ready two steps ahead, so that neither
-//             the tensor cores nor the softmax wait for the other's latency; a step of 128 keys would leave
-//             tensor memory for one buffer only (2 x 128 columns of S beside 2 x 128 of O).
+//     issuer  S = Q K^T (M = 128, N = 64) into one of two or three tensor-memory buffers, then O += P V
+//             (P from tensor memory, V MN-major).  A step's scores are issued two or three steps ahead, so
+//             that neither the tensor cores nor the softmax wait for the other's latency.  (N = 128 would
+//             need less of shared memory's bandwidth, which bounds a product of N = 64 to 48 cycles instead
+//             of 32, but leaves room for one buffer only: 1.76 against 1.59 ms for a prompt of 16384 tokens.)
 //     softmax a thread a row: s from tensor memory, p = 2^(s c - m c) with c = scale log2(e), the sum of p
 //             in fp32, and p as bf16.  Tensor-core operands are bf16, so p is rounded to it: 2^-8 relative,
 //             like the output's own rounding.  The reference m is the maximum of the row's first 64 keys
@@ -57,15 +58,16 @@ struct AttnLayout {
     static constexpr uint32_t HALF = PAGED ? 1024 : AT_KEYS * 128;   // from a block to the other 64 channels'
     static constexpr uint32_t GROUP = PAGED ? 16 * D : 1024;         // from a block to the next 8 rows'
     static constexpr uint32_t Q = STAGES * TILE, BAR = Q + 2 * TILE;
+    // Buffers of scores an engine has: what tensor memory holds beside two outputs of D columns
+    static constexpr uint32_t BUFS = (512 - 2 * D) / (2 * AT_STEP) < 3 ? 2 : 3;
     // barriers: query tile loaded / free [slot]; scores ready, weights ready, output product done
     // [engine][buffer]; output read [engine]; key / value tile loaded / free, value tile to be cleaned loaded
-    // [stage].  A step's scores are
-    // ready only after the output product two steps before it, so that with one barrier a buffer no wait can
-    // take an earlier phase for its own.
-    enum { QF = 0, QE = 2, SF = 4, PF = 8, PV = 12, OE = 16, KF = 18, KE = 18 + STAGES, VL = 18 + 2 * STAGES,
-           COUNT = 18 + 3 * STAGES };
+    // [stage].  A step's scores are ready only after the output product BUFS steps before it, so that with one
+    // barrier a buffer no wait can take an earlier phase for its own.
+    enum { QF = 0, QE = 2, SF = 4, PF = SF + 2 * BUFS, PV = PF + 2 * BUFS, OE = PV + 2 * BUFS, KF = OE + 2,
+           KE = KF + STAGES, VL = KF + 2 * STAGES, COUNT = KF + 3 * STAGES };
     static constexpr uint32_t SLOT = BAR + 8 * COUNT, FLAG = SLOT + 4, BYTES = BAR + 512 + 1024;
-    static_assert(8 * COUNT + 8 <= 512 && BYTES <= 232448, "attention shared memory");
+    static_assert(2 * D + 2 * AT_STEP * BUFS <= 512 && 8 * COUNT + 8 <= 512 && BYTES <= 232448, "attention shared memory");
 };
 
 // A unit cut by a share's end: its rows, and how many CTAs from this one on hold a piece of it.
@@ -369,7 +371,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     }
     __syncthreads();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::SLOT);
-    const uint32_t tS = tmem, tO = tmem + 256;
+    const uint32_t tS = tmem, tO = tmem + 2 * AT_STEP * L::BUFS;
 
     // the head and unit that hold place s_x of request s_n: every thread tries one unit, the last that starts at
     // or before it wins
@@ -504,7 +506,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         if (elect_lane()) {
             constexpr uint32_t id_s = idesc_bf16(128, AT_STEP), id_o = idesc_bf16(128, D) | (1u << 16);
             constexpr uint32_t HALF_STEP = AT_STEP / 8 * L::GROUP;   // bytes between a tile's two steps
-            const uint32_t s_at = tS + 128 * e, o_at = tO + D * e;
+            const uint32_t s_at = tS + AT_STEP * L::BUFS * e, o_at = tO + D * e;
             // ring positions of the next key and value tile
             uint32_t ks = 0, kp = 0, vs = 1, vp = 0;
             auto advance = [](uint32_t &stage, uint32_t &phase) {
@@ -531,7 +533,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 const uint64_t dq = umma_desc(sbase + L::Q + slot * L::TILE, 16, 1024);
                 // scores of step s
                 auto scores = [&](int s) {
-                    const uint32_t buf = (steps + (s - s0)) & 1;
+                    const uint32_t buf = (steps + (s - s0)) % L::BUFS;
                     if ((s & 1) == 0 && !wait_one(L::KF + ks, kp)) return;
                     tc_fence_after();
                     const uint64_t dk = umma_desc(sbase + ks * L::TILE + (s & 1) * HALF_STEP, 16, L::GROUP);
@@ -541,32 +543,34 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                         const uint64_t to_k = (uint64_t)(((k >> 2) * L::HALF + (k & 3) * 32) >> 4);
                         umma_bf16(s_at + AT_STEP * buf, dq + to_q, dk + to_k, id_s, k > 0 ? 1u : 0u);
                     }
-                    umma_commit(bar + 8 * (L::SF + 2 * e + buf));
+                    umma_commit(bar + 8 * (L::SF + L::BUFS * e + buf));
                     if (s + 1 == s1) umma_commit(bar + 8 * (L::QE + slot));
                     if ((s & 1) || s + 1 == s1) {
                         umma_commit(bar + 8 * (L::KE + ks));
                         advance(ks, kp);
                     }
                 };
-                if (ok && s0 < s1) scores(s0);
-                if (ok && s0 + 1 < s1) scores(s0 + 1);
+                for (int s = s0; ok && s < s1 && s < s0 + (int)L::BUFS; ++s) scores(s);
                 for (int s = s0; ok && s < s1; ++s) {
-                    const uint32_t n = steps + (s - s0), buf = n & 1;
+                    const uint32_t n = steps + (s - s0), buf = n % L::BUFS;
                     if ((s & 1) == 0 && !wait_one(L::KF + vs, vp)) break;
                     if (s == s0 && jobs > 0 && !wait_one(L::OE + e, (jobs - 1) & 1)) break;
-                    if (!wait_one(L::PF + 2 * e + buf, (n >> 1) & 1)) break;
+                    if (!wait_one(L::PF + L::BUFS * e + buf, (n / L::BUFS) & 1)) break;
                     tc_fence_after();
                     const uint64_t dv = umma_desc(sbase + vs * L::TILE + (s & 1) * HALF_STEP, L::HALF, L::GROUP);
 #pragma unroll
                     for (int k = 0; k < AT_STEP / 16; ++k)
                         umma_bf16_ta(o_at, s_at + AT_STEP * buf + 8 * k, dv + (uint64_t)(k * (2 * L::GROUP >> 4)), id_o,
                                      s > s0 || k > 0 ? 1u : 0u);
-                    umma_commit(bar + 8 * (L::PV + 2 * e + buf));
+                    umma_commit(bar + 8 * (L::PV + L::BUFS * e + buf));
                     if ((s & 1) || s + 1 == s1) {
                         umma_commit(bar + 8 * (L::KE + vs));
                         advance(vs, vp);
                     }
-                    if (s + 2 < s1) scores(s + 2);
+                    // the next scores take this step's buffer: they follow its product, in this thread's order and with the
+                    // fences between them
+                    tc_fence_before();
+                    if (s + (int)L::BUFS < s1) scores(s + L::BUFS);
                 }
                 // tiles of the piece that this engine has no part in
                 for (int t = (s1 + 1) >> 1; ok && t < w.b; ++t) {
@@ -592,7 +596,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         // ------------------------------------------------------------ softmax of engine e
         const int e = warp >> 2, row = (warp & 3) * 32 + lane, tok = row / p.G, g = row - tok * p.G;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tS + 128 * e + lane_off, o_at = tO + D * e + lane_off;
+        const uint32_t s_at = tS + AT_STEP * L::BUFS * e + lane_off, o_at = tO + D * e + lane_off;
         uint32_t ns = 0;   // steps so far: phases of S, P and PV
         const float c = p.c;
         while (ok && w.next(p)) {
@@ -615,8 +619,8 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             const int limit = real ? w.r.keys - w.r.fresh + w.token0 + i * p.tile_tokens + tok + 1 : 0x7fffffff;
             float m = -INFINITY, l = 0.f;   // reference maximum of s, sum of p
             for (int s = 2 * w.a; ok && s < w.end[i]; ++s, ++ns) {
-                const uint32_t buf = ns & 1;
-                if (!wait(L::SF + 2 * e + buf, (ns >> 1) & 1)) break;
+                const uint32_t buf = ns % L::BUFS;
+                if (!wait(L::SF + L::BUFS * e + buf, (ns / L::BUFS) & 1)) break;
                 if (warp_real) {
                     tc_fence_after();
                     uint32_t x[2][32], pk[2][16];
@@ -680,7 +684,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                             if (grow) m = top;
                             l *= f;
                             if (s > 2 * w.a) {
-                                if (!wait(L::PV + 2 * e + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) break;
+                                if (!wait(L::PV + L::BUFS * e + (ns - 1) % L::BUFS, ((ns - 1) / L::BUFS) & 1)) break;
                                 tc_fence_after();
 #pragma unroll 1
                                 for (int b = 0; b < D / 16; ++b) {
@@ -703,12 +707,12 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar + 8 * (L::PF + 2 * e + buf));
+                if (lane == 0) mbar_arrive(bar + 8 * (L::PF + L::BUFS * e + buf));
             }
             if (!ok) break;
             // ---- the piece's rows: final ones go out, others to the workspace
             if (w.active(i)) {
-                if (!wait(L::PV + 2 * e + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) break;
+                if (!wait(L::PV + L::BUFS * e + (ns - 1) % L::BUFS, ((ns - 1) / L::BUFS) & 1)) break;
                 tc_fence_after();
             }
             if (w.tokens[i] && warp_real) {
