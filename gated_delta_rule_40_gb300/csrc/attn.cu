@@ -400,7 +400,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     // Bounded waits, of one thread or of a whole warp (whose lanes give up together).  The first probe is on its
     // own: for a phase that is complete already, which is the rule, it is all that runs.
     bool ok = true;
-    constexpr uint32_t LIMIT = 1u << 20;
+    constexpr uint32_t LIMIT = 1u << 22;
     auto wait_one = [&](int b, uint32_t parity) {
         if (mbar_try(bar + 8 * b, parity)) return true;
         for (uint32_t i = 0; i < LIMIT; ++i) {

@@ -357,7 +357,7 @@ int kda_la_decode(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v,
  * T may exceed the number of new tokens (a captured step of fixed size).  The
  * outputs must not overlap the inputs, except that block_table is both.  Errors in
  * the status word: KDA_ERR_BAD_SEQLENS for a negative length (taken as 0), more than T new
- * tokens (those past T get no slot) or a request longer than its table row, and
+ * tokens (those past T get no slot, nor their blocks an entry) or a request longer than its table row, and
  * KDA_ERR_NO_BLOCKS when free_blocks ends; tokens without a block get slot -1, which
  * kda_kv_write leaves out.
  */
