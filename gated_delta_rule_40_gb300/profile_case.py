@@ -8,6 +8,8 @@
     python -m gated_delta_rule_40_gb300.profile_case --method decode --B 256 --H 64 --iters 4
     python -m gated_delta_rule_40_gb300.profile_case --method gdn --B 1 --T 8192 --H 32 --iters 4
     python -m gated_delta_rule_40_gb300.profile_case --method decode_tokens --B 256 --T 4 --H 64 --iters 4
+    python -m gated_delta_rule_40_gb300.profile_case --method attn --B 1 --T 8192 --H 32 --iters 3
+    python -m gated_delta_rule_40_gb300.profile_case --method attn_decode --B 64 --T 4096 --H 32 --iters 3
 
 Inputs come from ``kda_inputs`` (same recipe as the tests and the benchmark);
 the workspace is allocated once, so every iteration is exactly the three
@@ -16,7 +18,9 @@ and scan_kernel; two for ``kda_la_fwd``: plan and la_fwd_kernel; eight for ``kda
 plan, bwdc_prep_kernel, bwdc_chain_kernel forward and backward, bwdc_gradv_kernel,
 bwdc_gradk_kernel, bwdc_jacobian_kernel and bwdc_dalog_kernel; one for ``kda_decode_tokens``, whose
 ``--T`` is the token count Tq of the step and whose state is fp32 unless
-``--bf16-state``; one for ``kda_decode_step``).  A profiler then selects launches by kernel name and index (e.g.
+``--bf16-state``; one for ``kda_decode_step``; two for ``kda_attn_fwd`` and ``kda_attn_paged``:
+attn_kernel and attn_join_kernel, with a key/value head to four query heads; ``attn_decode``
+gives each of ``--B`` requests one token over a cache of ``--T``).  A profiler then selects launches by kernel name and index (e.g.
 ``ncu -k regex:intra_kernel -s 2 -c 1``).  ``--kernel-times`` (kda and bwd) times the
 last iteration's kernels with the library's CUDA events instead and prints them.
 """
@@ -38,7 +42,8 @@ def main() -> None:
     ap.add_argument("--H", type=int, default=32, help="value heads (= q/k heads)")
     ap.add_argument("--iters", type=int, default=4)
     ap.add_argument("--seed", type=int, default=0)
-    ap.add_argument("--method", choices=["kda", "gdn", "la", "bwd", "la_decode", "decode_tokens", "decode"],
+    ap.add_argument("--method", choices=["kda", "gdn", "la", "bwd", "la_decode", "decode_tokens", "decode", "attn",
+                                         "attn_decode"],
                     default="kda")
     ap.add_argument("--bf16-state", action="store_true", help="decode_tokens: bf16 state")
     ap.add_argument("--kernel-times", action="store_true",
@@ -87,6 +92,26 @@ def main() -> None:
         torch.cuda.synchronize()
         print(f"kda_la_fwd B={a.B} T={a.T} H={a.H} x{a.iters}: |out| {float(out.float().abs().mean()):.6f} "
               f"|S| {float(fin.abs().mean()):.6f}")
+        return
+    if a.method in ("attn", "attn_decode"):
+        g = torch.Generator(device="cuda").manual_seed(a.seed)
+        rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+        Hkv, bs = max(1, a.H // 4), 64
+        if a.method == "attn":
+            q, k, v = rnd(a.B, a.T, a.H, 128), rnd(a.B, a.T, Hkv, 128), rnd(a.B, a.T, Hkv, 128)
+            run = lambda: kda.kda_attn_fwd(q, k, v, 128 ** -0.5)  # noqa: E731
+        else:
+            nb = -(-a.T // bs)
+            q, k, v = rnd(a.B, a.H, 128), rnd(a.B * nb, Hkv, bs, 128), rnd(a.B * nb, Hkv, bs, 128)
+            i32 = dict(dtype=torch.int32, device="cuda")
+            table = torch.randperm(a.B * nb, generator=g, device="cuda").to(torch.int32).reshape(a.B, nb)
+            lens, cu = torch.full((a.B,), a.T, **i32), torch.arange(a.B + 1, **i32)
+            run = lambda: kda.kda_attn_paged(q, k, v, table, lens, cu, 128 ** -0.5)  # noqa: E731
+        for _ in range(a.iters):
+            out, lse = run()
+        torch.cuda.synchronize()
+        print(f"{a.method} B={a.B} T={a.T} H={a.H}/{Hkv} x{a.iters}: |out| {float(out.float().abs().mean()):.6f} "
+              f"lse {float(lse.mean()):.6f}")
         return
     x = kda_inputs.make_inputs(B=a.B, T=a.T, H_qk=a.H, H_v=a.H, seed=a.seed, with_state=True,
                                scalar_gate=a.method == "gdn")
