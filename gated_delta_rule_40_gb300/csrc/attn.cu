@@ -141,7 +141,8 @@ struct Request {
         return x - cost < least ? 0 : cost + n - x < least ? cost + n : x;
     }
     // length of the first u units (u <= units) of w tokens each: their key tiles and their costs
-    __host__ __device__ long long prefix(int u, int w) const {
+    // (not inlined: code that runs once is paid for by its fetching)
+    __host__ __device__ __noinline__ long long prefix(int u, int w) const {
         long long sum = (long long)u * cost, first = keys - fresh;   // a unit has max(1, ceil((first + (j + 1) w) / 128)) tiles
         int full = u;
         if (u > 0 && u == units) {
@@ -173,11 +174,11 @@ struct Walk {
     int end[2];      // steps of a query tile up to the piece's end
     int engine;      // of the first query tile
     long long line_end;   // place of the share's end in the unit's line
-    __host__ __device__ void start(const AttnParams &p, int n_, int hk_, int unit_, int at_, long long left_) {
+    __host__ __device__ void start(const Request &r_, int n_, int hk_, int unit_, int at_, long long left_) {
         engine = 1;
         tokens[1] = 0;
         n = n_; hk = hk_; unit = unit_; at = at_; left = left_;
-        if (left > 0) r.load(p, n);
+        r = r_;
     }
     __host__ __device__ bool next(const AttnParams &p) {
         for (;;) {
@@ -281,6 +282,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     unsigned char *sm = aligned_smem<1024>(smem_raw);
     __shared__ long long s_warp[AT_THREADS / 32], s_x, s_head, s_at;
     __shared__ int s_n, s_unit;
+    __shared__ Request s_req;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t sbase = smem_u32(sm), bar = sbase + L::BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::FLAG);
@@ -308,16 +310,18 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
 
     // ---- this CTA's share: the length of all requests, then the request that holds the share's start
     long long total = 0, mine = 0, before = 0;
+    Request mine_req;
     auto group = [&](int n0) {   // lengths of requests n0 + tid: this thread's, the ones before it, all
         const int n = n0 + tid;
         mine = 0;
         if (n < nseq) {
-            Request r;
-            r.load(p, n);
+            mine_req.load(p, n);
             bool wrong = p.a.cu && p.a.cu[n + 1] < p.a.cu[n];
-            if (PAGED) wrong |= r.keys < 0 || r.keys > min((long long)p.a.max_blocks << p.a.block_log2, AT_MAX_KEYS);
+            if (PAGED)
+                wrong |= mine_req.keys < 0 ||
+                         mine_req.keys > min((long long)p.a.max_blocks << p.a.block_log2, AT_MAX_KEYS);
             bad |= wrong;
-            if (!wrong) mine = r.prefix(r.units, p.tile_tokens * p.tiles) * p.a.H_kv;
+            if (!wrong) mine = mine_req.prefix(mine_req.units, p.tile_tokens * p.tiles) * p.a.H_kv;
         }
         long long x = mine;
 #pragma unroll
@@ -337,39 +341,50 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         }
         return sum;
     };
-    tc_fence_before();
-    total = group(0);
-    tc_fence_after();
-    for (int n0 = AT_THREADS; n0 < nseq; n0 += AT_THREADS) total += group(n0);
-    if (bad) {
-        if (tid == 0) set_status(KDA_ERR_BAD_SEQLENS);
-        leave();
-        return;
-    }
     // 32-bit divisions wherever they do
     auto divide = [](long long a, long long b) {
         return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
     };
-    const long long share = max(divide(total + gridDim.x - 1, gridDim.x), (long long)p.min_share);
-    const long long start = share * blockIdx.x, left = min(share, total - start);
-    if (left <= 0) {
-        leave();
-        return;
-    }
-    long long base = 0;
-    for (int n0 = 0; n0 < nseq; n0 += AT_THREADS) {
-        const long long sum = nseq <= AT_THREADS ? total : group(n0);
-        if (start < base + sum) {
-            if (start >= base + before && start < base + before + mine) {
-                s_n = n0 + tid;
-                s_x = start - (base + before);
-                s_head = divide(mine, p.a.H_kv);
+    tc_fence_before();
+    // first pass: the sum of all; second pass, up to the group that holds the start (the first pass's only
+    // group, mostly)
+    long long share = 0, start = 0, left = 0, base = 0;
+    bool found = false;
+    for (int pass = 0; pass < 2 && !found; ++pass) {
+        base = 0;
+        for (int n0 = 0; !found && (n0 < nseq || n0 == 0); n0 += AT_THREADS) {
+            const long long sum = group(n0);
+            if (pass == 0) {
+                total += sum;
+                if (n0 + AT_THREADS < nseq) continue;
+                if (bad) {
+                    if (tid == 0) set_status(KDA_ERR_BAD_SEQLENS);
+                    leave();
+                    return;
+                }
+                share = max(divide(total + gridDim.x - 1, gridDim.x), (long long)p.min_share);
+                start = share * blockIdx.x;
+                left = min(share, total - start);
+                if (left <= 0) {
+                    leave();
+                    return;
+                }
+                if (nseq > AT_THREADS) break;
             }
-            break;
+            if (start < base + sum) {
+                found = true;
+                if (start >= base + before && start < base + before + mine) {
+                    s_n = n0 + tid;
+                    s_x = start - (base + before);
+                    s_head = divide(mine, p.a.H_kv);
+                    s_req = mine_req;
+                }
+            }
+            base += sum;
         }
-        base += sum;
     }
     __syncthreads();
+    tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::SLOT);
     const uint32_t tS = tmem, tO = tmem + 2 * AT_STEP * L::BUFS;
 
@@ -377,8 +392,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     // or before it wins
     Walk w;
     {
-        Request r;
-        r.load(p, s_n);
+        const Request r = s_req;
         const int wt = p.tile_tokens * p.tiles;
         const int hk = (int)divide(s_x, s_head);
         long long x = s_x - hk * s_head;
@@ -394,7 +408,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             x -= s_at;
             for (int n; x >= (n = r.tiles_to((unit + 1) * wt) + r.cost); ++unit) x -= n;
         }
-        w.start(p, s_n, hk, unit, (int)x, left);
+        w.start(r, s_n, hk, unit, (int)x, left);
     }
 
     // Bounded waits, of one thread or of a whole warp (whose lanes give up together).  The first probe is on its
