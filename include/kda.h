@@ -1,6 +1,7 @@
 /*
  * libkda: Kimi Delta Attention (KDA) forward and single-token decode on
- * NVIDIA GB300 (sm_103a).
+ * NVIDIA GB300 (sm_103a), with lightning attention, and softmax attention over
+ * prompts and a paged cache for the layers between them.
  *
  * KDA is a gated delta-rule linear attention with a per-channel decay.  Per
  * sequence and value head h, with state S (V x K, fp32, S[v][k]):
@@ -390,7 +391,7 @@ int kda_kv_write(const kda_bf16_t *k, const kda_bf16_t *v, const int32_t *slots,
  * head h / (H_q / H_kv).  D is 64 or 128.  cu_seqlens as kda_fwd (B = 1, N packed
  * prompts), else B prompts of T tokens.  A malformed cu_seqlens sets
  * KDA_ERR_BAD_SEQLENS and writes nothing.  Scores, the softmax's statistics and the
- * output sums are fp32; exp(s - max) enters the second product rounded to bf16.
+ * output sums are fp32; the weights exp(s - a reference of the row) enter the second product rounded to bf16.
  * The values a query may not see are multiplied by an exact 0, so a NaN or infinity
  * in v of a later token of the same prompt reaches earlier tokens, as it does in a masked matrix
  * product; tokens of other prompts never do.
