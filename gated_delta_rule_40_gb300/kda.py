@@ -140,11 +140,17 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _raw_stream(stream) -> int:
-    """``_stream`` as a plain number, which ctypes takes too; the current stream without a Stream object."""
+def _raw_stream(stream, device: int) -> int:
+    """``_stream`` as a plain number, which ctypes takes too; the current stream of the current ``device``
+    without a Stream object."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(device)
     return _stream(stream).value or 0
+
+
+def _device_of(t) -> int:
+    """The current device, or -2, which no tensor is on, for a tensor off the GPU (whose check then says so)."""
+    return torch._C._cuda_getDevice() if t.is_cuda else -2
 
 
 def _check(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional=False, device: str = "cuda"):
@@ -169,8 +175,7 @@ def _check(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional=Fal
 
 def _arg(t, name: str, dtype, shape, device: int) -> int:
     """Address of a required tensor after ``_check``'s checks, which for a tensor that passes are made here in
-    a quarter of the time: a call of one decoding step costs the host more than the GPU.  ``device`` is the
-    current one, or -2, which no tensor is on."""
+    a quarter of the time: a call of one decoding step costs the host more than the GPU."""
     if t is not None and t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     _check(t, name, dtype, shape)
@@ -566,7 +571,7 @@ def kda_page_plan(cached_lens, new_lens, free_blocks, free_start, block_table, b
     [N,max_blocks] (new entries written in place), all int32.  ``num_tokens`` is
     the size of the slot map: the number of new tokens, or more."""
     lib = _lib or load()
-    i32, dev = torch.int32, torch.cuda.current_device() if cached_lens.is_cuda else -2
+    i32, dev = torch.int32, _device_of(cached_lens)
     N, F, width = cached_lens.shape[0], free_blocks.shape[0], block_table.shape[-1]
     pc = _arg(cached_lens, "cached_lens", i32, (N,), dev)
     pn = _arg(new_lens, "new_lens", i32, (N,), dev)
@@ -575,18 +580,19 @@ def kda_page_plan(cached_lens, new_lens, free_blocks, free_start, block_table, b
     pt = _arg(block_table, "block_table", i32, (N, width), dev)
     if num_tokens < 0:
         raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
-    # one allocation for the five outputs
-    buf = cached_lens.new_empty(2 * N + 2 * num_tokens + 2)
-    plan = PagePlan(*buf.split_with_sizes((N + 1, N, num_tokens, num_tokens, 1)))
-    at = buf.data_ptr()
-    lens = at + 4 * (N + 1)
-    slots = lens + 4 * N
-    pos = slots + 4 * num_tokens
-    rc = lib.kda_page_plan(pc, pn, pf, ps, pt, N, num_tokens, width, block_size, F, at, lens, slots, pos,
-                           pos + 4 * num_tokens, _raw_stream(stream))
-    _raise(rc, "kda_page_plan")
+    # five allocations: one, split, takes the host 7 us more
+    new, at = torch.empty, cached_lens.device
+    plan = PagePlan(new(N + 1, dtype=i32, device=at), new(N, dtype=i32, device=at),
+                    new(num_tokens, dtype=i32, device=at), new(num_tokens, dtype=i32, device=at),
+                    new(1, dtype=i32, device=at))
+    rc = lib.kda_page_plan(pc, pn, pf, ps, pt, N, num_tokens, width, block_size, F, plan.cu_seqlens.data_ptr(),
+                           plan.seq_lens.data_ptr(), plan.slots.data_ptr(), plan.positions.data_ptr(),
+                           plan.free_next.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _raise(rc, "kda_page_plan")
     if stream is not None:
-        buf.record_stream(stream)
+        for t in plan:
+            t.record_stream(stream)
     return plan
 
 
@@ -594,55 +600,48 @@ def kda_kv_write(k, v, slots, k_cache, v_cache, stream=None) -> None:
     """Store k, v [T,H_kv,D] (bf16) in the caches [num_blocks,H_kv,block_size,D] at
     ``slots`` [T] (int32, kda_page_plan's); a negative slot is left out."""
     lib = _lib or load()
-    bf, dev = torch.bfloat16, torch.cuda.current_device() if k.is_cuda else -2
+    bf, dev = torch.bfloat16, _device_of(k)
     T, H_kv, D = k.shape
     nb, _, bs, _ = k_cache.shape
     rc = lib.kda_kv_write(_arg(k, "k", bf, (T, H_kv, D), dev), _arg(v, "v", bf, (T, H_kv, D), dev),
                           _arg(slots, "slots", torch.int32, (T,), dev),
                           _arg(k_cache, "k_cache", bf, (nb, H_kv, bs, D), dev),
                           _arg(v_cache, "v_cache", bf, (nb, H_kv, bs, D), dev), T, H_kv, D, nb, bs,
-                          _raw_stream(stream))
-    _raise(rc, "kda_kv_write")
+                          _raw_stream(stream, dev))
+    if rc:
+        _raise(rc, "kda_kv_write")
 
 
 def kda_attn_workspace_size(D: int = 128) -> int:
     return int(load().kda_attn_workspace_size(D))
 
 
-_attn_ws_bytes: dict = {}   # by head dimension
-
-
-def _attend(name: str, args, q, heads, out, lse, return_lse: bool, workspace, stream, dev: int):
-    """Outputs, workspace and call of kda_attn_fwd / kda_attn_paged.  On the current stream the workspace comes
-    from torch's caching allocator; on a stream of the caller's, which that allocator knows nothing of, from the
-    library's pool on that stream, and the outputs made here are kept until it has passed."""
+def _attend(call, call_ws, name: str, args, q, heads, out, lse, return_lse: bool, workspace, stream, dev: int):
+    """Outputs, workspace and call of kda_attn_fwd / kda_attn_paged.  The workspace comes from the library's pool
+    (on any stream; 4 us less than an allocation of torch's), under stream capture from torch, whose graphs keep
+    their memory.  Outputs made here for a stream of the caller's are kept until it has passed."""
     made = []
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         made.append(out)
         p_out = out.data_ptr()
     else:
         p_out = _arg(out, "out", torch.bfloat16, q.shape, dev)
+    p_lse = None
     if lse is not None:
         p_lse = _arg(lse, "lse", torch.float32, heads, dev)
     elif return_lse:
         lse = torch.empty(heads, dtype=torch.float32, device=q.device)
         made.append(lse)
         p_lse = lse.data_ptr()
-    else:
-        p_lse = None
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8)
-    elif stream is None:
-        D = q.shape[-1]
-        if D not in _attn_ws_bytes:
-            _attn_ws_bytes[D] = kda_attn_workspace_size(D)
-        workspace = torch.empty(_attn_ws_bytes[D], dtype=torch.uint8, device=q.device)
-    s = _raw_stream(stream)
+    elif stream is None and torch._C._cuda_isCurrentStreamCapturing():
+        workspace = torch.empty(kda_attn_workspace_size(q.shape[-1]), dtype=torch.uint8, device=q.device)
     if workspace is None:
-        rc = getattr(_lib, name)(*args, p_out, p_lse, s)
+        rc = call(*args, p_out, p_lse, _raw_stream(stream, dev))
     else:
-        rc = getattr(_lib, name + "_ws")(*args, p_out, p_lse, workspace.data_ptr(), workspace.numel(), s)
+        rc = call_ws(*args, p_out, p_lse, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         _raise(rc, name)
     if stream is not None:
@@ -657,8 +656,8 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, ret
     [B,T,H_kv,D] (bf16, D 64 or 128, H_q a multiple of H_kv); cu_seqlens int32
     [N+1] (device, B = 1) or None; workspace uint8 (kda_attn_workspace_size(D)
     bytes) or None.  Returns (out [B,T,H_q,D], lse [B,T,H_q] fp32 or None)."""
-    load()
-    bf, dev = torch.bfloat16, torch.cuda.current_device() if q.is_cuda else -2
+    lib = _lib or load()
+    bf, dev = torch.bfloat16, _device_of(q)
     B, T, H_q, D = q.shape
     H_kv = k.shape[2]
     N, pcu = B, None
@@ -667,7 +666,8 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, ret
         pcu = _arg(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
     args = (_arg(q, "q", bf, (B, T, H_q, D), dev), _arg(k, "k", bf, (B, T, H_kv, D), dev),
             _arg(v, "v", bf, (B, T, H_kv, D), dev), scale, pcu, N, B, T, H_q, H_kv, D)
-    return _attend("kda_attn_fwd", args, q, (B, T, H_q), out, lse, return_lse, workspace, stream, dev)
+    return _attend(lib.kda_attn_fwd, lib.kda_attn_fwd_ws, "kda_attn_fwd", args, q, (B, T, H_q), out, lse, return_lse,
+                   workspace, stream, dev)
 
 
 def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale: float, out=None, lse=None,
@@ -679,8 +679,8 @@ def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale
     block_table [N,max_blocks], seq_lens [N] (int32; cached + new tokens);
     workspace as ``kda_attn_fwd``.  Returns (out [T,H_q,D], lse [T,H_q] fp32 or
     None)."""
-    load()
-    bf, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device() if q.is_cuda else -2
+    lib = _lib or load()
+    bf, i32, dev = torch.bfloat16, torch.int32, _device_of(q)
     T, H_q, D = q.shape
     nb, H_kv, bs, _ = k_cache.shape
     N, width = seq_lens.shape[0], block_table.shape[-1]
@@ -688,4 +688,5 @@ def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale
             _arg(v_cache, "v_cache", bf, (nb, H_kv, bs, D), dev), scale,
             _arg(block_table, "block_table", i32, (N, width), dev), _arg(seq_lens, "seq_lens", i32, (N,), dev),
             _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,), dev), N, T, H_q, H_kv, D, nb, bs, width)
-    return _attend("kda_attn_paged", args, q, (T, H_q), out, lse, return_lse, workspace, stream, dev)
+    return _attend(lib.kda_attn_paged, lib.kda_attn_paged_ws, "kda_attn_paged", args, q, (T, H_q), out, lse, return_lse,
+                   workspace, stream, dev)

@@ -199,3 +199,52 @@ def test_binding_refuses_wrong_shapes_and_layouts():
     with pytest.raises(kda.KdaError) as e:
         kda.kda_attn_fwd(bad, bad, bad, 0.1)
     assert e.value.code == kda.KDA_ERR_UNSUPPORTED
+
+
+def _rows_64(q, k, v, scale, limits):
+    """Rows q [A,H,D] in fp64 on the GPU, row i over the first limits[i] of k, v [L,H,D]: out, lse and the out bound."""
+    outs, lses, tols = [], [], []
+    for i, n in enumerate(limits):
+        s = torch.einsum("hd,lhd->hl", q[i].double(), k[:n].double()) * scale
+        lse = torch.logsumexp(s, -1)
+        p = torch.exp(s - lse[:, None])
+        o = torch.einsum("hl,lhd->hd", p, v[:n].double())
+        a = torch.einsum("hl,lhd->hd", p, v[:n].double().abs())
+        outs.append(o)
+        lses.append(lse)
+        tols.append((2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -12) * a) * (1 + 2.0 ** -8))
+    return torch.stack(outs), torch.stack(lses), torch.stack(tols)
+
+
+def test_a_million_keys():
+    """One token over 2^20 + 3 keys: every CTA holds a piece of the same unit."""
+    kda = _kda()
+    L, bs, D = (1 << 20) + 3, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(11)
+    nb = -(-L // bs)
+    kc, vc = (torch.randn((nb, 1, bs, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((1, 1, D), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.randperm(nb, generator=g, device="cuda").to(torch.int32)[None]
+    one = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out, lse = kda.kda_attn_paged(q, kc, vc, table, one([L]), one([0, 1]), D ** -0.5)
+    k, v = (c[table[0].long()].reshape(-1, 1, D) for c in (kc, vc))
+    ro, rl, to = _rows_64(q, k, v, D ** -0.5, [L])
+    assert ((out.double() - ro).abs() <= to).all()
+    assert ((lse.double() - rl).abs() <= 2.0 ** -17 * 30 + 2.0 ** -20 * (1 + rl.abs())).all()
+
+
+def test_long_prompt_and_short_neighbours():
+    """A prompt of 70001 tokens packed behind and before short ones: sampled rows."""
+    kda = _kda()
+    lens, D = [3, 70001, 130], 64
+    T = sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q, k, v = (torch.randn((1, T, 1, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    cu = torch.tensor([0, 3, 70004, T], dtype=torch.int32, device="cuda")
+    out, lse = kda.kda_attn_fwd(q, k, v, D ** -0.5, cu_seqlens=cu)
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+    at = [0, 1, 127, 128, 4095, 30000, 65535, 65536, 70000]
+    ro, rl, to = _rows_64(q[0, [3 + a for a in at]], k[0, 3:], v[0, 3:], D ** -0.5, [a + 1 for a in at])
+    got = out[0, [3 + a for a in at]].double()
+    assert ((got - ro).abs() <= to).all()
+    assert ((lse[0, [3 + a for a in at]].double() - rl).abs() <= 2.0 ** -17 * 30 + 2.0 ** -20 * (1 + rl.abs())).all()
