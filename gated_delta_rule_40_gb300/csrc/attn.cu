@@ -87,7 +87,7 @@ struct JoinDesc {
 
 struct AttnParams {
     AttnArgs a;
-    JoinDesc *join;
+    JoinDesc *join;   // NULL where no unit can be cut
     float2 *ml;       // [CTA][2][256] reference maximum (in log2 units) and sum of a piece's rows
     float *o;         // [CTA][2][D / 4][256][4] unnormalised outputs
     float c;          // scale log2(e), not negative
@@ -302,7 +302,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     // barriers and tensor memory, under the latency of the lengths' loads
     bool bad = false;
     if (tid == 0) {
-        p.join[blockIdx.x].pieces = 0;
+        if (p.join) p.join[blockIdx.x].pieces = 0;
         bad = p.a.cu && (p.a.cu[0] != 0 || (PAGED ? p.a.cu[p.a.N] > p.a.T : p.a.cu[p.a.N] != p.a.T));
     } else if (tid == 32) {
         for (int i = 0; i < L::COUNT; ++i)
@@ -929,7 +929,7 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
         ready[dev & 63] = true;
     }
     attn_kernel<D, PAGED><<<grid, AT_THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || !p.join) return e;
     cudaLaunchConfig_t cfg = {};
     // rows that a unit can have: a tile's, and those of the next one behind it
     const int tokens = a.T < p.tile_tokens * p.tiles ? a.T : p.tile_tokens * p.tiles;
@@ -946,6 +946,11 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
 }
 }  // namespace
 
+// A unit of two query tiles is cut into pieces of AT_LEAST key tiles or more, one of a single query tile anywhere;
+// a prompt of up to 128 / G tokens has one key tile.  So prompts below 2 AT_LEAST key tiles are never cut, and
+// need neither workspace nor the second kernel: 3 us on the GPU and 2 us of the host's.
+bool attn_may_cut(const AttnArgs &a) { return a.lens || a.T > (2 * AT_LEAST - 1) * AT_KEYS; }
+
 size_t attn_workspace_bytes(int D) {
     return align256_at(sizeof(JoinDesc) * AT_MAX_CTAS) + align256_at(sizeof(float2) * 256 * 2 * AT_MAX_CTAS) +
            sizeof(float) * 256 * D * 2 * AT_MAX_CTAS;
@@ -956,8 +961,9 @@ cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *l
     if (sms == 0) return cudaErrorInvalidDevice;
     AttnParams p;
     p.a = a;
+    const bool cut = attn_may_cut(a);
     char *base = static_cast<char *>(ws);
-    p.join = reinterpret_cast<JoinDesc *>(base);
+    p.join = cut ? reinterpret_cast<JoinDesc *>(base) : nullptr;
     base += align256_at(sizeof(JoinDesc) * AT_MAX_CTAS);
     p.ml = reinterpret_cast<float2 *>(base);
     base += align256_at(sizeof(float2) * 256 * 2 * AT_MAX_CTAS);
@@ -971,7 +977,7 @@ cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *l
     p.tiles = 2;
     p.min_share = 2;
     p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
-    *launches = 2;
+    *launches = cut ? 2 : 1;
     if (a.lens) return a.D == 64 ? run<64, true>(p, sms, stream) : run<128, true>(p, sms, stream);
     return a.D == 64 ? run<64, false>(p, sms, stream) : run<128, false>(p, sms, stream);
 }

@@ -18,7 +18,8 @@ struct AttnArgs {
     int num_blocks, block_log2, max_blocks;
 };
 
-// Device workspace of one attention call, for any lengths.
+// Whether the call needs its workspace, and the size of one for any lengths.
+bool attn_may_cut(const AttnArgs &a);
 size_t attn_workspace_bytes(int D);
 cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches);
 

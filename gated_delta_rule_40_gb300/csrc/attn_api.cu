@@ -58,9 +58,11 @@ int validate_attn(const kda::AttnArgs &a) {
 // Runs the kernels in the given workspace, or in one from the library's pool
 int attend(const kda::AttnArgs &a, bool own_ws, void *ws, size_t ws_bytes, cudaStream_t stream) {
     const size_t need = kda::attn_workspace_bytes(a.D);
+    const bool given = !own_ws;
+    own_ws = own_ws && kda::attn_may_cut(a);
     if (own_ws) {
         if (kda::ws_alloc(&ws, need, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    } else if (!ws || !aligned(ws, 256) || ws_bytes < need) {
+    } else if (given && (!ws || !aligned(ws, 256) || ws_bytes < need)) {
         return KDA_ERR_WORKSPACE;
     }
     int launches = 0;

@@ -248,3 +248,18 @@ def test_long_prompt_and_short_neighbours():
     got = out[0, [3 + a for a in at]].double()
     assert ((got - ro).abs() <= to).all()
     assert ((lse[0, [3 + a for a in at]].double() - rl).abs() <= 2.0 ** -17 * 30 + 2.0 ** -20 * (1 + rl.abs())).all()
+
+
+@pytest.mark.parametrize("T", [128, 639, 640, 641, 768, 900])
+def test_prompts_around_the_first_cut(T):
+    """Short prompts run without a workspace and a second kernel; the first lengths that may need them, packed and not."""
+    kda = _kda()
+    g = torch.Generator().manual_seed(T)
+    q, k, v = normal(g, 1, T, 8, 128, gain=1.5), normal(g, 1, T, 1, 128), normal(g, 1, T, 1, 128)
+    ref = reference(q[0], k[0], v[0], 0.1)
+    out, lse = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), 0.1)
+    check(out[0], lse[0], ref)
+    assert kda.kda_last_launch_count() == (1 if T <= 640 else 2)
+    cu = torch.tensor([0, 0, T], dtype=torch.int32, device="cuda")
+    out2, lse2 = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), 0.1, cu_seqlens=cu)
+    check(out2[0], lse2[0], ref)
