@@ -52,6 +52,10 @@ constexpr long long AT_MAX_KEYS = 0x7fffff00;   // key positions, rounded up to 
 constexpr int AT_THREADS = 384;              // 8 softmax warps, 2 issuers, loader, cleaner
 constexpr int AT_ISSUER = 8, AT_LOADER = 10, AT_CLEANER = 11;   // warps
 constexpr int AT_STEP = 64;                  // keys a softmax step
+constexpr int AT_TILES = 2;                  // query tiles a unit: with one, every key tile is loaded twice as often
+                                             // and one engine is idle (16384 tokens: 1.79 against 1.31 ms)
+constexpr int AT_SHARE = 2;                  // key tiles a CTA has at least (4 decoded tokens over 1000 keys: 13 us
+                                             // with 1 or 2, 16 with 3 or 4)
 constexpr int AT_LEAST = 3;                  // tiles of a piece of a unit of two query tiles, at least
 constexpr float AT_SLACK = 8.0f;             // log2 of how far a row's maximum may outgrow its reference in a step that
                                              // looks at it
@@ -93,8 +97,7 @@ struct AttnParams {
     float c;          // scale log2(e), not negative
     int neg;          // the scale's sign
     bool whole;       // out is aligned to 32 bytes
-    int G, tile_tokens, tiles;   // query heads a key/value head, tokens a tile, tiles a unit
-    int min_share;
+    int G, tile_tokens;   // query heads a key/value head, tokens a tile
     int unit_cost;    // of a unit with two query tiles, in key tiles
 };
 
@@ -134,7 +137,7 @@ struct Request {
             row0 = n * p.a.T;
             fresh = keys = p.a.T;
         }
-        const int w = p.tile_tokens * p.tiles;
+        const int w = p.tile_tokens * AT_TILES;
         units = (fresh + w - 1) / w;
         cost = fresh > p.tile_tokens ? p.unit_cost : 0;
         least = fresh > p.tile_tokens ? AT_LEAST : 1;
@@ -201,8 +204,8 @@ struct Walk {
                     while (r.units == 0);
                 }
             }
-            token0 = unit * p.tile_tokens * p.tiles;
-            all = r.tiles_to(token0 + p.tile_tokens * p.tiles);
+            token0 = unit * p.tile_tokens * AT_TILES;
+            all = r.tiles_to(token0 + p.tile_tokens * AT_TILES);
             // from place `at` of the unit's cost + all
             const int whole = all + r.cost, from = r.cut(at, all), to = at + left >= whole ? whole : r.cut((int)(at + left), all);
             line_end = at + left;
@@ -216,7 +219,7 @@ struct Walk {
         const int w = p.tile_tokens;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            tokens[i] = i < p.tiles ? max(0, min(w, r.fresh - token0 - i * w)) : 0;
+            tokens[i] = max(0, min(w, r.fresh - token0 - i * w));
             const int seen = r.keys - r.fresh + token0 + i * w + tokens[i];
             end[i] = tokens[i] ? min(2 * b, seen > AT_STEP ? (seen + AT_STEP - 1) / AT_STEP : 1) : 0;
         }
@@ -230,7 +233,7 @@ struct Walk {
     __host__ __device__ bool dirty(const AttnParams &p, int t) const { return keys(p) < (t + 1) * AT_KEYS; }
     // keys that the unit's last token sees
     __host__ __device__ int keys(const AttnParams &p) const {
-        return max(0, r.keys - r.fresh + min(token0 + p.tile_tokens * p.tiles, r.fresh));
+        return max(0, r.keys - r.fresh + min(token0 + p.tile_tokens * AT_TILES, r.fresh));
     }
 };
 
@@ -331,7 +334,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 wrong |= mine_req.keys < 0 ||
                          mine_req.keys > min((long long)p.a.max_blocks << p.a.block_log2, AT_MAX_KEYS);
             bad |= wrong;
-            if (!wrong) mine = mine_req.prefix(mine_req.units, p.tile_tokens * p.tiles) * p.a.H_kv;
+            if (!wrong) mine = mine_req.prefix(mine_req.units, p.tile_tokens * AT_TILES) * p.a.H_kv;
         }
         long long x = mine;
 #pragma unroll
@@ -372,7 +375,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     leave();
                     return;
                 }
-                share = max(divide(total + gridDim.x - 1, gridDim.x), (long long)p.min_share);
+                share = max(divide(total + gridDim.x - 1, gridDim.x), (long long)AT_SHARE);
                 start = share * blockIdx.x;
                 left = min(share, total - start);
                 if (left <= 0) {
@@ -403,7 +406,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     Walk w;
     {
         const Request r = s_req;
-        const int wt = p.tile_tokens * p.tiles;
+        const int wt = p.tile_tokens * AT_TILES;
         const int hk = (int)divide(s_x, s_head);
         long long x = s_x - hk * s_head;
         int unit = 0;
@@ -932,7 +935,7 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
     if ((e = cudaGetLastError()) != cudaSuccess || !p.join) return e;
     cudaLaunchConfig_t cfg = {};
     // rows that a unit can have: a tile's, and those of the next one behind it
-    const int tokens = a.T < p.tile_tokens * p.tiles ? a.T : p.tile_tokens * p.tiles;
+    const int tokens = a.T < p.tile_tokens * AT_TILES ? a.T : p.tile_tokens * AT_TILES;
     const int unit_rows = tokens <= p.tile_tokens ? tokens * p.G : AT_ROWS + (tokens - p.tile_tokens) * p.G;
     cfg.gridDim = dim3(grid, (unit_rows + 31) / 32, D / 64);
     cfg.blockDim = dim3(256);
@@ -974,8 +977,6 @@ cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *l
     p.c = fmaxf(fabsf(a.scale) * LOG2E, 1e-36f);
     p.G = a.H_q / a.H_kv;
     p.tile_tokens = AT_ROWS / p.G;
-    p.tiles = 2;
-    p.min_share = 2;
     p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
     *launches = cut ? 2 : 1;
     if (a.lens) return a.D == 64 ? run<64, true>(p, sms, stream) : run<128, true>(p, sms, stream);
