@@ -35,7 +35,7 @@
 // memory (75 % of its wavefronts at 8192 tokens), and over long runs the power limit (1.7 GHz): 16384
 // tokens x 32 heads over 8 in 1.31 to 1.34 ms, 1640 to 1680 TFLOP/s, where cuBLAS sustains 1705 on the same
 // board; 20 packed prompts with 16384 tokens in 0.42 to 0.43 ms.  Heads of 64: the softmax's arithmetic, 2 x 4001
-// tokens x 16 heads in 0.089 ms by itself, 0.10 ms behind hot calls.  Decode: DRAM, 256 requests with 2.2 GB of keys and values in 0.346 ms, 6.4 TB/s;
+// tokens x 16 heads in 0.086 ms by itself, 0.093 to 0.10 ms behind hot calls.  Decode: DRAM, 256 requests with 2.2 GB of keys and values in 0.346 ms, 6.4 TB/s;
 // one request over 131072 keys in 0.093 ms, 5.8 TB/s, of which the start and the joining take 10 us.
 // The ring's 160 KiB (heads of 128) cover DRAM's latency at the 45 GB/s that an SM gets of its bandwidth.
 //
@@ -625,7 +625,12 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tS + AT_STEP * L::BUFS * e + lane_off, o_at = tO + D * e + lane_off;
         uint32_t ns = 0;   // steps so far: phases of S, P and PV
-        const float c = p.c;
+        // A negative scale: the sign goes into the factor of p with heads of 64, and into the scores, as they are read,
+        // with heads of 128.  (2 x 4001 tokens x 16 heads of 64: 98 against 103 us; with heads of 128 the factor costs
+        // prompts 0 to 2 % and pages 4 %.)
+        constexpr bool FOLD = D == 64;
+        const float c = p.c, factor = FOLD && p.neg ? -c : c;
+        const uint32_t sign = FOLD && p.neg ? 0x80000000u : 0u, nothing = 0xff800000u ^ sign;   // -infinity
         while (ok && w.next(p)) {
             const bool closed = w.a == 0 && w.b == w.all;
             if (tid == 0 && w.a == 0 && !closed) {
@@ -655,7 +660,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
 #pragma unroll
                     for (int b = 0; b < 2; ++b) tmem_ld32_nowait(s_at + AT_STEP * buf + 32 * b, x[b]);
                     tmem_wait_ld();
-                    if (p.neg) {
+                    if (!FOLD && p.neg) {
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -667,11 +672,11 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (32 * b + j >= seen) x[b][j] = 0xff800000u;
+                                if (32 * b + j >= seen) x[b][j] = nothing;
                     }
                     auto weights = [&]() {
                         const float base = m == -INFINITY ? 0.f : m * c;
-                        const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                        const float2 c2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
                         float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
@@ -696,13 +701,12 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     }
                     if (look) {
                         float mx[4];
+                        auto score = [&](int j) { return __uint_as_float(x[j >> 5][j & 31] ^ sign); };
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            mx[b] = fmaxf(__uint_as_float(x[b >> 1][16 * (b & 1)]), __uint_as_float(x[b >> 1][16 * (b & 1) + 1]));
+                            mx[b] = fmaxf(score(16 * b), score(16 * b + 1));
 #pragma unroll
-                            for (int j = 2; j < 16; j += 2)
-                                mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(x[b >> 1][16 * (b & 1) + j])),
-                                              __uint_as_float(x[b >> 1][16 * (b & 1) + j + 1]));
+                            for (int j = 2; j < 16; j += 2) mx[b] = fmaxf(fmaxf(mx[b], score(16 * b + j)), score(16 * b + j + 1));
                         }
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                         const bool grow = real && (top - m) * c > AT_SLACK;   // the first step's m is -infinity

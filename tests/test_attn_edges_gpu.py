@@ -57,6 +57,29 @@ def test_later_keys_are_never_seen(bad):
     check(out[0, :at], lse[0, :at], ref)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_negative_scale_is_negated_keys(D):
+    """-scale with -k is scale with k, bit for bit: over prompts whose rows' maxima grow and with later keys of any
+    value, and over pages."""
+    kda = _kda()
+    g = torch.Generator().manual_seed(11)
+    T, at = 700, 601
+    q, k, v = normal(g, 1, T, 4, D, gain=3), normal(g, 1, T, 2, D), normal(g, 1, T, 2, D)
+    k[0, 250] *= 8
+    k[0, at:at + 2] = torch.tensor([math.inf, math.nan], dtype=torch.bfloat16)[:, None, None]
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    want, got = kda.kda_attn_fwd(q, k, v, 0.25), kda.kda_attn_fwd(q, -k, v, -0.25)
+    for a, b in zip(want, got):
+        assert torch.isfinite(a[0, :at].float()).all() and torch.equal(a[0, :at], b[0, :at])
+    check(got[0][0, :at], got[1][0, :at], reference(q[0, :at].cpu(), k[0, :at].cpu(), v[0, :at].cpu(), 0.25))
+    c = Paged([1500, 40, 0], [1, 130, 3], 6, 2, D, 32, seed=12)
+    out, lse = c.run()
+    c.check(out, lse)
+    c.kc, c.scale = -c.kc, -c.scale
+    out2, lse2 = c.run()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
 def test_visible_nan_is_not_hidden():
     """A NaN that a row does see is its answer, in a split unit and in a whole one."""
     for total in (90, 9000):
