@@ -36,8 +36,8 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
-            glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
+    headers = [f for d in (CSRC, os.path.join(ROOT, "include")) for x in ("*.cuh", "*.h") for f in glob.glob(os.path.join(d, x))]
+    return _sources() + headers + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
