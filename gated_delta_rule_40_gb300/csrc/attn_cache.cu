@@ -12,7 +12,9 @@ namespace kda {
 // waiting for another's: a few loads a thread.  Each CTA then writes its share of the tokens, whose
 // new blocks it reads from the free list directly (an entry that another CTA writes is never read),
 // and of the per-request outputs.  A new block begins with a new token, whose thread enters the block
-// in the table.  Latency is the bound: 3.6 us for 64 single tokens, 6.2 us for 2000 requests with 66000.
+// in the table; a block that cannot be had is entered as -1, so that no later step takes an old id that
+// stood there for the request's own.  Latency is the bound: 3.6 us for 64 single tokens, 6.3 us for 2000
+// requests with 66000.
 constexpr int PP_THREADS = 1024;
 
 struct PagePlanParams {
@@ -94,6 +96,12 @@ __global__ __launch_bounds__(PP_THREADS) void page_plan_kernel(const PagePlanPar
         __syncthreads();
         tok_base += w_tok[31];
         blk_base += w_blk[31];
+        // Enters a new block of the group's request r.  Without an id (-1) the entry names no block afterwards; one
+        // that is negative does not anyway, and stays.
+        auto enter = [&](int r, long long e, long long id) {
+            int32_t *entry = p.table + (size_t)(n0 + r) * p.max_blocks + e;
+            if (id >= 0 || *entry >= 0) *entry = (int)id;
+        };
         // this CTA's tokens among the group's
         const long long lo = max(t0, s_cu[0]), hi = min(t1, s_cu[PP_THREADS]);
         for (long long t = lo + tid; t < hi; t += PP_THREADS) {
@@ -105,21 +113,28 @@ __global__ __launch_bounds__(PP_THREADS) void page_plan_kernel(const PagePlanPar
             const long long e = pos >> p.block_log2, held = (cached + bs - 1) >> p.block_log2;
             long long id = -1;
             if (e < p.max_blocks) {
-                if (e < held) {
-                    id = p.table[(size_t)(n0 + r) * p.max_blocks + e];
-                } else {
-                    const long long f = s_free[r] + (e - held);
-                    if (f < p.num_free) {
-                        id = p.free_blocks[f];
-                        if ((pos & (bs - 1)) == 0) p.table[(size_t)(n0 + r) * p.max_blocks + e] = (int)id;
-                    }
-                }
+                const long long f = s_free[r] + (e - held);
+                if (e < held) id = p.table[(size_t)(n0 + r) * p.max_blocks + e];
+                else if (f < p.num_free) id = p.free_blocks[f];
+                if (e >= held && (pos & (bs - 1)) == 0) enter(r, e, id);
+                // an owned entry without a block (an earlier step could not have it), or such an id in the list
+                if (id < 0 && (e < held || f < p.num_free)) bad = KDA_ERR_BAD_PAGES;
             }
             const long long slot = id < 0 ? -1 : (id << p.block_log2) + (pos & (bs - 1));
             if (slot > 0x7fffffffll) bad = KDA_ERR_BAD_PAGES;
             p.slots[t] = slot > 0x7fffffffll ? -1 : (int)slot;
             p.positions[t] = (int)min(pos, 0x7fffffffll);
         }
+        // blocks whose first token is past T (reported below): entered all the same, a warp a request
+        if (tok_base > p.T)
+            for (int r = warp * gridDim.x + blockIdx.x; r < min(PP_THREADS, p.N - n0); r += 32 * gridDim.x) {
+                const long long c = s_cached[r], held = (c + bs - 1) >> p.block_log2;
+                const long long end = min((c + s_cu[r + 1] - s_cu[r] + bs - 1) >> p.block_log2, (long long)p.max_blocks);
+                for (long long e = held + lane; e < end; e += 32) {
+                    const long long f = s_free[r] + (e - held);
+                    if (s_cu[r] + (e << p.block_log2) - c >= p.T) enter(r, e, f < p.num_free ? p.free_blocks[f] : -1);
+                }
+            }
     }
     // padding past the last token
     for (long long t = max(t0, tok_base) + tid; t < t1; t += PP_THREADS) p.slots[t] = p.positions[t] = -1;
