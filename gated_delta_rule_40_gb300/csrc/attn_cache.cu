@@ -30,9 +30,10 @@ __global__ __launch_bounds__(PP_THREADS) void page_plan_kernel(const PagePlanPar
     __shared__ long long w_tok[32], w_blk[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int bs = 1 << p.block_log2;
-    const long long start = p.free_start[0];
-    long long tok_base = 0, blk_base = start < 0 ? 0 : start;
-    int bad = start < 0 ? KDA_ERR_NO_BLOCKS : 0;
+    // a negative place is one past the list's end too, where nothing is handed out
+    const uint32_t start = (uint32_t)p.free_start[0];
+    long long tok_base = 0, blk_base = start;
+    int bad = 0;
     // this CTA's tokens
     const long long per = (p.T + (long long)gridDim.x - 1) / gridDim.x;
     const long long t0 = per * blockIdx.x, t1 = min(t0 + per, (long long)p.T);
@@ -140,7 +141,8 @@ __global__ __launch_bounds__(PP_THREADS) void page_plan_kernel(const PagePlanPar
     for (long long t = max(t0, tok_base) + tid; t < t1; t += PP_THREADS) p.slots[t] = p.positions[t] = -1;
     if (blockIdx.x == 0 && tid == 0) {
         p.cu[0] = 0;
-        p.free_next[0] = (int)min(blk_base, (long long)max(p.num_free, 0));
+        p.free_next[0] = (int)(start <= (uint32_t)p.num_free ? min(blk_base, (long long)p.num_free) : start);
+        if (start > (uint32_t)p.num_free) bad = KDA_ERR_NO_BLOCKS;
         if (tok_base > p.T) bad = KDA_ERR_BAD_SEQLENS;
     }
     if (bad) set_status(bad);

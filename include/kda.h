@@ -359,7 +359,8 @@ int kda_la_decode(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v,
  * outputs must not overlap the inputs, except that block_table is both.  Errors in
  * the status word: KDA_ERR_BAD_SEQLENS for a negative length (taken as 0), more than T new
  * tokens (those past T get no slot; their blocks are taken and entered) or a request longer than its
- * table row, KDA_ERR_NO_BLOCKS when free_blocks ends, and KDA_ERR_BAD_PAGES for a new token in a
+ * table row, KDA_ERR_NO_BLOCKS when free_blocks ends or *free_start lies outside 0 .. num_free (then no
+ * block is handed out and *free_next = *free_start), and KDA_ERR_BAD_PAGES for a new token in a
  * block whose id is negative or too large for a slot.  Tokens without a block get slot -1, which
  * kda_kv_write leaves out; the entry of a new block that could not be had is negative afterwards
  * (-1, unless it was negative before), so that later steps give its tokens no slot either and
