@@ -750,6 +750,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                 const long long out_row = ((long long)w.r.row0 + w.token0 + i * p.tile_tokens + tok) * p.a.H_q + w.hk * p.G + g;
                 const int piece = 2 * blockIdx.x + (w.a > 0 ? 0 : 1), prow = i * AT_ROWS + row;
                 const bool any = w.active(i);
+                if (limit <= 0) l = 0.f;   // no key: 0 and -infinity, under a NaN scale too
                 const float inv = l != 0.f ? 1.f / l : 0.f;
                 const float base = m == -INFINITY ? 0.f : m * c;
 #pragma unroll
@@ -977,8 +978,9 @@ cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *l
     p.o = reinterpret_cast<float *>(base);
     p.neg = a.scale < 0.f;
     p.whole = ((uintptr_t)a.out & 31u) == 0;
-    // a scale of 0 keeps a vanishing factor instead: the masked scores' -infinity x 0 would be NaN
-    p.c = fmaxf(fabsf(a.scale) * LOG2E, 1e-36f);
+    // a scale of 0 keeps a vanishing factor instead: the masked scores' -infinity x 0 would be NaN.  A NaN stays one.
+    p.c = fabsf(a.scale) * LOG2E;
+    if (p.c < 1e-36f) p.c = 1e-36f;
     p.G = a.H_q / a.H_kv;
     p.tile_tokens = AT_ROWS / p.G;
     p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
