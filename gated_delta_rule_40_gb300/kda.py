@@ -182,6 +182,19 @@ def _arg(t, name: str, dtype, shape, device: int) -> int:
     return t.data_ptr()
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """Uninitialised memory for a call's output.  With a ``stream`` it is that stream's: freed memory of the caller's
+    stream may still be in use by work queued there, which the call does not wait for.  It is not handed out again
+    before the caller's stream, where it is read, has passed its release."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(caller)
+    return t
+
+
 def _raise(rc: int, where: str):
     if rc != KDA_OK:
         raise KdaError(rc, where)
@@ -581,18 +594,13 @@ def kda_page_plan(cached_lens, new_lens, free_blocks, free_start, block_table, b
     if num_tokens < 0:
         raise ValueError(f"num_tokens must not be negative, got {num_tokens}")
     # five allocations: one, split, takes the host 7 us more
-    new, at = torch.empty, cached_lens.device
-    plan = PagePlan(new(N + 1, dtype=i32, device=at), new(N, dtype=i32, device=at),
-                    new(num_tokens, dtype=i32, device=at), new(num_tokens, dtype=i32, device=at),
-                    new(1, dtype=i32, device=at))
+    at = cached_lens.device
+    plan = PagePlan(*[_new(n, i32, at, stream) for n in (N + 1, N, num_tokens, num_tokens, 1)])
     rc = lib.kda_page_plan(pc, pn, pf, ps, pt, N, num_tokens, width, block_size, F, plan.cu_seqlens.data_ptr(),
                            plan.seq_lens.data_ptr(), plan.slots.data_ptr(), plan.positions.data_ptr(),
                            plan.free_next.data_ptr(), _raw_stream(stream, dev))
     if rc:
         _raise(rc, "kda_page_plan")
-    if stream is not None:
-        for t in plan:
-            t.record_stream(stream)
     return plan
 
 
@@ -619,11 +627,9 @@ def kda_attn_workspace_size(D: int = 128) -> int:
 def _attend(call, call_ws, name: str, args, q, heads, out, lse, return_lse: bool, workspace, stream, dev: int):
     """Outputs, workspace and call of kda_attn_fwd / kda_attn_paged.  The workspace comes from the library's pool
     (on any stream; 4 us less than an allocation of torch's), under stream capture from torch, whose graphs keep
-    their memory.  Outputs made here for a stream of the caller's are kept until it has passed."""
-    made = []
+    their memory."""
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        made.append(out)
+        out = _new(q.shape, torch.bfloat16, q.device, stream)
         p_out = out.data_ptr()
     else:
         p_out = _arg(out, "out", torch.bfloat16, q.shape, dev)
@@ -631,8 +637,7 @@ def _attend(call, call_ws, name: str, args, q, heads, out, lse, return_lse: bool
     if lse is not None:
         p_lse = _arg(lse, "lse", torch.float32, heads, dev)
     elif return_lse:
-        lse = torch.empty(heads, dtype=torch.float32, device=q.device)
-        made.append(lse)
+        lse = _new(heads, torch.float32, q.device, stream)
         p_lse = lse.data_ptr()
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8)
@@ -644,9 +649,6 @@ def _attend(call, call_ws, name: str, args, q, heads, out, lse, return_lse: bool
         rc = call_ws(*args, p_out, p_lse, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         _raise(rc, name)
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
     return out, lse
 
 
