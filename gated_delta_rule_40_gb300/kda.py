@@ -224,10 +224,10 @@ def kda_fwd(q, k, v, graw, b, A_log, scale: float, initial_state=None, cu_seqlen
     _check(initial_state, "initial_state", torch.float32, (N, H_v, V, K), optional=True)
     _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
     if out is None:
-        out = torch.empty((B, T, H_v, V), dtype=bf, device=q.device)
+        out = _new((B, T, H_v, V), bf, q.device, stream)
     _check(out, "out", bf, (B, T, H_v, V))
     if final_state is None and output_final_state:
-        final_state = torch.empty((N, H_v, V, K), dtype=torch.float32, device=q.device)
+        final_state = _new((N, H_v, V, K), torch.float32, q.device, stream)
     _check(final_state, "final_state", torch.float32, (N, H_v, V, K), optional=True)
     args = [_ptr(q), _ptr(k), _ptr(v), _ptr(graw), _ptr(b), _ptr(A_log), ctypes.c_float(scale),
             _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens), N, B, T, H_qk, H_v, K, V, _ptr(out)]
@@ -261,10 +261,10 @@ def kda_fwd_scalar_gate(q, k, v, graw, b, A_log, scale: float, initial_state=Non
     _check(initial_state, "initial_state", torch.float32, (N, H_v, V, K), optional=True)
     _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
     if out is None:
-        out = torch.empty((B, T, H_v, V), dtype=bf, device=q.device)
+        out = _new((B, T, H_v, V), bf, q.device, stream)
     _check(out, "out", bf, (B, T, H_v, V))
     if final_state is None and output_final_state:
-        final_state = torch.empty((N, H_v, V, K), dtype=torch.float32, device=q.device)
+        final_state = _new((N, H_v, V, K), torch.float32, q.device, stream)
     _check(final_state, "final_state", torch.float32, (N, H_v, V, K), optional=True)
     rc = lib.kda_fwd_scalar_gate(_ptr(q), _ptr(k), _ptr(v), _ptr(graw), _ptr(b), _ptr(A_log), ctypes.c_float(scale),
                                  _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens), N, B, T, H_qk, H_v, K, V,
@@ -337,7 +337,7 @@ def kda_fwd_noalloc(q, k, v, graw, b, A_log, scale: float, initial_state=None, c
     _check(initial_state, "initial_state", torch.float32, (N, H_v, V, K), optional=True)
     _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
     if out is None:
-        out = torch.empty((B, T, H_v, V), dtype=bf, device=q.device)
+        out = _new((B, T, H_v, V), bf, q.device, stream)
     _check(out, "out", bf, (B, T, H_v, V))
     _check(final_state, "final_state", torch.float32, (N, H_v, V, K), optional=True)
     rc = lib.kda_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(graw), _ptr(b), _ptr(A_log), ctypes.c_float(scale),
@@ -362,7 +362,7 @@ def kda_decode_step(q, k, v, graw, b, A_log, scale: float, state, out=None, stre
     _check(A_log, "A_log", torch.float32, (H_v,))
     _check(state, "state", torch.float32, (B, H_v, V, K))
     if out is None:
-        out = torch.empty((B, H_v, V), dtype=bf, device=q.device)
+        out = _new((B, H_v, V), bf, q.device, stream)
     _check(out, "out", bf, (B, H_v, V))
     rc = lib.kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(graw), _ptr(b), _ptr(A_log),
                              ctypes.c_float(scale), _ptr(state), B, H_qk, H_v, K, V, _ptr(out),
@@ -421,7 +421,7 @@ def kda_decode_tokens(q, k, v, graw, b, A_log, scale: float, state, out=None, st
         raise TypeError(f"state must be float32 or bfloat16, got {state.dtype}")
     _check(state, "state", state.dtype, (B, H_v, V, K))
     if out is None:
-        out = torch.empty((B, Tq, H_v, V), dtype=bf, device=q.device)
+        out = _new((B, Tq, H_v, V), bf, q.device, stream)
     _check(out, "out", bf, (B, Tq, H_v, V))
     rc = lib.kda_decode_tokens(_ptr(q), _ptr(k), _ptr(v), _ptr(graw), _ptr(b), _ptr(A_log), ctypes.c_float(scale),
                                _ptr(state), 1 if state.dtype == bf else 0, B, Tq, H_qk, H_v, K, V, _ptr(out),
@@ -455,10 +455,10 @@ def kda_la_fwd(q, k, v, slope, scale: float, initial_state=None, cu_seqlens=None
     _check(initial_state, "initial_state", torch.float32, (N, H_v, V, K), optional=True)
     _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
     if out is None:
-        out = torch.empty((B, T, H_v, V), dtype=bf, device=q.device)
+        out = _new((B, T, H_v, V), bf, q.device, stream)
     _check(out, "out", bf, (B, T, H_v, V))
     if final_state is None and output_final_state:
-        final_state = torch.empty((N, H_v, V, K), dtype=torch.float32, device=q.device)
+        final_state = _new((N, H_v, V, K), torch.float32, q.device, stream)
     _check(final_state, "final_state", torch.float32, (N, H_v, V, K), optional=True)
     rc = lib.kda_la_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(slope), ctypes.c_float(scale), _ptr(initial_state),
                         _ptr(final_state), _ptr(cu_seqlens), N, B, T, H_qk, H_v, K, V, _ptr(out), _stream(stream))
@@ -479,7 +479,7 @@ def kda_la_decode(q, k, v, slope, scale: float, state, out=None, stream=None) ->
     _check(slope, "slope", torch.float32, (H_v,))
     _check(state, "state", torch.float32, (B, H_v, V, K))
     if out is None:
-        out = torch.empty((B, H_v, V), dtype=bf, device=q.device)
+        out = _new((B, H_v, V), bf, q.device, stream)
     _check(out, "out", bf, (B, H_v, V))
     rc = lib.kda_la_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(slope), ctypes.c_float(scale), _ptr(state), B, H_qk,
                            H_v, K, V, _ptr(out), _stream(stream))
@@ -516,16 +516,16 @@ def kda_bwd(q, k, v, graw, b, A_log, scale: float, dout, initial_state=None, cu_
     _check(dht, "dht", f32, (N, H_v, V, K), optional=True)
     _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
     dev = q.device
-    g = {"dq": torch.empty((B, T, H_qk, K), dtype=f32, device=dev),
-         "dk": torch.empty((B, T, H_qk, K), dtype=f32, device=dev),
-         "dv": torch.empty((B, T, H_v, V), dtype=f32, device=dev),
-         "dgraw": torch.empty((B, T, H_v, K), dtype=f32, device=dev),
-         "db": torch.empty((B, T, H_v), dtype=f32, device=dev),
-         "dA_log": torch.empty((H_v,), dtype=f32, device=dev),
-         "dh0": torch.empty((N, H_v, V, K), dtype=f32, device=dev)}
+    g = {"dq": _new((B, T, H_qk, K), f32, dev, stream),
+         "dk": _new((B, T, H_qk, K), f32, dev, stream),
+         "dv": _new((B, T, H_v, V), f32, dev, stream),
+         "dgraw": _new((B, T, H_v, K), f32, dev, stream),
+         "db": _new((B, T, H_v), f32, dev, stream),
+         "dA_log": _new((H_v,), f32, dev, stream),
+         "dh0": _new((N, H_v, V, K), f32, dev, stream)}
     if workspace is None:
         nbytes = int(lib.kda_bwd_workspace_size(N, B, T, H_qk, H_v, K, V))
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        workspace = _new(max(nbytes, 1), torch.uint8, dev, stream)
     _check(workspace, "workspace", torch.uint8)
     rc = lib.kda_bwd_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(graw), _ptr(b), _ptr(A_log), ctypes.c_float(scale),
                         _ptr(initial_state), _ptr(cu_seqlens), N, B, T, H_qk, H_v, K, V, _ptr(dout), _ptr(dht),
@@ -555,10 +555,10 @@ def kda_fwd_bf16_state(q, k, v, graw, b, A_log, scale: float, initial_state=None
     _check(initial_state, "initial_state", bf, (N, H_v, V, K), optional=True)
     _check(cu_seqlens, "cu_seqlens", torch.int32, optional=True)
     if out is None:
-        out = torch.empty((B, T, H_v, V), dtype=bf, device=q.device)
+        out = _new((B, T, H_v, V), bf, q.device, stream)
     _check(out, "out", bf, (B, T, H_v, V))
     if final_state is None and output_final_state:
-        final_state = torch.empty((N, H_v, V, K), dtype=bf, device=q.device)
+        final_state = _new((N, H_v, V, K), bf, q.device, stream)
     _check(final_state, "final_state", bf, (N, H_v, V, K), optional=True)
     rc = lib.kda_fwd_bf16_state(_ptr(q), _ptr(k), _ptr(v), _ptr(graw), _ptr(b), _ptr(A_log), ctypes.c_float(scale),
                                 _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens), N, B, T, H_qk, H_v, K, V,

@@ -89,3 +89,38 @@ def test_outputs_come_from_the_stream_that_writes_them(made, call, outputs):
     assert len(made) == outputs
     for m in made:
         assert m.allocated is SIDE and CALLER in m.recorded
+
+
+def _linear(name, *extra, lead=(1, 4), K=128, state=None, gate=True, **kw):
+    """A call of the linear-attention entry points on [*lead, heads, K] inputs."""
+    q, v = _tensors((*lead, 2, K), (*lead, 2, K))
+    args = [q, q, v] + ([v, torch.zeros(*lead, 2)] if gate else []) + [torch.zeros(2), 0.1, *extra]
+    if state is not None:
+        args.append(torch.zeros(state))
+    return lambda stream: getattr(kda, name)(*args, stream=stream, **kw)
+
+
+LINEAR = [
+    (_linear("kda_fwd"), 2), (_linear("kda_fwd_scalar_gate"), 2), (_linear("kda_fwd_bf16_state"), 2),
+    (_linear("kda_fwd_noalloc"), 1), (_linear("kda_la_fwd", gate=False), 2),
+    (_linear("kda_decode_step", lead=(3,), state=(3, 2, 128, 128)), 1),
+    (_linear("kda_la_decode", lead=(3,), state=(3, 2, 128, 128), gate=False), 1),
+    (_linear("kda_decode_tokens", lead=(3, 4), state=(3, 2, 128, 128)), 1),
+    (_linear("kda_bwd", torch.zeros((1, 4, 2, 128))), 8)]   # seven gradients and the workspace
+
+
+@pytest.mark.parametrize("call,outputs", LINEAR)
+def test_linear_attention_outputs_come_from_the_stream_that_writes_them(made, call, outputs):
+    call(SIDE)
+    assert len(made) == outputs
+    for m in made:
+        assert m.allocated is SIDE and CALLER in m.recorded
+
+
+@pytest.mark.parametrize("call,outputs", SERVING + LINEAR)
+def test_without_a_stream_nothing_is_recorded(made, monkeypatch, call, outputs):
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
+    call(None)
+    assert len(made) == outputs
+    assert all(m.allocated is CALLER and not m.recorded for m in made)
