@@ -21,6 +21,12 @@ void timing_mark(const char *name, cudaStream_t s);
 namespace {
 bool aligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
+// Every int32 array (or NULL) starts on 4 bytes
+template <typename... P>
+bool ints_aligned(const P *...p) {
+    return (... && aligned(p, 4));
+}
+
 // log2 of a supported block size, or -1
 int block_log2(int size) {
     for (int s = 4; s <= 10; ++s)
@@ -50,7 +56,8 @@ int validate_attn(const kda::AttnArgs &a) {
     if (tokens * a.H_q > 0x7fffffffLL || (long long)(a.cu ? a.N : a.B) * a.H_q > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
     if (tokens == 0) return KDA_OK;
     if (!a.q || !a.k || !a.v || !a.out) return KDA_ERR_INVALID_ARG;
-    if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.out, 16) || !aligned(a.lse, 4))
+    if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.out, 16) || !aligned(a.lse, 4) ||
+        !ints_aligned(a.cu, a.table, a.lens))
         return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
@@ -119,6 +126,9 @@ int kda_page_plan(const int32_t *cached_lens, const int32_t *new_lens, const int
     if (!free_start || !free_next || !cu_seqlens) return KDA_ERR_INVALID_ARG;
     if (N > 0 && (!cached_lens || !new_lens || !seq_lens || (max_blocks > 0 && !block_table))) return KDA_ERR_INVALID_ARG;
     if ((T > 0 && (!slots || !positions)) || (num_free > 0 && !free_blocks)) return KDA_ERR_INVALID_ARG;
+    if (!ints_aligned(cached_lens, new_lens, free_blocks, free_start, block_table, cu_seqlens, seq_lens, slots, positions,
+                      free_next))
+        return KDA_ERR_INVALID_ARG;
     kda::timing_begin(stream);
     return finish(kda::launch_page_plan(cached_lens, new_lens, free_blocks, free_start, block_table, N, T, max_blocks,
                                         lg, num_free, cu_seqlens, seq_lens, slots, positions, free_next, stream),
@@ -134,7 +144,9 @@ int kda_kv_write(const kda_bf16_t *k, const kda_bf16_t *v, const int32_t *slots,
     if ((long long)T * H_kv * (D / 8) > 0x7fffffffLL * 256) return KDA_ERR_INVALID_ARG;
     if (T == 0) return nothing_to_do();
     if (!k || !v || !slots || (num_blocks > 0 && (!k_cache || !v_cache))) return KDA_ERR_INVALID_ARG;
-    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(slots, 4))
+        return KDA_ERR_INVALID_ARG;
     kda::timing_begin(stream);
     return finish(kda::launch_kv_write(k, v, slots, k_cache, v_cache, T, H_kv, D, num_blocks, lg, stream),
                   "kv_write_kernel", stream);

@@ -338,6 +338,8 @@ int kda_la_decode(const kda_bf16_t *q, const kda_bf16_t *k, const kda_bf16_t *v,
  * [N, max_blocks] int32 names request n's blocks in order: token p of the request
  * is row p % block_size of block block_table[n][p / block_size], and its slot is
  * that block id * block_size + p % block_size.
+ *
+ * q, k, v, out and the caches must be 16-byte aligned, lse and the int32 arrays 4-byte.
  */
 
 /*
