@@ -20,7 +20,14 @@
 //             unit, or units of one tile in turn):
 //     issuer  S = Q K^T (M = 128, N = 64) into one of two or three tensor-memory buffers, then O += P V
 //             (P from tensor memory, V MN-major).  A step's scores are issued two or three steps ahead, so
-//             that neither the tensor cores nor the softmax wait for the other's latency.  (N = 128 would
+//             that neither the tensor cores nor the softmax wait for the other's latency.  They overwrite the
+//             weights that the output product BUFS steps before reads, and are issued behind it by the same thread
+//             without waiting for it.  That rests on the tensor cores running one thread's products in the order
+//             of their issue.  PTX promises that only for products with the same accumulator and shape, which
+//             these are not, and no fence here adds to it; no run has shown another order.  Waiting for the
+//             product takes 16384 tokens from 1.32 to 1.45 ms (spinning; 1.49 with try_wait), chunks among single
+//             tokens from 127 to 142 us, decode from 347 to 350 us, and with heads of 64 a prompt of 2 x 4001
+//             tokens from 98 to 100 us and decode (256 requests, 16 heads over 8) from 208 to 217 us.  (N = 128 would
 //             need less of shared memory's bandwidth, which bounds a product of N = 64 to 48 cycles instead
 //             of 32, but leaves room for one buffer only: 1.76 against 1.59 ms for a prompt of 16384 tokens.)
 //     softmax a thread a row: s from tensor memory, p = 2^(s c - m c) with c = scale log2(e), the sum of p
@@ -594,8 +601,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                         umma_commit(bar + 8 * (L::KE + vs));
                         advance(vs, vp);
                     }
-                    // the next scores take this step's buffer: they follow its product, in this thread's order and with the
-                    // fences between them
+                    // the next scores take this step's buffer behind its product (see "issuer" at the top)
                     tc_fence_before();
                     if (s + (int)L::BUFS < s1) scores(s + L::BUFS);
                 }
