@@ -174,7 +174,7 @@ struct Request {
             j0 = (int)min((long long)full, (-first) / w);
             sum += j0;
             first += (long long)j0 * w;
-            if (j0 < full && first < 0) {   // the unit that reaches the first key: its end is below w <= 128
+            if (j0 < full && first < 0) {   // the unit that reaches the first key: it ends below w <= 256
                 sum += max(1ll, (first + w + AT_KEYS - 1) / AT_KEYS);
                 ++j0;
                 first += w;
