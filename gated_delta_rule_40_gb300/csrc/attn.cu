@@ -38,13 +38,15 @@
 //             in most steps.
 // Keys past a row's own position are masked in s.
 //
-// What bounds it, and what it measured.  Prompts: the tensor cores, whose N = 64 products wait for shared
+// What bounds it, and what it measured (on the GPU, without a call's host side).  Prompts: the tensor cores, whose N = 64 products wait for shared
 // memory (75 % of its wavefronts at 8192 tokens), and over long runs the power limit (1.7 GHz): 16384
 // tokens x 32 heads over 8 in 1.31 to 1.34 ms, 1640 to 1680 TFLOP/s, where cuBLAS sustains 1705 on the same
 // board; 20 packed prompts with 16384 tokens in 0.42 to 0.43 ms.  Heads of 64: the softmax's arithmetic, 2 x 4001
-// tokens x 16 heads in 0.086 ms by itself, 0.093 to 0.10 ms behind hot calls.  Decode: DRAM, 256 requests with 2.2 GB of keys and values in 0.346 ms, 6.4 TB/s;
-// one request over 131072 keys in 0.093 ms, 5.8 TB/s, of which the start and the joining take 10 us.
-// The ring's 160 KiB (heads of 128) cover DRAM's latency at the 45 GB/s that an SM gets of its bandwidth.
+// tokens x 16 heads in 0.086 ms by itself, 0.093 to 0.10 ms behind hot calls.  Decode: DRAM, 256 requests with
+// 2.2 GB of keys and values in 0.346 to 0.349 ms, 6.4 TB/s; one request over 131072 keys in 0.093 ms, 5.8 TB/s, of
+// which the start and the joining take 10 us.  The ring's 160 KiB (heads of 128) cover DRAM's latency at the 45 GB/s
+// that an SM gets of its bandwidth.  Decode with heads of 64 (a ring of 128 KiB): 256 requests, 16 heads over 8, with
+// 1.1 GB in 0.208 ms, 5.3 TB/s.
 //
 // Every wait is bounded; a timeout records KDA_ERR_DEVICE_TIMEOUT and all roles stop.
 #include "attn.h"

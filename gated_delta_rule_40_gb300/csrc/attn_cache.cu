@@ -166,8 +166,8 @@ cudaError_t launch_page_plan(const int32_t *cached, const int32_t *fresh, const 
 // A row of one (token, head) is D bf16 = D / 8 units of 16 bytes; a thread moves one unit of k and the same
 // one of v.  Neighbouring threads take neighbouring units, so loads are whole lines and stores whole rows of
 // 128 or 256 bytes at the slot's place in each head.  DRAM is the bound: both loads go out before either
-// store (32768 tokens x 8 heads of 128: 43.0 us, 6.24 TB/s, against 45.6 us with each store behind its own
-// load; two or four units a thread cost 46.5 and 52.9 us, as a warp's accesses then skip lines).  The new
+// store (32768 tokens x 8 heads of 128: 43.0 us on the GPU, 6.24 TB/s, a call 45 us; 45.6 us on the GPU with each
+// store behind its own load; two or four units a thread 46.5 and 52.9 us, as a warp's accesses then skip lines).  The new
 // keys and values are read once (streaming loads); the cache's lines stay, as attention reads them next.
 __global__ __launch_bounds__(256) void kv_write_kernel(const uint4 *k, const uint4 *v, const int32_t *slots,
                                                        uint4 *k_cache, uint4 *v_cache, long long units, int per_token,
