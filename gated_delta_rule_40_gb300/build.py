@@ -36,7 +36,8 @@ def _sources():
 
 
 def _deps():
-    headers = [f for d in (CSRC, os.path.join(ROOT, "include")) for x in ("*.cuh", "*.h") for f in glob.glob(os.path.join(d, x))]
+    include = os.path.join(ROOT, "include")
+    headers = [f for d in (CSRC, include) for x in ("*.cuh", "*.h") for f in glob.glob(os.path.join(d, x))]
     return _sources() + headers + [os.path.abspath(__file__)]
 
 
