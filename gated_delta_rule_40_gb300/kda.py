@@ -99,6 +99,26 @@ def load() -> ctypes.CDLL:
     lib.kda_attn_paged_ws.restype = I
     lib.kda_attn_workspace_size.argtypes = [I]
     lib.kda_attn_workspace_size.restype = Z
+    S = ctypes.c_int64
+    rope_args = [P, P, S, S, P, P, F, I, P, I, I, P, I, I, I, I]
+    lib.kda_qk_norm_rope.argtypes = rope_args + [P, P, P]
+    lib.kda_qk_norm_rope.restype = I
+    lib.kda_qk_norm_rope_bwd.argtypes = rope_args + [P] * 6 + [P]
+    lib.kda_qk_norm_rope_bwd.restype = I
+    lib.kda_qk_norm_rope_bwd_ws.argtypes = rope_args + [P] * 6 + [P, Z, P]
+    lib.kda_qk_norm_rope_bwd_ws.restype = I
+    lib.kda_qk_norm_rope_bwd_workspace_size.argtypes = [I]
+    lib.kda_qk_norm_rope_bwd_workspace_size.restype = Z
+    lib.kda_kv_write_q4.argtypes = [P, P, S, S, P, P, P] + [I] * 5 + [P]
+    lib.kda_kv_write_q4.restype = I
+    lib.kda_kv_read_q4.argtypes = [P] * 5 + [I] * 5 + [P]
+    lib.kda_kv_read_q4.restype = I
+    lib.kda_attn_paged_q4.argtypes = paged_args + [P]
+    lib.kda_attn_paged_q4.restype = I
+    lib.kda_attn_paged_q4_ws.argtypes = paged_args + [P, Z, P]
+    lib.kda_attn_paged_q4_ws.restype = I
+    lib.kda_attn_q4_workspace_size.argtypes = [I]
+    lib.kda_attn_q4_workspace_size.restype = Z
     lib.kda_status_string.argtypes = [I]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_get_status.argtypes = [P]
@@ -624,8 +644,9 @@ def kda_attn_workspace_size(D: int = 128) -> int:
     return int(load().kda_attn_workspace_size(D))
 
 
-def _attend(call, call_ws, name: str, args, q, heads, out, lse, return_lse: bool, workspace, stream, dev: int):
-    """Outputs, workspace and call of kda_attn_fwd / kda_attn_paged.  The workspace comes from the library's pool
+def _attend(call, call_ws, name: str, args, q, heads, out, lse, return_lse: bool, workspace, stream, dev: int,
+            workspace_size=kda_attn_workspace_size):
+    """Outputs, workspace and call of kda_attn_fwd / kda_attn_paged(_q4).  The workspace comes from the library's pool
     (on any stream; 4 us less than an allocation of torch's), under stream capture from torch, whose graphs keep
     their memory."""
     if out is None:
@@ -642,7 +663,7 @@ def _attend(call, call_ws, name: str, args, q, heads, out, lse, return_lse: bool
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8)
     elif stream is None and torch._C._cuda_isCurrentStreamCapturing():
-        workspace = torch.empty(kda_attn_workspace_size(q.shape[-1]), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(workspace_size(q.shape[-1]), dtype=torch.uint8, device=q.device)
     if workspace is None:
         rc = call(*args, p_out, p_lse, _raw_stream(stream, dev))
     else:
@@ -692,3 +713,172 @@ def kda_attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale
             _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,), dev), N, T, H_q, H_kv, D, nb, bs, width)
     return _attend(lib.kda_attn_paged, lib.kda_attn_paged_ws, "kda_attn_paged", args, q, (T, H_q), out, lse, return_lse,
                    workspace, stream, dev)
+
+
+def _rows_arg(t, name: str, shape, device: int):
+    """Address and stride between tokens of a bf16 tensor [T,H,D] whose tokens' rows are contiguous (a slice of a
+    fused projection's heads, or a contiguous tensor)."""
+    T, H, D = shape
+    if t is None or t.dtype is not torch.bfloat16 or t.get_device() != device or t.shape != shape:
+        _check(t, name, torch.bfloat16)   # (a strided tensor that is wrong in another way is reported as not contiguous)
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.numel() == 0:
+        return t.data_ptr(), H * D
+    step, head, one = t.stride()
+    if one != 1 or (H > 1 and head != D) or (T > 1 and (step < H * D or step % 8)):
+        raise ValueError(f"{name} must have contiguous heads, and tokens a multiple of 8 elements apart; strides "
+                         f"are {t.stride()}")
+    return t.data_ptr(), step if T > 1 else H * D
+
+
+def _weight_arg(w, name: str, D: int, norm: bool, device: int):
+    if w is None:
+        return None
+    if not norm:
+        raise ValueError(f"{name} needs norm=True")
+    return _arg(w, name, torch.float32, (D,), device)
+
+
+def kda_qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
+                     interleaved: bool = False, q_out=None, k_out=None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Norms of queries and keys for each head, and their rotation by position, in one pass.  Shapes: q [T,H_q,D],
+    k [T,H_kv,D] (bf16, D 64 or 128; slices of a fused projection's heads are taken as they are); positions [T]
+    int32 (kda_page_plan's; rows of a token with a negative one are not written); freqs [R/2] fp32, radians a
+    token, for the first R channels (a multiple of 8, 0 for none); q_weight, k_weight [D] fp32 or None for ones.
+    Pairs are (i, i + R/2), with ``interleaved`` (2i, 2i + 1).  Without ``norm`` only the rotation.  Returns
+    contiguous (q_out, k_out), which may be q and k where those are contiguous."""
+    lib = _lib or load()
+    bf, dev = torch.bfloat16, _device_of(q)
+    T, H_q, D = q.shape
+    H_kv = k.shape[1]
+    pq, sq = _rows_arg(q, "q", (T, H_q, D), dev)
+    pk, sk = _rows_arg(k, "k", (T, H_kv, D), dev)
+    half = freqs.shape[0]
+    args = (pq, pk, sq, sk, _weight_arg(q_weight, "q_weight", D, norm, dev),
+            _weight_arg(k_weight, "k_weight", D, norm, dev), eps, 1 if norm else 0,
+            _arg(freqs, "freqs", torch.float32, (half,), dev), 2 * half, 1 if interleaved else 0,
+            _arg(positions, "positions", torch.int32, (T,), dev), T, H_q, H_kv, D)
+    if q_out is None:
+        q_out = _new((T, H_q, D), bf, q.device, stream)
+    if k_out is None:
+        k_out = _new((T, H_kv, D), bf, q.device, stream)
+    rc = lib.kda_qk_norm_rope(*args, _arg(q_out, "q_out", bf, (T, H_q, D), dev),
+                              _arg(k_out, "k_out", bf, (T, H_kv, D), dev), _raw_stream(stream, dev))
+    if rc:
+        _raise(rc, "kda_qk_norm_rope")
+    return q_out, k_out
+
+
+def kda_qk_norm_rope_bwd_workspace_size(D: int = 128) -> int:
+    return int(load().kda_qk_norm_rope_bwd_workspace_size(D))
+
+
+def kda_qk_norm_rope_bwd(q, k, positions, freqs, dq_out, dk_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+                         norm: bool = True, interleaved: bool = False, workspace=None, stream=None) -> dict:
+    """Backward of ``kda_qk_norm_rope`` for dq_out, dk_out (bf16, shapes of q_out and k_out): fp32 gradients
+    ``dq`` [T,H_q,D], ``dk`` [T,H_kv,D] (rows of tokens with a negative position are not written), ``dq_weight`` and
+    ``dk_weight`` [D] (None where that weight is None).  ``workspace`` uint8
+    (kda_qk_norm_rope_bwd_workspace_size(D) bytes) or None."""
+    lib = _lib or load()
+    bf, f32, dev = torch.bfloat16, torch.float32, _device_of(q)
+    T, H_q, D = q.shape
+    H_kv = k.shape[1]
+    pq, sq = _rows_arg(q, "q", (T, H_q, D), dev)
+    pk, sk = _rows_arg(k, "k", (T, H_kv, D), dev)
+    half = freqs.shape[0]
+    args = (pq, pk, sq, sk, _weight_arg(q_weight, "q_weight", D, norm, dev),
+            _weight_arg(k_weight, "k_weight", D, norm, dev), eps, 1 if norm else 0,
+            _arg(freqs, "freqs", f32, (half,), dev), 2 * half, 1 if interleaved else 0,
+            _arg(positions, "positions", torch.int32, (T,), dev), T, H_q, H_kv, D,
+            _arg(dq_out, "dq_out", bf, (T, H_q, D), dev), _arg(dk_out, "dk_out", bf, (T, H_kv, D), dev))
+    at = q.device
+    g = {"dq": _new((T, H_q, D), f32, at, stream), "dk": _new((T, H_kv, D), f32, at, stream),
+         "dq_weight": None if q_weight is None else _new((D,), f32, at, stream),
+         "dk_weight": None if k_weight is None else _new((D,), f32, at, stream)}
+    if workspace is None and (q_weight is not None or k_weight is not None):
+        workspace = _new((kda_qk_norm_rope_bwd_workspace_size(D),), torch.uint8, at, stream)
+    size = 0
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8)
+        size = workspace.numel()
+    rc = lib.kda_qk_norm_rope_bwd_ws(*args, *(None if x is None else x.data_ptr() for x in g.values()),
+                                     None if workspace is None else workspace.data_ptr(), size, _raw_stream(stream, dev))
+    if rc:
+        _raise(rc, "kda_qk_norm_rope_bwd_ws")
+    return g
+
+
+def q4_row_bytes(D: int) -> int:
+    """Bytes of a row of D channels in a 4-bit cache, whose shape is [num_blocks,H_kv,block_size,q4_row_bytes(D)]."""
+    return D // 2 + D // 32
+
+
+def _q4_dim(cache, name: str) -> int:
+    """The head dimension of a 4-bit cache."""
+    D = {q4_row_bytes(d): d for d in (64, 128)}.get(cache.shape[-1])
+    if D is None:
+        raise ValueError(f"{name} has rows of {cache.shape[-1]} bytes, expected {q4_row_bytes(64)} (D = 64) or "
+                         f"{q4_row_bytes(128)} (D = 128)")
+    return D
+
+
+def kda_kv_write_q4(k, v, slots, k_cache, v_cache, stream=None) -> None:
+    """``kda_kv_write`` into caches held in 4 bits, [num_blocks,H_kv,block_size,q4_row_bytes(D)] uint8: k, v
+    [T,H_kv,D] (bf16; slices of a fused projection's heads are taken as they are) are rounded to the format of
+    include/kda.h and stored at ``slots`` [T] (int32; a negative one is left out)."""
+    lib = _lib or load()
+    u8, dev = torch.uint8, _device_of(k)
+    T, H_kv, D = k.shape
+    nb, _, bs, _ = k_cache.shape
+    pk, sk = _rows_arg(k, "k", (T, H_kv, D), dev)
+    pv, sv = _rows_arg(v, "v", (T, H_kv, D), dev)
+    row = q4_row_bytes(D)
+    rc = lib.kda_kv_write_q4(pk, pv, sk, sv, _arg(slots, "slots", torch.int32, (T,), dev),
+                             _arg(k_cache, "k_cache", u8, (nb, H_kv, bs, row), dev),
+                             _arg(v_cache, "v_cache", u8, (nb, H_kv, bs, row), dev), T, H_kv, D, nb, bs,
+                             _raw_stream(stream, dev))
+    if rc:
+        _raise(rc, "kda_kv_write_q4")
+
+
+def kda_kv_read_q4(k_cache, v_cache, slots, k=None, v=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The values that rows ``slots`` [T] (int32) of 4-bit caches stand for: k, v [T,H_kv,D] bf16, zeros where a
+    slot is negative."""
+    lib = _lib or load()
+    bf, u8, dev = torch.bfloat16, torch.uint8, _device_of(k_cache)
+    nb, H_kv, bs, row = k_cache.shape
+    T, D = slots.shape[0], _q4_dim(k_cache, "k_cache")
+    args = (_arg(k_cache, "k_cache", u8, (nb, H_kv, bs, row), dev), _arg(v_cache, "v_cache", u8, (nb, H_kv, bs, row), dev),
+            _arg(slots, "slots", torch.int32, (T,), dev))
+    if k is None:
+        k = _new((T, H_kv, D), bf, k_cache.device, stream)
+    if v is None:
+        v = _new((T, H_kv, D), bf, k_cache.device, stream)
+    rc = lib.kda_kv_read_q4(*args, _arg(k, "k", bf, (T, H_kv, D), dev), _arg(v, "v", bf, (T, H_kv, D), dev), T, H_kv, D, nb,
+                            bs, _raw_stream(stream, dev))
+    if rc:
+        _raise(rc, "kda_kv_read_q4")
+    return k, v
+
+
+def kda_attn_q4_workspace_size(D: int = 128) -> int:
+    return int(load().kda_attn_q4_workspace_size(D))
+
+
+def kda_attn_paged_q4(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, scale: float, out=None, lse=None,
+                      return_lse: bool = True, workspace=None,
+                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``kda_attn_paged`` over caches held in 4 bits, [num_blocks,H_kv,block_size,q4_row_bytes(D)] uint8;
+    workspace uint8 (kda_attn_q4_workspace_size(D) bytes) or None."""
+    lib = _lib or load()
+    u8, i32, dev = torch.uint8, torch.int32, _device_of(q)
+    T, H_q, D = q.shape
+    nb, H_kv, bs, _ = k_cache.shape
+    N, width, row = seq_lens.shape[0], block_table.shape[-1], q4_row_bytes(D)
+    args = (_arg(q, "q", torch.bfloat16, (T, H_q, D), dev), _arg(k_cache, "k_cache", u8, (nb, H_kv, bs, row), dev),
+            _arg(v_cache, "v_cache", u8, (nb, H_kv, bs, row), dev), scale,
+            _arg(block_table, "block_table", i32, (N, width), dev), _arg(seq_lens, "seq_lens", i32, (N,), dev),
+            _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,), dev), N, T, H_q, H_kv, D, nb, bs, width)
+    return _attend(lib.kda_attn_paged_q4, lib.kda_attn_paged_q4_ws, "kda_attn_paged_q4", args, q, (T, H_q), out, lse,
+                   return_lse, workspace, stream, dev, kda_attn_q4_workspace_size)

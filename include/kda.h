@@ -1,7 +1,7 @@
 /*
  * libkda: Kimi Delta Attention (KDA) forward and single-token decode on
  * NVIDIA GB300 (sm_103a), with lightning attention, and softmax attention over
- * prompts and a paged cache for the layers between them.
+ * prompts and a paged cache (bf16, or held in 4 bits) for the layers between them.
  *
  * KDA is a gated delta-rule linear attention with a per-channel decay.  Per
  * sequence and value head h, with state S (V x K, fp32, S[v][k]):
@@ -442,6 +442,108 @@ int kda_attn_paged_ws(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_
                       const int32_t *cu_seqlens, int N, int T, int H_q, int H_kv, int D,
                       int num_blocks, int block_size, int max_blocks, kda_bf16_t *out, float *lse,
                       void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Norms of queries and keys for each head, and the rotation by position, in one pass: what stands between
+ * a softmax layer's projection and kda_kv_write / kda_attn_*.  For each row x of D channels, with a the
+ * position times freqs[i] for pair i of the first rot_dim channels:
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (norm = 0: y = x, without weights)
+ *   out[p] = y[p] cos a - y[p'] sin a,  out[p'] = y[p] sin a + y[p'] cos a
+ *
+ * Pair i is (p, p') = (i, i + rot_dim / 2), or (2i, 2i + 1) where interleaved is not 0.  Channels from rot_dim
+ * on are not turned.
+ *
+ *   q, k          [T, H_q, D], [T, H_kv, D] bf16, rows of a token contiguous, tokens q_stride and k_stride
+ *                 elements apart (slices of a fused projection need no copy); strides are multiples of 8
+ *   q_weight, k_weight  [D] fp32, or NULL for ones
+ *   freqs         [rot_dim / 2] fp32, radians a token, below 2^24 in magnitude (others turn by NaN);
+ *                 NULL for rot_dim = 0
+ *   positions     [T] int32 (kda_page_plan's); a token with a negative one is left out: its rows of the
+ *                 outputs are not written
+ *   q_out, k_out  [T, H_q, D], [T, H_kv, D] bf16, contiguous; may be q and k themselves where those are
+ *                 contiguous, and must not overlap the inputs otherwise
+ *
+ * D is 64 or 128, rot_dim a multiple of 8 from 0 to D (KDA_ERR_UNSUPPORTED otherwise); eps is not negative.
+ * Statistics, angles and products are fp32 or better (the angle is exact to 2^-31 of a turn before its cosine, at
+ * any position), rounded once to bf16.  Tensors must be 16-byte aligned, weights, freqs and positions 4-byte.
+ */
+int kda_qk_norm_rope(const kda_bf16_t *q, const kda_bf16_t *k, int64_t q_stride, int64_t k_stride,
+                     const float *q_weight, const float *k_weight, float eps, int norm, const float *freqs,
+                     int rot_dim, int interleaved, const int32_t *positions, int T, int H_q, int H_kv, int D,
+                     kda_bf16_t *q_out, kda_bf16_t *k_out, cudaStream_t stream);
+
+/*
+ * Backward of kda_qk_norm_rope: inputs as there, and
+ *
+ *   dq_out, dk_out        [T, H_q, D], [T, H_kv, D] bf16, contiguous: dL/dq_out, dL/dk_out
+ *   dq, dk                [T, H_q, D], [T, H_kv, D] fp32, contiguous; rows of tokens left out are not written
+ *   dq_weight, dk_weight  [D] fp32, or NULL: summed over the tokens that are not left out (zeros for none), in a
+ *                         fixed order, so that bits repeat; also where the weight itself is NULL (ones);
+ *                         both NULL for norm = 0, where q and k are not read and may be NULL
+ *
+ * The workspace, for the weights' partial sums, comes from the library's pool, or from the caller
+ * (kda_qk_norm_rope_bwd_ws: kda_qk_norm_rope_bwd_workspace_size(D) bytes, on the terms of kda_fwd_ws; NULL will do
+ * where both weight gradients are NULL).
+ */
+int kda_qk_norm_rope_bwd(const kda_bf16_t *q, const kda_bf16_t *k, int64_t q_stride, int64_t k_stride,
+                         const float *q_weight, const float *k_weight, float eps, int norm, const float *freqs,
+                         int rot_dim, int interleaved, const int32_t *positions, int T, int H_q, int H_kv, int D,
+                         const kda_bf16_t *dq_out, const kda_bf16_t *dk_out, float *dq, float *dk,
+                         float *dq_weight, float *dk_weight, cudaStream_t stream);
+size_t kda_qk_norm_rope_bwd_workspace_size(int D);
+int kda_qk_norm_rope_bwd_ws(const kda_bf16_t *q, const kda_bf16_t *k, int64_t q_stride, int64_t k_stride,
+                            const float *q_weight, const float *k_weight, float eps, int norm,
+                            const float *freqs, int rot_dim, int interleaved, const int32_t *positions, int T,
+                            int H_q, int H_kv, int D, const kda_bf16_t *dq_out, const kda_bf16_t *dk_out,
+                            float *dq, float *dk, float *dq_weight, float *dk_weight, void *ws,
+                            size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The paged cache held in 4 bits: 4.25 bits a channel instead of 16.  Layout of slots, blocks and tables as
+ * above; k_cache and v_cache are [num_blocks, H_kv, block_size, KDA_Q4_ROW_BYTES(D)] bytes.
+ *
+ * 32 channels share a scale byte b for s = 2^((b >> 3) - 15) (1 + (b & 7) / 8), from 2^-15 to 1.875 2^16: the
+ * smallest whose sevenfold reaches the largest magnitude among them (the largest there is, where none does).
+ * A channel is a code c = 8 + n of 4 bits for the value n s, n = -7 .. 7 nearest to x / s, halves away from zero
+ * (an infinity gives 7 or -7 of the largest scale, a NaN 0).  Every such value is a bf16 number.  A (block, kv head)
+ * holds D / 2 bytes of codes for each row, then D / 32 scale bytes for each row; the 32-bit word of 8
+ * channels has channel 2j in bits 4j .. 4j + 3 and channel 2j + 1 in bits 16 + 4j .. 19 + 4j.
+ */
+#define KDA_Q4_ROW_BYTES(D) ((D) / 2 + (D) / 32)
+
+/*
+ * kda_kv_write into such a cache: rounds the keys and values of T tokens to the format and stores them.
+ * k and v [T, H_kv, D] bf16 may have tokens k_stride and v_stride elements apart (multiples of 8), slots as
+ * kda_kv_write.
+ */
+int kda_kv_write_q4(const kda_bf16_t *k, const kda_bf16_t *v, int64_t k_stride, int64_t v_stride,
+                    const int32_t *slots, uint8_t *k_cache, uint8_t *v_cache, int T, int H_kv, int D,
+                    int num_blocks, int block_size, cudaStream_t stream);
+
+/*
+ * Reads T rows of the cache back: k, v [T, H_kv, D] bf16 become the values that the rows at slots [T] stand
+ * for.  A negative slot gives zeros; one outside the cache too, with KDA_ERR_BAD_PAGES in the status word.
+ */
+int kda_kv_read_q4(const uint8_t *k_cache, const uint8_t *v_cache, const int32_t *slots, kda_bf16_t *k,
+                   kda_bf16_t *v, int T, int H_kv, int D, int num_blocks, int block_size,
+                   cudaStream_t stream);
+
+/*
+ * kda_attn_paged over such a cache: the attention of q over the values that the cache stands for, with the same
+ * arguments, masks, precision and errors.
+ */
+int kda_attn_paged_q4(const kda_bf16_t *q, const uint8_t *k_cache, const uint8_t *v_cache, float scale,
+                      const int32_t *block_table, const int32_t *seq_lens, const int32_t *cu_seqlens, int N,
+                      int T, int H_q, int H_kv, int D, int num_blocks, int block_size, int max_blocks,
+                      kda_bf16_t *out, float *lse, cudaStream_t stream);
+/* ... with a workspace of at least kda_attn_q4_workspace_size(D) bytes, on the terms of kda_fwd_ws. */
+size_t kda_attn_q4_workspace_size(int D);
+int kda_attn_paged_q4_ws(const kda_bf16_t *q, const uint8_t *k_cache, const uint8_t *v_cache, float scale,
+                         const int32_t *block_table, const int32_t *seq_lens, const int32_t *cu_seqlens,
+                         int N, int T, int H_q, int H_kv, int D, int num_blocks, int block_size,
+                         int max_blocks, kda_bf16_t *out, float *lse, void *ws, size_t ws_bytes,
+                         cudaStream_t stream);
 
 /* Self-test of the device-side failure path: queues one tiny kernel whose bounded
  * wait on a barrier that nothing completes gives up, recording
