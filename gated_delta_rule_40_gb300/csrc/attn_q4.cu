@@ -3,7 +3,12 @@
 #include "q4.cuh"
 
 namespace kda {
+size_t attn_q4_few_workspace_bytes(int D);
+cudaError_t launch_attn_q4_few(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches);
+
 namespace {
+// Rows (new tokens x query heads of a group) of a request up to which the kernel for few rows takes it
+constexpr int F4_MOST_ROWS = 32;
 
 template <int D>
 __global__ __launch_bounds__(256) void attn_q4_simple_kernel(const AttnQ4Args p) {
@@ -27,6 +32,7 @@ __global__ __launch_bounds__(256) void attn_q4_simple_kernel(const AttnQ4Args p)
         if (p.cu[mid] <= t) lo = mid;
         else hi = mid;
     }
+    if ((long long)(p.cu[lo + 1] - p.cu[lo]) * (p.H_q / p.H_kv) <= F4_MOST_ROWS) return;   // the other kernel's
     const int limit = p.lens[lo] - (p.cu[lo + 1] - (int)t) + 1;   // keys seen
     const size_t row = (size_t)t * p.H_q + h;
     for (int d = lane; d < D; d += 32) s_q[warp][d] = bf16_to_f(p.q[row * D + d]) * p.scale;
@@ -86,12 +92,13 @@ __global__ __launch_bounds__(256) void attn_q4_simple_kernel(const AttnQ4Args p)
 }
 }  // namespace
 
-size_t attn_q4_workspace_bytes(int D) { return 256; }
+size_t attn_q4_workspace_bytes(int D) { return attn_q4_few_workspace_bytes(D); }
 
 cudaError_t launch_attn_q4(const AttnQ4Args &a, void *ws, cudaStream_t stream, int *launches) {
-    (void)ws;
+    cudaError_t e = launch_attn_q4_few(a, F4_MOST_ROWS, ws, stream, launches);
+    if (e != cudaSuccess || (long long)a.T * (a.H_q / a.H_kv) <= F4_MOST_ROWS) return e;
     const unsigned grid = (unsigned)(((long long)a.T * a.H_q + 7) / 8);
-    *launches = 1;
+    ++*launches;
     if (a.D == 64) attn_q4_simple_kernel<64><<<grid, 256, 0, stream>>>(a);
     else attn_q4_simple_kernel<128><<<grid, 256, 0, stream>>>(a);
     return cudaGetLastError();

@@ -67,12 +67,31 @@ def bf16_values(x):
 
 
 def reference(q, k, v, scale, first=0):
-    """A.reference, with room for underflow.  An exponential below 2^-126 of the largest may become 0, which takes
-    at most 2^-126 |v_j| from a sum of which the largest term's weight is 1: 2^-126 L max |v| over L keys.  It shows
-    where v is 0 in every key of weight, which values rounded to 4 bits often are.  bf16's smallest step is 2^-133."""
+    """A.reference, with room for what computing with the codes themselves adds:
+
+    * A channel of q is two e4m3 numbers, with the row's largest between 128 and 256: 8 bits, or 2^-10 absolute, which
+      is 2^-17 of the largest.  A score is off by e = scale 2^-17 max|q| sum|k|, a weight by a factor of 2 e more.
+    * The sums over codes c = 8 + n, less 8 times the sum of p s, are off by 2^-19 of 16 sum p s (chains of up to 32
+      fp32 additions, 2^-24 each).  A block's s is at most a sixth of its largest value (its largest n is 6 or 7, as
+      scales are 1.125 apart or less), or 2^-15 for a block of zeros.
+    * An exponential below 2^-126 of the largest may become 0, which takes at most 2^-126 |v_j| from a sum of which
+      the largest term's weight is 1: 2^-126 L max |v| over L keys.  It shows where v is 0 in every key of weight,
+      which values rounded to 4 bits often are.  bf16's smallest step is 2^-133."""
     o, l, to, tl = A.reference(q, k, v, scale, first)
-    tiny = 2.0 ** -126 * k.shape[0] * (float(v.double().abs().max()) if v.numel() else 0.0) + 2.0 ** -133
-    return o, l, to + tiny, tl
+    if k.shape[0] == 0:
+        return o, l, to, tl
+    q, k, v = q.double(), k.double(), v.double()
+    G = q.shape[1] // k.shape[1]
+    seen = torch.arange(k.shape[0])[None, :] <= first + torch.arange(q.shape[0])[:, None]
+    s = torch.einsum("ahd,lhd->ahl", q, k.repeat_interleave(G, 1)) * scale
+    p = torch.where(seen[:, None, :], torch.exp(s - torch.where(torch.isfinite(l), l, 0.0)[..., None]), 0.0)
+    sizes = torch.where(seen[:, None, :], k.abs().sum(-1).repeat_interleave(G, 1).T[None], 0.0).amax(-1)
+    e = scale * 2.0 ** -17 * q.abs().amax(-1) * sizes
+    steps = v.unflatten(-1, (-1, 32)).abs().amax(-1) / 6 + 2.0 ** -15
+    ps = torch.einsum("ahl,lhb->ahb", p, steps.repeat_interleave(G, 1)).repeat_interleave(32, -1)
+    sums = torch.einsum("ahl,lhd->ahd", p, v.abs().repeat_interleave(G, 1))
+    tiny = 2.0 ** -126 * k.shape[0] * float(v.abs().max()) + 2.0 ** -133
+    return o, l, to + torch.expm1(2 * e)[..., None] * sums + 2.0 ** -19 * 16 * ps + tiny, tl + e
 
 
 class PagedQ4(A.Paged):
