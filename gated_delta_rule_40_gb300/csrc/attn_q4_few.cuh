@@ -2,7 +2,6 @@
 #pragma once
 
 #include "attn_q4.h"
-#include "kda_tma.cuh"
 #include "q4.cuh"
 
 namespace kda {
@@ -17,26 +16,20 @@ constexpr float F4_MOST = 65536.0f;    // sum of a lane's weights that makes a w
 // Rows a unit has at most, and how a CTA is made for them
 template <int D, int ROWS>
 struct F4Layout {
-    static constexpr int WARPS = ROWS == 16 ? 7 : 15;           // that attend; one more loads
-    static constexpr int THREADS = 32 * (WARPS + 1);
-    static constexpr int STAGES = ROWS == 16 ? 4 : 2;                             // a warp's ring
-    static constexpr int TILES = ROWS / 4;                        // score tiles: 4 queries, each a high and a low column
-    static constexpr int QT = (ROWS + 7) / 8;                     // output tiles of 8 columns
+    static constexpr int WARPS = ROWS == 16 ? 8 : 12;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int STAGES = ROWS == 16 ? 4 : 3;             // a warp's ring of chunks
+    static constexpr int TILES = ROWS / 8;                        // of 8 queries, the columns of a product
+    // A chunk: codes of keys and values, then their scales
     static constexpr uint32_t CODES = F4_KEYS * (D / 2), SCALES = F4_KEYS * (D / 32);
-    static constexpr uint32_t STAGE = 2 * CODES;                  // of codes: keys, then values
-    static constexpr uint32_t RING = WARPS * STAGES * STAGE;
-    static constexpr uint32_t SC = RING, SC_STAGE = 2 * SCALES;
-    static constexpr uint32_t PART = SC + WARPS * STAGES * SC_STAGE;   // partial outputs [buffer][warp][row][D] fp32
-    static constexpr int BUFS = ROWS == 4 ? 2 : 1;
-    static constexpr uint32_t PART_ROW = D * 4;
-    static constexpr uint32_t PART_WARP = ROWS * PART_ROW;
-    static constexpr uint32_t ML = PART + BUFS * WARPS * PART_WARP;    // [buffer][warp][row] reference, sum
-    static constexpr uint32_t BAR = ML + BUFS * WARPS * ROWS * 8;
-    // barriers: chunk loaded / free [warp][stage], partial outputs written / read [buffer]
-    enum { FULL = 0, EMPTY = FULL + WARPS * STAGES, PF = EMPTY + WARPS * STAGES, PE = PF + BUFS, COUNT = PE + BUFS };
-    static constexpr uint32_t BADS = BAR + 8 * COUNT;             // [warp][stage] halves of a chunk without a block
-    static constexpr uint32_t FLAG = BADS + 4 * WARPS * STAGES;
-    static constexpr uint32_t BYTES = FLAG + 16 + 1024;
+    static constexpr uint32_t STAGE = 2 * (CODES + SCALES);
+    static constexpr uint32_t RING = STAGES * STAGE;              // of a warp
+    // Partial outputs [row][D] fp32: of the unit that a warp's share begins in; the one it ends in takes the ring's place
+    static constexpr uint32_t PART = WARPS * RING;
+    static constexpr uint32_t PART_ROW = D * 4, PART_WARP = ROWS * PART_ROW;
+    static constexpr uint32_t ML = PART + WARPS * PART_WARP;      // [warp][begin, end][row] reference, sum
+    static constexpr uint32_t BYTES = ML + WARPS * 2 * ROWS * 8 + 128;
+    static_assert(PART_WARP <= RING, "a partial output in the ring's place");
     static_assert(BYTES <= 232448, "few-row attention shared memory");
 };
 
@@ -53,6 +46,9 @@ struct F4Params {
     int G;
     int most_rows;    // requests with more rows are another kernel's
     int unit_cost;    // of a unit, in chunks
+    // Constants that the compiler does not know: a product with a power of two stays one (the multiplier has room, the
+    // shifter has not), and a mask with a leading bit stays one instruction.
+    uint32_t two20, two4, low, low_bit, high, high_bit;
 };
 
 // One request's units
@@ -79,7 +75,7 @@ struct F4Request {
     }
 };
 
-// The pieces of units in a CTA's share
+// The pieces of units in a warp's share
 struct F4Walk {
     F4Request r;
     int n, hk, unit, at;
@@ -115,36 +111,30 @@ struct F4Walk {
     }
 };
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2], float c0) {
-    asm(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};\n"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(0.f));
-}
+// What a warp has of a unit that its share cuts
+struct F4Part {
+    int n, hk, first, rows;
+    bool there, ends;   // whether there is one, whether it holds the unit's last chunk
+    long long rest;     // of the unit's line behind it
+};
+
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         const uint32_t (&b)[2]) {
+                                         uint32_t b0, uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
     return y;
 }
-// Two numbers as e4m3, the first in the low byte
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    uint16_t y;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(y) : "f"(hi), "f"(lo));
+// (x & mask) | bit
+__device__ __forceinline__ uint32_t masked(uint32_t x, uint32_t mask, uint32_t bit) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(y) : "r"(x), "r"(mask), "r"(bit));
     return y;
-}
-__device__ __forceinline__ float2 e4m3x2_to_f(uint32_t x) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)x));
-    float lo, hi;
-    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.f32.f16 %0, a;\ncvt.f32.f16 %1, b;\n}\n" : "=f"(lo), "=f"(hi) : "r"(h));
-    return make_float2(lo, hi);
 }
 
 }  // namespace kda
