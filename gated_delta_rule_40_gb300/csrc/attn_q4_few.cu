@@ -6,7 +6,7 @@ namespace {
 
 // Row of out and lse that is row `flat` of a request's rows of one head's group
 __device__ __forceinline__ size_t out_row(const F4Params &p, const F4Request &r, int hk, int flat) {
-    const int tok = flat / p.G;
+    const int tok = f4_token(p, flat);
     return (size_t)(r.row0 + tok) * p.a.H_q + hk * p.G + (flat - tok * p.G);
 }
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
@@ -204,10 +204,13 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
         cp_async_commit();
     };
     look_up();
+#pragma unroll
     for (int i = 0; i < S - 1; ++i) {
         load(ring + i * L::STAGE);
         look_up();
     }
+    uint32_t to = (S - 1) * L::STAGE, at = 0;   // places in the ring of the next chunk to load, to work on
+    auto advance = [](uint32_t &place) { place = place == L::RING - L::STAGE ? 0 : place + L::STAGE; };
 
     // ---- attention
     {
@@ -229,7 +232,6 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
         const uint32_t blk = D == 128 ? g >> 1 : g >> 2, second = D == 128 ? 4 + blk : 2 + blk;
         const uint32_t sel = odd ? second | blk << 8 : blk | second << 8;
 
-        uint32_t k_use = 0;   // chunks of this warp so far
         while (w.next(p, ROWS)) {
             {
                 // ---- queries: columns g of the products.  A lane's channels are those of its words of a key, 8 in each block
@@ -256,7 +258,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     }
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
-                        limit[n][x] = w.r.keys - w.r.fresh + min(w.first + 8 * n + 2 * t + x, w.first + w.rows - 1) / p.G + 1;
+                        limit[n][x] = w.r.keys - w.r.fresh + f4_token(p, min(w.first + 8 * n + 2 * t + x, w.first + w.rows - 1)) + 1;
                     m[n] = make_float2(-INFINITY, -INFINITY);
                     l[n] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -266,15 +268,17 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                         for (int i = 0; i < MT; ++i) o[i][n][x] = 0.f;
                     }
                 }
-                const int lowest = w.r.keys - w.r.fresh + w.first / p.G + 1;   // of the rows' limits
+                const int lowest = w.r.keys - w.r.fresh + f4_token(p, w.first) + 1;   // of the rows' limits
 
-                for (int c = w.a; c < w.b; ++c, ++k_use) {
-                    load(ring + (k_use + S - 1) % S * L::STAGE);
+                for (int c = w.a; c < w.b; ++c) {
+                    load(ring + to);
+                    advance(to);
                     look_up();
                     cp_async_wait<S - 1>();
                     __syncwarp();
                     // plain loads, whose offsets go into the instructions
-                    const unsigned char *stage = sm + warp * L::RING + k_use % S * L::STAGE;
+                    const unsigned char *stage = sm + warp * L::RING + at;
+                    advance(at);
                     const unsigned char *k_scales = stage + 2 * L::CODES + (D == 128 ? kr : kr & ~1) * (D / 32);
                     const unsigned char *v_scales = stage + 2 * L::CODES + L::SCALES + 2 * t * (D / 32);
                     auto word = [](const unsigned char *at) { return *reinterpret_cast<const uint32_t *>(at); };
@@ -652,8 +656,9 @@ cudaError_t launch_attn_q4_few(const AttnQ4Args &a, int most_rows, void *ws, cud
     p.o = reinterpret_cast<float *>(base);
     p.c = a.scale * LOG2E;
     p.G = a.H_q / a.H_kv;
+    p.over_g = (65536u + p.G - 1) / p.G;
     p.most_rows = most_rows;
-    p.unit_cost = 2;
+    p.unit_cost = 2;   // 4000 cycles of a warp, whose chunks take 3100 (0, 1, 2, 4: 159, 143, 136, 140 us for 256 decoded tokens)
     p.two20 = 1u << 20;
     p.two4 = 1u << 4;
     p.low = 0x000f000fu; p.low_bit = 0x43004300u;     // codes in bits 0 .. 3: 128 + c

@@ -44,12 +44,16 @@ struct F4Params {
     float *o;         // [CTA][2][F4_MAX_ROWS][D]
     float c;          // scale log2(e)
     int G;
+    uint32_t over_g;  // 2^16 / G, rounded up: (row over_g) >> 16 is row / G for the rows of this kernel's requests
     int most_rows;    // requests with more rows are another kernel's
     int unit_cost;    // of a unit, in chunks
     // Constants that the compiler does not know: a product with a power of two stays one (the multiplier has room, the
     // shifter has not), and a mask with a leading bit stays one instruction.
     uint32_t two20, two4, low, low_bit, high, high_bit;
 };
+
+// Token of a request's row (exact: row < 512, G <= 128)
+__device__ __forceinline__ int f4_token(const F4Params &p, int row) { return (int)((uint32_t)row * p.over_g >> 16); }
 
 // One request's units
 struct F4Request {
@@ -63,7 +67,7 @@ struct F4Request {
         units = (rows + R - 1) / R;
     }
     // keys that the rows up to (not including) row `end` of the request see
-    __device__ int seen(const F4Params &p, int end) const { return keys - fresh + (min(end, rows) - 1) / p.G + 1; }
+    __device__ int seen(const F4Params &p, int end) const { return keys - fresh + f4_token(p, min(end, rows) - 1) + 1; }
     __device__ int chunks(const F4Params &p, int end) const {
         const int s = seen(p, end);
         return s > F4_KEYS ? (s + F4_KEYS - 1) / F4_KEYS : 1;
