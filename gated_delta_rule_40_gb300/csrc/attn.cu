@@ -52,6 +52,7 @@
 #include "attn.h"
 #include "kda_common.cuh"
 #include "kda_tma.cuh"
+#include "q4.cuh"
 
 namespace kda {
 
@@ -70,8 +71,13 @@ constexpr float AT_SLACK = 8.0f;             // log2 of how far a row's maximum 
                                              // looks at it
 constexpr float AT_MOST = 65536.0f;          // sum of a step's p that makes it look
 
-template <int D, bool PAGED>
+// Where the keys and values of a call are: rows of a prompt, pages of a bf16 cache, pages of a 4-bit cache
+enum { AT_PROMPT = 0, AT_PAGES = 1, AT_PAGES_Q4 = 2 };
+
+template <int D, int MODE>
 struct AttnLayout {
+    static constexpr bool PAGED = MODE == AT_PAGES;   // boxes of a page each
+    static constexpr int THREADS = MODE == AT_PAGES_Q4 ? AT_THREADS + 128 : AT_THREADS;
     static constexpr uint32_t TILE = AT_KEYS * D * 2;          // bytes of a query, key or value tile
     static constexpr int STAGES = D == 128 ? 5 : 8;            // key / value ring
     // A tile is made of 8-row x 64-channel swizzled blocks of 1 KiB.  A query tile, and a key or value tile of a
@@ -108,6 +114,7 @@ struct AttnParams {
     bool whole;       // out is aligned to 32 bytes
     int G, tile_tokens;   // query heads a key/value head, tokens a tile
     int unit_cost;    // of a unit with two query tiles, in key tiles
+    int few_tokens;   // requests with up to so many new tokens are another kernel's (0: none is)
 };
 
 // Sum of floor((a i + b) / m) over 0 <= i < n, a, m >= 1 (Euclid's descent on the lattice points under a
@@ -147,7 +154,7 @@ struct Request {
             fresh = keys = p.a.T;
         }
         const int w = p.tile_tokens * AT_TILES;
-        units = (fresh + w - 1) / w;
+        units = fresh <= p.few_tokens ? 0 : (fresh + w - 1) / w;
         cost = fresh > p.tile_tokens ? p.unit_cost : 0;
         least = fresh > p.tile_tokens ? AT_LEAST : 1;
     }
@@ -294,15 +301,23 @@ __device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w, boo
     }
 }
 
-template <int D, bool PAGED>
-__global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_constant__ CUtensorMap tq,
+// A pair of codes' words as bf16 (see q4.cuh): 16 bytes, 8 channels, of a word
+__device__ __forceinline__ uint4 q4_expand(uint32_t word, uint32_t s2, uint32_t minus24s2) {
+    return make_uint4(q4_value(q4_raw(word, 0), s2, minus24s2), q4_value(q4_raw(word, 1), s2, minus24s2),
+                      q4_value(q4_raw(word, 2), s2, minus24s2), q4_value(q4_raw(word, 3), s2, minus24s2));
+}
+
+template <int D, int MODE>
+__global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(const __grid_constant__ CUtensorMap tq,
                                                              const __grid_constant__ CUtensorMap tk,
                                                              const __grid_constant__ CUtensorMap tv,
                                                              const __grid_constant__ AttnParams p) {
-    using L = AttnLayout<D, PAGED>;
+    using L = AttnLayout<D, MODE>;
+    constexpr bool PAGED = L::PAGED, Q4 = MODE == AT_PAGES_Q4;
+    constexpr int THREADS = L::THREADS;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = aligned_smem<1024>(smem_raw);
-    __shared__ long long s_warp[AT_THREADS / 32], s_x, s_head, s_at;
+    __shared__ long long s_warp[THREADS / 32], s_x, s_head, s_at;
     __shared__ int s_n, s_unit;
     __shared__ Request s_req;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -315,10 +330,11 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     bool bad = false;
     if (tid == 0) {
         if (p.join) p.join[blockIdx.x].pieces = 0;
-        bad = p.a.cu && (p.a.cu[0] != 0 || (PAGED ? p.a.cu[p.a.N] > p.a.T : p.a.cu[p.a.N] != p.a.T));
+        bad = p.a.cu && (p.a.cu[0] != 0 || (MODE != AT_PROMPT ? p.a.cu[p.a.N] > p.a.T : p.a.cu[p.a.N] != p.a.T));
     } else if (tid == 32) {
         for (int i = 0; i < L::COUNT; ++i)
-            mbar_init(bar + 8 * i, i >= L::KE && i < L::VL ? 2 : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) ? 4 : 1);
+            mbar_init(bar + 8 * i, i >= L::KE && i < L::VL ? 2
+                                   : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) || (Q4 && i >= L::KF && i < L::KE) ? 4 : 1);
         mbar_fence_init();
         *abort_flag = 0;
         s_unit = 0;
@@ -339,7 +355,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         if (n < nseq) {
             mine_req.load(p, n);
             bool wrong = p.a.cu && p.a.cu[n + 1] < p.a.cu[n];
-            if (PAGED)
+            if (MODE != AT_PROMPT)
                 wrong |= mine_req.keys < 0 ||
                          mine_req.keys > min((long long)p.a.max_blocks << p.a.block_log2, AT_MAX_KEYS);
             bad |= wrong;
@@ -351,13 +367,13 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             const long long y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (nseq > AT_THREADS) __syncthreads();   // the last group's sums have been read
+        if (nseq > THREADS) __syncthreads();   // the last group's sums have been read
         if (lane == 31) s_warp[warp] = x;
         bad = __syncthreads_or(bad);
         long long sum = 0;
         before = x - mine;
 #pragma unroll
-        for (int w = 0; w < AT_THREADS / 32; ++w) {
+        for (int w = 0; w < THREADS / 32; ++w) {
             if (w < warp) before += s_warp[w];
             sum += s_warp[w];
         }
@@ -374,11 +390,11 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     bool found = false;
     for (int pass = 0; pass < 2 && !found; ++pass) {
         base = 0;
-        for (int n0 = 0; !found && (n0 < nseq || n0 == 0); n0 += AT_THREADS) {
+        for (int n0 = 0; !found && (n0 < nseq || n0 == 0); n0 += THREADS) {
             const long long sum = group(n0);
             if (pass == 0) {
                 total += sum;
-                if (n0 + AT_THREADS < nseq) continue;
+                if (n0 + THREADS < nseq) continue;
                 if (bad) {
                     if (tid == 0) set_status(KDA_ERR_BAD_SEQLENS);
                     leave();
@@ -391,7 +407,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
                     leave();
                     return;
                 }
-                if (nseq > AT_THREADS) break;
+                if (nseq > THREADS) break;
             }
             if (start < base + sum) {
                 found = true;
@@ -420,7 +436,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         long long x = s_x - hk * s_head;
         int unit = 0;
         if (r.units > 1) {
-            const int step = (r.units + AT_THREADS - 1) / AT_THREADS, u = min(tid * step, r.units - 1);
+            const int step = (r.units + THREADS - 1) / THREADS, u = min(tid * step, r.units - 1);
             const long long at = r.prefix(u, wt);
             if (at <= x) atomicMax(&s_unit, u);
             __syncthreads();
@@ -454,7 +470,88 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
         return ok = false;
     };
 
-    if (warp == AT_LOADER) {
+    if constexpr (Q4) {
+        // The softmax warps take registers over from the others: 256 threads of 168 and 256 of 88 are the launch's
+        // 512 of 128 (which the host checks).
+        if (warp < AT_ISSUER) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    }
+    if (Q4 && warp >= AT_THREADS / 32) {
+        // ------------------------------------------------------------ expander (4-bit pages)
+        // 4 warps write a tile's values as bf16, which they are, into the ring.  A lane takes 16 bytes of codes, 32
+        // channels under one scale, of row 8 i + lane % 8 of its warp's 32 rows: 8 lanes with neighbouring rows write
+        // to different banks.  Codes go from global memory to registers, a key or value tile ahead, block ids a tile
+        // ahead of those.  Rows past the unit's last key, and rows without a block, become zeros.
+        constexpr int PARTS = D / 32, ROWS_AT_ONCE = 32 / PARTS, TIMES = 32 / ROWS_AT_ONCE;   // 16-byte parts of a row
+        const int xw = warp - AT_THREADS / 32, part = lane / ROWS_AT_ONCE, r0 = xw * 32 + lane % ROWS_AT_ONCE;
+        const int bs = 1 << p.a.block_log2;
+        const uint8_t *caches[2] = {reinterpret_cast<const uint8_t *>(p.a.k), reinterpret_cast<const uint8_t *>(p.a.v)};
+        uint32_t kv = 0;
+        while (ok && w.next(p)) {
+            const int keys = w.keys(p);
+            // blocks of the warp's first and second 16 rows of tile t: -2 none to load
+            auto pages = [&](int t, int (&id)[2]) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int key = t * AT_KEYS + xw * 32 + 16 * h;
+                    id[h] = t < w.b && key < keys ? max(p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)], -1) : -2;
+                }
+            };
+            uint4 codes[TIMES];
+            uint32_t scale[TIMES];
+            auto fetch = [&](int t, int which, const int (&id)[2]) {
+#pragma unroll
+                for (int i = 0; i < TIMES; ++i) {
+                    const int key = t * AT_KEYS + r0 + ROWS_AT_ONCE * i, b = id[(ROWS_AT_ONCE * i) >> 4];
+                    codes[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                    scale[i] = 0;
+                    if (b != -2 && (uint32_t)b >= (uint32_t)p.a.num_blocks) set_status(KDA_ERR_BAD_PAGES);
+                    if (t < w.b && key < keys && (uint32_t)b < (uint32_t)p.a.num_blocks) {
+                        const size_t slab = (((size_t)b * p.a.H_kv + w.hk) << p.a.block_log2) * q4_row_bytes(D);
+                        const int row = key & (bs - 1);
+                        codes[i] = *reinterpret_cast<const uint4 *>(caches[which] + slab + (size_t)row * (D / 2) + 16 * part);
+                        scale[i] = caches[which][slab + ((size_t)(D / 2) << p.a.block_log2) + row * (D / 32) + part];
+                    }
+                }
+            };
+            int id[2], next_id[2];
+            pages(w.a, id);
+            fetch(w.a, 0, id);
+            for (int t = w.a; ok && t < w.b; ++t) {
+                pages(t + 1, next_id);
+#pragma unroll
+                for (int which = 0; which < 2; ++which, ++kv) {
+                    const uint32_t s = kv % L::STAGES, use = kv / L::STAGES;
+                    if (use > 0 && !wait(L::KE + s, (use - 1) & 1)) break;
+                    unsigned char *tile = sm + s * L::TILE + (part >> 1) * L::HALF;
+                    uint4 now[TIMES];
+                    uint32_t now_scale[TIMES];
+#pragma unroll
+                    for (int i = 0; i < TIMES; ++i) {
+                        now[i] = codes[i];
+                        now_scale[i] = scale[i];
+                    }
+                    if (which == 0) fetch(t, 1, id);
+                    else fetch(t + 1, 0, next_id);
+#pragma unroll
+                    for (int i = 0; i < TIMES; ++i) {
+                        const int row = r0 + ROWS_AT_ONCE * i;
+                        const uint32_t s2 = q4_scale2(now_scale[i] * 0x00010001u), o2 = q4_offset2(s2);
+                        const uint32_t word[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            *reinterpret_cast<uint4 *>(tile + (row >> 3) * 1024 + (row & 7) * 128 +
+                                                       ((((part & 1) * 4 + x) ^ (row & 7)) << 4)) = q4_expand(word[x], s2, o2);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar + 8 * (L::KF + s));
+                }
+                id[0] = next_id[0];
+                id[1] = next_id[1];
+            }
+        }
+    } else if (warp == AT_LOADER) {
         // ------------------------------------------------------------ loader
         uint32_t kv = 0, qu = 0;
         constexpr int HALVES = D / 64;
@@ -464,7 +561,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             const int keys = w.keys(p);
             // block id of this lane's box of tile t; looked at only when the tile is loaded, a tile later
             auto page = [&](int t) {
-                if (!PAGED) return 0;
+                if (!PAGED || Q4) return 0;
                 const int key = t * AT_KEYS + lane * box;
                 if (lane >= boxes || key >= keys || t >= w.b) return 0;
                 return p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)];
@@ -488,9 +585,9 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
             };
             // the first queries go out at once; later ones follow the piece's first key tile, so that they wait
             // for their slot under its load
-            const bool early = qu == 0;
+            const bool early = Q4 || qu == 0;
             if (early) queries();
-            for (int t = w.a; ok && t < w.b; ++t) {
+            for (int t = w.a; !Q4 && ok && t < w.b; ++t) {
                 const int next_id = page(t + 1);
                 if (PAGED && (id < 0 || id >= p.a.num_blocks)) {
                     set_status(KDA_ERR_BAD_PAGES);
@@ -520,7 +617,7 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attn_kernel(const __grid_consta
     } else if (warp == AT_CLEANER) {
         // ------------------------------------------------------------ cleaner
         uint32_t kv = 0, uses = 0;   // ring entries so far; per stage, the parity of its value tiles cleaned
-        while (ok && w.next(p)) {
+        while (!Q4 && ok && w.next(p)) {
             const int t = w.b - 1;
             kv += 2 * (uint32_t)(w.b - w.a);
             if (!w.dirty(p, t)) continue;
@@ -905,9 +1002,10 @@ cudaError_t tensor_map(CUtensorMap *m, const void *base, int n, const long long 
 
 size_t align256_at(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <int D, bool PAGED>
+template <int D, int MODE>
 cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
-    using L = AttnLayout<D, PAGED>;
+    using L = AttnLayout<D, MODE>;
+    constexpr bool PAGED = L::PAGED;
     const AttnArgs &a = p.a;
     const long long rows = (long long)a.B * a.T;
     CUtensorMap mq, mk, mv;
@@ -917,7 +1015,8 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
         const int box[3] = {64, p.G, p.tile_tokens};
         if ((e = tensor_map(&mq, a.q, 3, size, stride, box)) != cudaSuccess) return e;
     }
-    for (int i = 0; i < 2; ++i) {
+    mk = mv = mq;
+    for (int i = 0; i < 2 && MODE != AT_PAGES_Q4; ++i) {
         const void *base = i ? a.v : a.k;
         CUtensorMap *m = i ? &mv : &mk;
         if (PAGED) {   // (64 channels, 8 rows, channel halves, groups of 8 rows in a block, block and head)
@@ -937,14 +1036,19 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     static bool ready[64] = {false};   // by device: the attributes are set once
     if (!ready[dev & 63]) {
-        e = cudaFuncSetAttribute(attn_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
+        e = cudaFuncSetAttribute(attn_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
         if (e != cudaSuccess) return e;
+        if (MODE == AT_PAGES_Q4) {   // its warps share out 512 x 128 registers
+            cudaFuncAttributes f;
+            if ((e = cudaFuncGetAttributes(&f, attn_kernel<D, MODE>)) != cudaSuccess) return e;
+            if (f.numRegs != 128) return cudaErrorLaunchOutOfResources;
+        }
         // the same split of an SM's memory for both kernels, so that it is not rearranged between them
         e = cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return e;
         ready[dev & 63] = true;
     }
-    attn_kernel<D, PAGED><<<grid, AT_THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
+    attn_kernel<D, MODE><<<grid, L::THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
     if ((e = cudaGetLastError()) != cudaSuccess || !p.join) return e;
     cudaLaunchConfig_t cfg = {};
     // rows that a unit can have: a tile's, and those of the next one behind it
@@ -972,7 +1076,7 @@ size_t attn_workspace_bytes(int D) {
            sizeof(float) * 256 * D * 2 * AT_MAX_CTAS;
 }
 
-cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches) {
+static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, void *ws, cudaStream_t stream, int *launches) {
     const int sms = sm_count();
     if (sms == 0) return cudaErrorInvalidDevice;
     AttnParams p;
@@ -992,9 +1096,19 @@ cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *l
     p.G = a.H_q / a.H_kv;
     p.tile_tokens = AT_ROWS / p.G;
     p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
-    *launches = cut ? 2 : 1;
-    if (a.lens) return a.D == 64 ? run<64, true>(p, sms, stream) : run<128, true>(p, sms, stream);
-    return a.D == 64 ? run<64, false>(p, sms, stream) : run<128, false>(p, sms, stream);
+    p.few_tokens = few_tokens;
+    *launches += cut ? 2 : 1;
+    if (q4) return a.D == 64 ? run<64, AT_PAGES_Q4>(p, sms, stream) : run<128, AT_PAGES_Q4>(p, sms, stream);
+    if (a.lens) return a.D == 64 ? run<64, AT_PAGES>(p, sms, stream) : run<128, AT_PAGES>(p, sms, stream);
+    return a.D == 64 ? run<64, AT_PROMPT>(p, sms, stream) : run<128, AT_PROMPT>(p, sms, stream);
+}
+
+cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches) {
+    return launch(a, false, 0, ws, stream, launches);
+}
+
+cudaError_t launch_attn_q4_many(const AttnArgs &a, int few_tokens, void *ws, cudaStream_t stream, int *launches) {
+    return launch(a, true, few_tokens, ws, stream, launches);
 }
 
 }  // namespace kda

@@ -21,6 +21,8 @@ struct AttnArgs {
 // Whether the call needs its workspace, and the size of one for any lengths.
 bool attn_may_cut(const AttnArgs &a);
 size_t attn_workspace_bytes(int D);
-cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches);
+cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches);   // adds to *launches
+// Over a cache held in 4 bits (k and v point to its bytes): the requests with more than few_tokens new tokens.
+cudaError_t launch_attn_q4_many(const AttnArgs &a, int few_tokens, void *ws, cudaStream_t stream, int *launches);
 
 }  // namespace kda
