@@ -79,14 +79,17 @@ struct AttnLayout {
     static constexpr bool PAGED = MODE == AT_PAGES;   // boxes of a page each
     static constexpr int THREADS = MODE == AT_PAGES_Q4 ? AT_THREADS + 128 : AT_THREADS;
     static constexpr uint32_t TILE = AT_KEYS * D * 2;          // bytes of a query, key or value tile
-    static constexpr int STAGES = D == 128 ? 5 : 8;            // key / value ring
+    static constexpr int STAGES = D == 64 ? 8 : MODE == AT_PAGES_Q4 ? 4 : 5;   // key / value ring
+    // Codes and scales of key or value tiles on their way to it, from 4-bit pages
+    static constexpr int PACKED = MODE == AT_PAGES_Q4 ? 3 : 0;
+    static constexpr uint32_t PACKED_CODES = AT_KEYS * (D / 2), PACKED_TILE = AT_KEYS * (D / 2 + D / 32);
     // A tile is made of 8-row x 64-channel swizzled blocks of 1 KiB.  A query tile, and a key or value tile of a
     // prompt, holds 64 channels of all rows, then the others; with pages, all channels of 8 rows, then the next
     // 8, so that a page, whatever its length, is one box.
     static constexpr uint32_t Q_HALF = AT_ROWS * 128;
     static constexpr uint32_t HALF = PAGED ? 1024 : AT_KEYS * 128;   // from a block to the other 64 channels'
     static constexpr uint32_t GROUP = PAGED ? 16 * D : 1024;         // from a block to the next 8 rows'
-    static constexpr uint32_t Q = STAGES * TILE, BAR = Q + 2 * TILE;
+    static constexpr uint32_t Q = STAGES * TILE, PACK = Q + 2 * TILE, BAR = PACK + PACKED * PACKED_TILE;
     // Buffers of scores an engine has: what tensor memory holds beside two outputs of D columns
     static constexpr uint32_t BUFS = (512 - 2 * D) / (2 * AT_STEP) < 3 ? 2 : 3;
     // barriers: query tile loaded / free [slot]; scores ready, weights ready, output product done
@@ -480,77 +483,90 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
         // ------------------------------------------------------------ expander (4-bit pages)
         // 4 warps write a tile's values as bf16, which they are, into the ring.  A lane takes 16 bytes of codes, 32
         // channels under one scale, of row 8 i + lane % 8 of its warp's 32 rows: 8 lanes with neighbouring rows write
-        // to different banks.  Codes go from global memory to registers, a key or value tile ahead, block ids a tile
-        // ahead of those.  Rows past the unit's last key, and rows without a block, become zeros.
+        // to different banks.  The codes come by cp.async, a tile ahead of their use (2400 cycles; the same loads into
+        // registers, which hold less, took 174 instead of 125 us for chunks among single tokens), block ids a tile ahead
+        // of those.  Rows past the unit's last key, and rows without a block, become zeros.
         constexpr int PARTS = D / 32, ROWS_AT_ONCE = 32 / PARTS, TIMES = 32 / ROWS_AT_ONCE;   // 16-byte parts of a row
-        const int xw = warp - AT_THREADS / 32, part = lane / ROWS_AT_ONCE, r0 = xw * 32 + lane % ROWS_AT_ONCE;
+        constexpr int PIECES = 32 * (D / 32) / 16, PIECE_ROWS = 32 / PIECES;                    // 16-byte pieces of scales
+        const int xw = warp - AT_THREADS / 32, part = lane / ROWS_AT_ONCE, r0 = lane % ROWS_AT_ONCE;
         const int bs = 1 << p.a.block_log2;
         const uint8_t *caches[2] = {reinterpret_cast<const uint8_t *>(p.a.k), reinterpret_cast<const uint8_t *>(p.a.v)};
-        uint32_t kv = 0;
+        unsigned char *mine = sm + L::PACK + (xw * TIMES * 32 + lane) * 16;             // this lane's codes
+        unsigned char *scales = sm + L::PACK + L::PACKED_CODES + xw * 32 * (D / 32);    // this warp's scales
+        uint32_t kv = 0, next_slot = 0, slot = 0;
         while (ok && w.next(p)) {
             const int keys = w.keys(p);
-            // blocks of the warp's first and second 16 rows of tile t: -2 none to load
+            // slabs of the warp's first and second 16 rows of tile t: block id, -1 for none that can be had, -2 for none
             auto pages = [&](int t, int (&id)[2]) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int key = t * AT_KEYS + xw * 32 + 16 * h;
-                    id[h] = t < w.b && key < keys ? max(p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)], -1) : -2;
+                    id[h] = -2;
+                    if (t < w.b && key < keys) id[h] = max(p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)], -1);
                 }
             };
-            uint4 codes[TIMES];
-            uint32_t scale[TIMES];
-            auto fetch = [&](int t, int which, const int (&id)[2]) {
+            auto copy = [&](int t, int which, const int (&id)[2]) {
+                const uint32_t to = next_slot * L::PACKED_TILE;
+                next_slot = next_slot + 1 == L::PACKED ? 0 : next_slot + 1;
 #pragma unroll
-                for (int i = 0; i < TIMES; ++i) {
-                    const int key = t * AT_KEYS + r0 + ROWS_AT_ONCE * i, b = id[(ROWS_AT_ONCE * i) >> 4];
-                    codes[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                    scale[i] = 0;
-                    if (b != -2 && (uint32_t)b >= (uint32_t)p.a.num_blocks) set_status(KDA_ERR_BAD_PAGES);
-                    if (t < w.b && key < keys && (uint32_t)b < (uint32_t)p.a.num_blocks) {
-                        const size_t slab = (((size_t)b * p.a.H_kv + w.hk) << p.a.block_log2) * q4_row_bytes(D);
-                        const int row = key & (bs - 1);
-                        codes[i] = *reinterpret_cast<const uint4 *>(caches[which] + slab + (size_t)row * (D / 2) + 16 * part);
-                        scale[i] = caches[which][slab + ((size_t)(D / 2) << p.a.block_log2) + row * (D / 32) + part];
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    if ((uint32_t)id[h] >= (uint32_t)p.a.num_blocks) continue;
+                    const uint8_t *slab = caches[which] + (((size_t)id[h] * p.a.H_kv + w.hk) << p.a.block_log2) * q4_row_bytes(D);
+                    const int row = (t * AT_KEYS + xw * 32 + 16 * h) & (bs - 1);
+                    const uint8_t *from = slab + (size_t)(row + r0) * (D / 2) + 16 * part;
+#pragma unroll
+                    for (int i = 0; i < TIMES / 2; ++i)
+                        cp_async16(mine + to + (h * (TIMES / 2) + i) * 512, from + i * ROWS_AT_ONCE * (D / 2));
+                    const int at = lane * PIECE_ROWS - 16 * h;   // of the half's rows
+                    if (at >= 0 && at < 16)
+                        cp_async16(scales + to + 16 * lane, slab + ((size_t)(D / 2) << p.a.block_log2) + (row + at) * (D / 32));
                 }
+                cp_async_commit();
             };
             int id[2], next_id[2];
             pages(w.a, id);
-            fetch(w.a, 0, id);
+            copy(w.a, 0, id);
+            copy(w.a, 1, id);
+            pages(w.a + 1, next_id);
             for (int t = w.a; ok && t < w.b; ++t) {
-                pages(t + 1, next_id);
+                if (max(id[0], id[1]) >= p.a.num_blocks || id[0] == -1 || id[1] == -1) set_status(KDA_ERR_BAD_PAGES);
 #pragma unroll
                 for (int which = 0; which < 2; ++which, ++kv) {
+                    copy(t + 1, which, next_id);
+                    cp_async_wait<2>();
+                    __syncwarp();
                     const uint32_t s = kv % L::STAGES, use = kv / L::STAGES;
                     if (use > 0 && !wait(L::KE + s, (use - 1) & 1)) break;
                     unsigned char *tile = sm + s * L::TILE + (part >> 1) * L::HALF;
-                    uint4 now[TIMES];
-                    uint32_t now_scale[TIMES];
 #pragma unroll
                     for (int i = 0; i < TIMES; ++i) {
-                        now[i] = codes[i];
-                        now_scale[i] = scale[i];
-                    }
-                    if (which == 0) fetch(t, 1, id);
-                    else fetch(t + 1, 0, next_id);
-#pragma unroll
-                    for (int i = 0; i < TIMES; ++i) {
-                        const int row = r0 + ROWS_AT_ONCE * i;
-                        const uint32_t s2 = q4_scale2(now_scale[i] * 0x00010001u), o2 = q4_offset2(s2);
-                        const uint32_t word[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+                        const int row = xw * 32 + ROWS_AT_ONCE * i + r0, b = id[(ROWS_AT_ONCE * i) >> 4];
+                        uint4 codes = *reinterpret_cast<const uint4 *>(mine + slot * L::PACKED_TILE + i * 512);
+                        uint32_t scale = scales[slot * L::PACKED_TILE + (ROWS_AT_ONCE * i + r0) * (D / 32) + part];
+                        if ((uint32_t)b >= (uint32_t)p.a.num_blocks || t * AT_KEYS + row >= keys) {
+                            codes = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                            scale = 0;
+                        }
+                        const uint32_t s2 = q4_scale2(scale * 0x00010001u), o2 = q4_offset2(s2);
+                        const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             *reinterpret_cast<uint4 *>(tile + (row >> 3) * 1024 + (row & 7) * 128 +
                                                        ((((part & 1) * 4 + x) ^ (row & 7)) << 4)) = q4_expand(word[x], s2, o2);
                     }
+                    slot = slot + 1 == L::PACKED ? 0 : slot + 1;
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar + 8 * (L::KF + s));
                 }
                 id[0] = next_id[0];
                 id[1] = next_id[1];
+                pages(t + 2, next_id);
             }
+            // (what the last tile copied ahead is nothing: its pages are -2)
+            next_slot = slot;
         }
+        cp_async_wait<0>();
     } else if (warp == AT_LOADER) {
         // ------------------------------------------------------------ loader
         uint32_t kv = 0, qu = 0;
