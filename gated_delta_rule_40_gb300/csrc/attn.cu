@@ -118,6 +118,7 @@ struct AttnParams {
     int G, tile_tokens;   // query heads a key/value head, tokens a tile
     int unit_cost;    // of a unit with two query tiles, in key tiles
     int few_tokens;   // requests with up to so many new tokens are another kernel's (0: none is)
+    uint32_t mask, bit;   // of a code in bits 3 .. 6: 16 + c (q4_masked)
 };
 
 // Sum of floor((a i + b) / m) over 0 <= i < n, a, m >= 1 (Euclid's descent on the lattice points under a
@@ -304,12 +305,6 @@ __device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w, boo
     }
 }
 
-// A pair of codes' words as bf16 (see q4.cuh): 16 bytes, 8 channels, of a word
-__device__ __forceinline__ uint4 q4_expand(uint32_t word, uint32_t s2, uint32_t minus24s2) {
-    return make_uint4(q4_value(q4_raw(word, 0), s2, minus24s2), q4_value(q4_raw(word, 1), s2, minus24s2),
-                      q4_value(q4_raw(word, 2), s2, minus24s2), q4_value(q4_raw(word, 3), s2, minus24s2));
-}
-
 template <int D, int MODE>
 __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(const __grid_constant__ CUtensorMap tq,
                                                              const __grid_constant__ CUtensorMap tk,
@@ -490,69 +485,88 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
         constexpr int PIECES = 32 * (D / 32) / 16, PIECE_ROWS = 32 / PIECES;                    // 16-byte pieces of scales
         const int xw = warp - AT_THREADS / 32, part = lane / ROWS_AT_ONCE, r0 = lane % ROWS_AT_ONCE;
         const int bs = 1 << p.a.block_log2;
-        const uint8_t *caches[2] = {reinterpret_cast<const uint8_t *>(p.a.k), reinterpret_cast<const uint8_t *>(p.a.v)};
+        // this lane's codes, and its piece of the warp's scales, in a block that begins the cache
+        const uint8_t *codes_of[2] = {reinterpret_cast<const uint8_t *>(p.a.k) + r0 * (D / 2) + 16 * part,
+                                      reinterpret_cast<const uint8_t *>(p.a.v) + r0 * (D / 2) + 16 * part};
+        const int piece_row = lane * PIECE_ROWS, piece_half = piece_row >> 4;
+        const size_t scales_at = ((size_t)(D / 2) << p.a.block_log2) + (piece_row & 15) * (D / 32);
+        const uint8_t *scales_of[2] = {reinterpret_cast<const uint8_t *>(p.a.k) + scales_at,
+                                       reinterpret_cast<const uint8_t *>(p.a.v) + scales_at};
+        const uint32_t slab_bytes = (uint32_t)q4_row_bytes(D) << p.a.block_log2;
         unsigned char *mine = sm + L::PACK + (xw * TIMES * 32 + lane) * 16;             // this lane's codes
         unsigned char *scales = sm + L::PACK + L::PACKED_CODES + xw * 32 * (D / 32);    // this warp's scales
         uint32_t kv = 0, next_slot = 0, slot = 0;
         while (ok && w.next(p)) {
             const int keys = w.keys(p);
-            // slabs of the warp's first and second 16 rows of tile t: block id, -1 for none that can be had, -2 for none
+            // blocks of the warp's first and second 16 rows of tile t: id, -1 for none that can be had, -2 for none
             auto pages = [&](int t, int (&id)[2]) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int key = t * AT_KEYS + xw * 32 + 16 * h;
-                    id[h] = -2;
-                    if (t < w.b && key < keys) id[h] = max(p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)], -1);
-                }
+                const int key = t * AT_KEYS + xw * 32;
+                const int32_t *table = p.a.table + (size_t)w.n * p.a.max_blocks;
+                id[0] = id[1] = -2;
+                if (t < w.b && key < keys) id[0] = max(table[key >> p.a.block_log2], -1);
+                if (t < w.b && key + 16 < keys) id[1] = bs > 16 ? id[0] : max(table[(key + 16) >> p.a.block_log2], -1);
             };
-            auto copy = [&](int t, int which, const int (&id)[2]) {
+            size_t slab[2];   // of tile t + 1
+            int row = 0;
+            auto locate = [&](int t, const int (&id)[2]) {
+                row = (t * AT_KEYS + xw * 32) & (bs - 1);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) slab[h] = (size_t)((uint32_t)id[h] * (uint32_t)p.a.H_kv + (uint32_t)w.hk) * slab_bytes;
+            };
+            auto copy = [&](int which, const int (&id)[2]) {
                 const uint32_t to = next_slot * L::PACKED_TILE;
                 next_slot = next_slot + 1 == L::PACKED ? 0 : next_slot + 1;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if ((uint32_t)id[h] >= (uint32_t)p.a.num_blocks) continue;
-                    const uint8_t *slab = caches[which] + (((size_t)id[h] * p.a.H_kv + w.hk) << p.a.block_log2) * q4_row_bytes(D);
-                    const int row = (t * AT_KEYS + xw * 32 + 16 * h) & (bs - 1);
-                    const uint8_t *from = slab + (size_t)(row + r0) * (D / 2) + 16 * part;
+                    const int at = (row + 16 * h) & (bs - 1);
+                    const uint8_t *from = codes_of[which] + slab[h] + at * (D / 2);
 #pragma unroll
                     for (int i = 0; i < TIMES / 2; ++i)
                         cp_async16(mine + to + (h * (TIMES / 2) + i) * 512, from + i * ROWS_AT_ONCE * (D / 2));
-                    const int at = lane * PIECE_ROWS - 16 * h;   // of the half's rows
-                    if (at >= 0 && at < 16)
-                        cp_async16(scales + to + 16 * lane, slab + ((size_t)(D / 2) << p.a.block_log2) + (row + at) * (D / 32));
+                    if (piece_half == h) cp_async16(scales + to + 16 * lane, scales_of[which] + slab[h] + at * (D / 32));
                 }
                 cp_async_commit();
             };
             int id[2], next_id[2];
             pages(w.a, id);
-            copy(w.a, 0, id);
-            copy(w.a, 1, id);
+            locate(w.a, id);
+            copy(0, id);
+            copy(1, id);
             pages(w.a + 1, next_id);
             for (int t = w.a; ok && t < w.b; ++t) {
                 if (max(id[0], id[1]) >= p.a.num_blocks || id[0] == -1 || id[1] == -1) set_status(KDA_ERR_BAD_PAGES);
+                const bool plain = min(id[0], id[1]) >= 0 && max(id[0], id[1]) < p.a.num_blocks && (t + 1) * AT_KEYS <= keys;
+                locate(t + 1, next_id);
 #pragma unroll
                 for (int which = 0; which < 2; ++which, ++kv) {
-                    copy(t + 1, which, next_id);
+                    copy(which, next_id);
                     cp_async_wait<2>();
                     __syncwarp();
                     const uint32_t s = kv % L::STAGES, use = kv / L::STAGES;
                     if (use > 0 && !wait(L::KE + s, (use - 1) & 1)) break;
-                    unsigned char *tile = sm + s * L::TILE + (part >> 1) * L::HALF;
+                    unsigned char *tile = sm + s * L::TILE + (part >> 1) * L::HALF + xw * 4096;
 #pragma unroll
                     for (int i = 0; i < TIMES; ++i) {
-                        const int row = xw * 32 + ROWS_AT_ONCE * i + r0, b = id[(ROWS_AT_ONCE * i) >> 4];
+                        const int at = ROWS_AT_ONCE * i + r0;   // of the warp's rows
                         uint4 codes = *reinterpret_cast<const uint4 *>(mine + slot * L::PACKED_TILE + i * 512);
-                        uint32_t scale = scales[slot * L::PACKED_TILE + (ROWS_AT_ONCE * i + r0) * (D / 32) + part];
-                        if ((uint32_t)b >= (uint32_t)p.a.num_blocks || t * AT_KEYS + row >= keys) {
+                        uint32_t scale = scales[slot * L::PACKED_TILE + at * (D / 32) + part];
+                        if (!plain && ((uint32_t)id[(ROWS_AT_ONCE * i) >> 4] >= (uint32_t)p.a.num_blocks ||
+                                       t * AT_KEYS + xw * 32 + at >= keys)) {
                             codes = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
                             scale = 0;
                         }
                         const uint32_t s2 = q4_scale2(scale * 0x00010001u), o2 = q4_offset2(s2);
                         const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            *reinterpret_cast<uint4 *>(tile + (row >> 3) * 1024 + (row & 7) * 128 +
-                                                       ((((part & 1) * 4 + x) ^ (row & 7)) << 4)) = q4_expand(word[x], s2, o2);
+                        for (int x = 0; x < 4; ++x) {   // 8 channels, 16 bytes
+                            uint32_t y[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                y[j] = q4_value(q4_masked(j ? word[x] >> (4 * j - 3) : word[x] << 3, p.mask, p.bit), s2, o2);
+                            *reinterpret_cast<uint4 *>(tile + (at >> 3) * 1024 + (at & 7) * 128 + ((((part & 1) * 4 + x) ^ (at & 7)) << 4)) =
+                                make_uint4(y[0], y[1], y[2], y[3]);
+                        }
                     }
                     slot = slot + 1 == L::PACKED ? 0 : slot + 1;
                     fence_async_smem();
@@ -1113,6 +1127,8 @@ static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, void *ws, 
     p.tile_tokens = AT_ROWS / p.G;
     p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
     p.few_tokens = few_tokens;
+    p.mask = 0x00780078u;
+    p.bit = 0x41804180u;
     *launches += cut ? 2 : 1;
     if (q4) return a.D == 64 ? run<64, AT_PAGES_Q4>(p, sms, stream) : run<128, AT_PAGES_Q4>(p, sms, stream);
     if (a.lens) return a.D == 64 ? run<64, AT_PAGES>(p, sms, stream) : run<128, AT_PAGES>(p, sms, stream);

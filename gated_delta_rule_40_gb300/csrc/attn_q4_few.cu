@@ -303,8 +303,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             uint32_t a[8];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                a[2 * j] = j ? masked(x0 >> (4 * j - 3), p.high, p.high_bit) : masked(x0, p.low, p.low_bit);
-                                a[2 * j + 1] = j ? masked(x1 >> (4 * j - 3), p.high, p.high_bit) : masked(x1, p.low, p.low_bit);
+                                a[2 * j] = j ? q4_masked(x0 >> (4 * j - 3), p.high, p.high_bit) : q4_masked(x0, p.low, p.low_bit);
+                                a[2 * j + 1] = j ? q4_masked(x1 >> (4 * j - 3), p.high, p.high_bit) : q4_masked(x1, p.low, p.low_bit);
                             }
 #pragma unroll
                             for (int n = 0; n < TILES; ++n) {
@@ -439,7 +439,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 auto value = [&](uint32_t word, int pair) {
-                                    return q4_value(masked(word >> (4 * j), p.low, p.low_bit), s2[pair], off[pair]);
+                                    return q4_value(q4_masked(word >> (4 * j), p.low, p.low_bit), s2[pair], off[pair]);
                                 };
                                 const uint32_t a0 = value(lo01, 0), a1 = value(hi01, 0), a2 = value(lo23, 1), a3 = value(hi23, 1);
 #pragma unroll

@@ -134,11 +134,5 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
     return y;
 }
-// (x & mask) | bit
-__device__ __forceinline__ uint32_t masked(uint32_t x, uint32_t mask, uint32_t bit) {
-    uint32_t y;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(y) : "r"(x), "r"(mask), "r"(bit));
-    return y;
-}
 
 }  // namespace kda

@@ -45,6 +45,12 @@ __device__ __forceinline__ uint32_t q4_raw(uint32_t word, int j) {
     const uint32_t x = j == 0 ? word << 3 : word >> (4 * j - 3);
     return (x & 0x00780078u) | 0x41804180u;
 }
+// (x & mask) | bit, with a mask and a bit that the compiler does not know (it makes two instructions of two it knows)
+__device__ __forceinline__ uint32_t q4_masked(uint32_t x, uint32_t mask, uint32_t bit) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(y) : "r"(x), "r"(mask), "r"(bit));
+    return y;
+}
 // (raw - 24) s with one rounding, which there is none of: s and 24 s as bf16 pairs, both exact
 __device__ __forceinline__ uint32_t q4_value(uint32_t raw, uint32_t s2, uint32_t minus24s2) {
     uint32_t y;
