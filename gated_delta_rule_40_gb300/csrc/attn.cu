@@ -94,12 +94,12 @@ struct AttnLayout {
     static constexpr uint32_t BUFS = (512 - 2 * D) / (2 * AT_STEP) < 3 ? 2 : 3;
     // barriers: query tile loaded / free [slot]; scores ready, weights ready, output product done
     // [engine][buffer]; output read [engine]; key / value tile loaded / free, value tile to be cleaned loaded
-    // [stage].  A step's scores are ready only after the output product BUFS steps before it, so that with one
+    // [stage]; codes of a tile loaded / free [packed tile].  A step's scores are ready only after the output product BUFS steps before it, so that with one
     // barrier a buffer no wait can take an earlier phase for its own.
     enum { QF = 0, QE = 2, SF = 4, PF = SF + 2 * BUFS, PV = PF + 2 * BUFS, OE = PV + 2 * BUFS, KF = OE + 2,
-           KE = KF + STAGES, VL = KF + 2 * STAGES, COUNT = KF + 3 * STAGES };
-    static constexpr uint32_t SLOT = BAR + 8 * COUNT, FLAG = SLOT + 4, BYTES = BAR + 512 + 1024;
-    static_assert(2 * D + 2 * AT_STEP * BUFS <= 512 && 8 * COUNT + 8 <= 512 && BYTES <= 232448, "attention shared memory");
+           KE = KF + STAGES, VL = KF + 2 * STAGES, CF = KF + 3 * STAGES, CE = CF + PACKED, COUNT = CE + PACKED };
+    static constexpr uint32_t SLOT = BAR + 8 * COUNT, FLAG = SLOT + 4, GOOD = FLAG + 4, BYTES = BAR + 512 + 1024;
+    static_assert(2 * D + 2 * AT_STEP * BUFS <= 512 && 8 * COUNT + 8 + 4 * PACKED <= 512 && BYTES <= 232448, "attention shared memory");
 };
 
 // A unit cut by a share's end: its rows, and how many CTAs from this one on hold a piece of it.
@@ -305,6 +305,11 @@ __device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w, boo
     }
 }
 
+__device__ __forceinline__ void copy_16_bytes(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+
 template <int D, int MODE>
 __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(const __grid_constant__ CUtensorMap tq,
                                                              const __grid_constant__ CUtensorMap tk,
@@ -332,7 +337,8 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
     } else if (tid == 32) {
         for (int i = 0; i < L::COUNT; ++i)
             mbar_init(bar + 8 * i, i >= L::KE && i < L::VL ? 2
-                                   : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) || (Q4 && i >= L::KF && i < L::KE) ? 4 : 1);
+                                   : (i >= L::PF && i < L::PV) || (i >= L::OE && i < L::KF) || (Q4 && i >= L::KF && i < L::KE) || i >= L::CE ? 4
+                                   : i >= L::CF ? 33 : 1);
         mbar_fence_init();
         *abort_flag = 0;
         s_unit = 0;
@@ -478,81 +484,28 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
         // ------------------------------------------------------------ expander (4-bit pages)
         // 4 warps write a tile's values as bf16, which they are, into the ring.  A lane takes 16 bytes of codes, 32
         // channels under one scale, of row 8 i + lane % 8 of its warp's 32 rows: 8 lanes with neighbouring rows write
-        // to different banks.  The codes come by cp.async, a tile ahead of their use (2400 cycles; the same loads into
-        // registers, which hold less, took 174 instead of 125 us for chunks among single tokens), block ids a tile ahead
-        // of those.  Rows past the unit's last key, and rows without a block, become zeros.
+        // to different banks.  Rows past the unit's last key, and rows without a block, become zeros.
         constexpr int PARTS = D / 32, ROWS_AT_ONCE = 32 / PARTS, TIMES = 32 / ROWS_AT_ONCE;   // 16-byte parts of a row
-        constexpr int PIECES = 32 * (D / 32) / 16, PIECE_ROWS = 32 / PIECES;                    // 16-byte pieces of scales
         const int xw = warp - AT_THREADS / 32, part = lane / ROWS_AT_ONCE, r0 = lane % ROWS_AT_ONCE;
-        const int bs = 1 << p.a.block_log2;
-        // this lane's codes, and its piece of the warp's scales, in a block that begins the cache
-        const uint8_t *codes_of[2] = {reinterpret_cast<const uint8_t *>(p.a.k) + r0 * (D / 2) + 16 * part,
-                                      reinterpret_cast<const uint8_t *>(p.a.v) + r0 * (D / 2) + 16 * part};
-        const int piece_row = lane * PIECE_ROWS, piece_half = piece_row >> 4;
-        const size_t scales_at = ((size_t)(D / 2) << p.a.block_log2) + (piece_row & 15) * (D / 32);
-        const uint8_t *scales_of[2] = {reinterpret_cast<const uint8_t *>(p.a.k) + scales_at,
-                                       reinterpret_cast<const uint8_t *>(p.a.v) + scales_at};
-        const uint32_t slab_bytes = (uint32_t)q4_row_bytes(D) << p.a.block_log2;
-        unsigned char *mine = sm + L::PACK + (xw * TIMES * 32 + lane) * 16;             // this lane's codes
-        unsigned char *scales = sm + L::PACK + L::PACKED_CODES + xw * 32 * (D / 32);    // this warp's scales
-        uint32_t kv = 0, next_slot = 0, slot = 0;
+        const unsigned char *mine = sm + L::PACK + (xw * TIMES * 32 + lane) * 16;
+        const unsigned char *scales = sm + L::PACK + L::PACKED_CODES + (xw * 32 + r0) * (D / 32) + part;
+        uint32_t kv = 0, slot = 0, phase = 0;
         while (ok && w.next(p)) {
             const int keys = w.keys(p);
-            // blocks of the warp's first and second 16 rows of tile t: id, -1 for none that can be had, -2 for none
-            auto pages = [&](int t, int (&id)[2]) {
-                const int key = t * AT_KEYS + xw * 32;
-                const int32_t *table = p.a.table + (size_t)w.n * p.a.max_blocks;
-                id[0] = id[1] = -2;
-                if (t < w.b && key < keys) id[0] = max(table[key >> p.a.block_log2], -1);
-                if (t < w.b && key + 16 < keys) id[1] = bs > 16 ? id[0] : max(table[(key + 16) >> p.a.block_log2], -1);
-            };
-            size_t slab[2];   // of tile t + 1
-            int row = 0;
-            auto locate = [&](int t, const int (&id)[2]) {
-                row = (t * AT_KEYS + xw * 32) & (bs - 1);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) slab[h] = (size_t)((uint32_t)id[h] * (uint32_t)p.a.H_kv + (uint32_t)w.hk) * slab_bytes;
-            };
-            auto copy = [&](int which, const int (&id)[2]) {
-                const uint32_t to = next_slot * L::PACKED_TILE;
-                next_slot = next_slot + 1 == L::PACKED ? 0 : next_slot + 1;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if ((uint32_t)id[h] >= (uint32_t)p.a.num_blocks) continue;
-                    const int at = (row + 16 * h) & (bs - 1);
-                    const uint8_t *from = codes_of[which] + slab[h] + at * (D / 2);
-#pragma unroll
-                    for (int i = 0; i < TIMES / 2; ++i)
-                        cp_async16(mine + to + (h * (TIMES / 2) + i) * 512, from + i * ROWS_AT_ONCE * (D / 2));
-                    if (piece_half == h) cp_async16(scales + to + 16 * lane, scales_of[which] + slab[h] + at * (D / 32));
-                }
-                cp_async_commit();
-            };
-            int id[2], next_id[2];
-            pages(w.a, id);
-            locate(w.a, id);
-            copy(0, id);
-            copy(1, id);
-            pages(w.a + 1, next_id);
             for (int t = w.a; ok && t < w.b; ++t) {
-                if (max(id[0], id[1]) >= p.a.num_blocks || id[0] == -1 || id[1] == -1) set_status(KDA_ERR_BAD_PAGES);
-                const bool plain = min(id[0], id[1]) >= 0 && max(id[0], id[1]) < p.a.num_blocks && (t + 1) * AT_KEYS <= keys;
-                locate(t + 1, next_id);
-#pragma unroll
+#pragma unroll 1
                 for (int which = 0; which < 2; ++which, ++kv) {
-                    copy(which, next_id);
-                    cp_async_wait<2>();
-                    __syncwarp();
                     const uint32_t s = kv % L::STAGES, use = kv / L::STAGES;
-                    if (use > 0 && !wait(L::KE + s, (use - 1) & 1)) break;
+                    if (!wait(L::CF + slot, phase) || (use > 0 && !wait(L::KE + s, (use - 1) & 1))) break;
+                    const uint32_t good = *reinterpret_cast<volatile uint32_t *>(sm + L::GOOD + 4 * slot);
+                    const bool plain = good == 0xffu && (t + 1) * AT_KEYS <= keys;
                     unsigned char *tile = sm + s * L::TILE + (part >> 1) * L::HALF + xw * 4096;
 #pragma unroll
                     for (int i = 0; i < TIMES; ++i) {
-                        const int at = ROWS_AT_ONCE * i + r0;   // of the warp's rows
+                        const int at = ROWS_AT_ONCE * i + r0, row = xw * 32 + at;   // of the warp's rows, of the tile's
                         uint4 codes = *reinterpret_cast<const uint4 *>(mine + slot * L::PACKED_TILE + i * 512);
-                        uint32_t scale = scales[slot * L::PACKED_TILE + at * (D / 32) + part];
-                        if (!plain && ((uint32_t)id[(ROWS_AT_ONCE * i) >> 4] >= (uint32_t)p.a.num_blocks ||
-                                       t * AT_KEYS + xw * 32 + at >= keys)) {
+                        uint32_t scale = scales[slot * L::PACKED_TILE + ROWS_AT_ONCE * i * (D / 32)];
+                        if (!plain && (!(good >> (row >> 4) & 1u) || t * AT_KEYS + row >= keys)) {
                             codes = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
                             scale = 0;
                         }
@@ -568,19 +521,74 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                                 make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     }
-                    slot = slot + 1 == L::PACKED ? 0 : slot + 1;
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar + 8 * (L::KF + s));
+                    if (lane == 0) {
+                        mbar_arrive(bar + 8 * (L::KF + s));
+                        mbar_arrive(bar + 8 * (L::CE + slot));
+                    }
+                    if (++slot == (uint32_t)L::PACKED) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
-                id[0] = next_id[0];
-                id[1] = next_id[1];
-                pages(t + 2, next_id);
             }
-            // (what the last tile copied ahead is nothing: its pages are -2)
-            next_slot = slot;
         }
-        cp_async_wait<0>();
+    } else if (Q4 && warp == AT_CLEANER) {
+        // ------------------------------------------------------------ copier (4-bit pages)
+        // Codes and scales of key and value tiles, by cp.async, as the expanders read them: 16 bytes of row r's place x
+        // (of D / 32) at place x rows_at_once + r of the rows' group.
+        constexpr int PARTS = D / 32, ROWS_AT_ONCE = 32 / PARTS, COPIES = AT_KEYS / ROWS_AT_ONCE;
+        constexpr int PIECES = AT_KEYS * PARTS / 16;   // of 16 bytes, of scales
+        const int bs = 1 << p.a.block_log2, r = lane / PARTS, x = lane % PARTS;
+        const uint32_t to = sbase + L::PACK + (x * ROWS_AT_ONCE + r) * 16, scales_to = sbase + L::PACK + L::PACKED_CODES + 16 * lane;
+        const int piece_row = lane * (AT_KEYS / PIECES);
+        const size_t in_codes = r * (D / 2) + 16 * x, in_scales = (size_t)(D / 2) << p.a.block_log2;
+        const uint32_t slab_bytes = (uint32_t)q4_row_bytes(D) << p.a.block_log2;
+        uint32_t n = 0;
+        while (ok && w.next(p)) {
+            const int keys = w.keys(p);
+            // block of the 16 rows that lane h < 8 answers for, of tile t: -1 none that can be had, -2 none wanted
+            auto page = [&](int t) {
+                const int key = t * AT_KEYS + 16 * lane;
+                return lane < 8 && t < w.b && key < keys ? max(p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)], -1) : -2;
+            };
+            int id = page(w.a);
+            for (int t = w.a; ok && t < w.b; ++t) {
+                const int next_id = page(t + 1);
+                if (id == -1 || id >= p.a.num_blocks) {
+                    set_status(KDA_ERR_BAD_PAGES);
+                    id = -1;
+                }
+                const uint32_t good = __ballot_sync(0xffffffffu, id >= 0);
+                // where the 16 rows' codes and scales begin
+                const size_t slab = (size_t)((uint32_t)max(id, 0) * (uint32_t)p.a.H_kv + (uint32_t)w.hk) * slab_bytes;
+                const int row = (t * AT_KEYS + 16 * lane) & (bs - 1);
+                const unsigned long long codes_at = slab + row * (D / 2), scales_at = slab + in_scales + row * PARTS;
+                const size_t piece = __shfl_sync(0xffffffffu, scales_at, piece_row >> 4 & 7) + (piece_row & 15) * PARTS;
+                const bool has_piece = lane < PIECES && (good >> (piece_row >> 4) & 1u);
+#pragma unroll 1
+                for (int which = 0; which < 2; ++which, ++n) {
+                    const uint32_t slot = n % L::PACKED, use = n / L::PACKED, at = slot * L::PACKED_TILE;
+                    if (use > 0 && !wait(L::CE + slot, (use - 1) & 1)) break;
+                    const uint8_t *cache = reinterpret_cast<const uint8_t *>(which ? p.a.v : p.a.k);
+#pragma unroll
+                    for (int c = 0; c < COPIES; ++c) {
+                        const int h = c * ROWS_AT_ONCE / 16;
+                        const size_t from = __shfl_sync(0xffffffffu, codes_at, h) + in_codes + (c * ROWS_AT_ONCE - 16 * h) * (D / 2);
+                        if (good >> h & 1u) copy_16_bytes(to + at + c * 512, cache + from);
+                    }
+                    if (has_piece) copy_16_bytes(scales_to + at, cache + piece);
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar + 8 * (L::CF + slot)) : "memory");
+                    if (lane == 0) {
+                        *reinterpret_cast<volatile uint32_t *>(sm + L::GOOD + 4 * slot) = good;
+                        mbar_arrive(bar + 8 * (L::CF + slot));
+                    }
+                }
+                id = next_id;
+            }
+        }
+        cp_async_wait_all();
     } else if (warp == AT_LOADER) {
         // ------------------------------------------------------------ loader
         uint32_t kv = 0, qu = 0;
@@ -647,7 +655,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
     } else if (warp == AT_CLEANER) {
         // ------------------------------------------------------------ cleaner
         uint32_t kv = 0, uses = 0;   // ring entries so far; per stage, the parity of its value tiles cleaned
-        while (!Q4 && ok && w.next(p)) {
+        while (ok && w.next(p)) {
             const int t = w.b - 1;
             kv += 2 * (uint32_t)(w.b - w.a);
             if (!w.dirty(p, t)) continue;
