@@ -173,8 +173,7 @@ int rope_bwd(kda::QkRopeArgs a, const kda_bf16_t *dq_out, const kda_bf16_t *dk_o
 int validate_cache_q4(const kda::Q4CacheArgs &a, int num_blocks) {
     if (a.block_log2 < 0 || (a.D != 64 && a.D != 128)) return KDA_ERR_UNSUPPORTED;
     if (a.T < 0 || a.H_kv <= 0 || a.H_kv > 65536 || !cache_ok(num_blocks, a.block_log2)) return KDA_ERR_INVALID_ARG;
-    // 256 words of 8 channels a thread block, and a 32-bit grid
-    if ((long long)a.T * a.H_kv * (a.D / 8) > 0x7fffffffLL * 256) return KDA_ERR_INVALID_ARG;
+    if ((long long)a.T * a.H_kv > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;   // rows carry 32-bit indices
     if (a.T == 0) return KDA_OK;
     if (!a.slots || !aligned(a.slots, 4) || (num_blocks > 0 && (!a.k_cache || !a.v_cache))) return KDA_ERR_INVALID_ARG;
     if (!aligned(a.k_cache, 16) || !aligned(a.v_cache, 16)) return KDA_ERR_INVALID_ARG;

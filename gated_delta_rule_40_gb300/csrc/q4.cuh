@@ -29,12 +29,13 @@ __device__ __forceinline__ uint32_t q4_scale_byte(float most) {
     return b < 255 && 7.f * q4_scale(b) < most ? b + 1 : b;
 }
 
-// Code of x under a scale of reciprocal inv: nearest, halves away from zero.  Halves are numbers of 8 significant
-// bits like bf16's x, so x / s is one exactly or is 2^-9 or more away; the product with the rounded reciprocal is off
-// by 2^-20 at most, which the 2^-12 on top outweighs.  A NaN gives 8, the code of 0.
-__device__ __forceinline__ uint32_t q4_code(float x, float inv) {
-    const int n = min(__float2int_rd(fmaf(fabsf(x), inv, 0.5f + 0x1p-12f)), 7);
-    return (uint32_t)(x < 0.f ? 8 - n : 8 + n);
+// Codes under a scale s are 8 + n, n nearest to x / s, halves away from zero.  Halves are numbers of 8 significant bits
+// like bf16's x, so x / s is one exactly or is 2^-9 (of it) or more away: times 1 / s and 1 + 2^-12, both roundings
+// included, a half rounds away from zero and nothing else crosses one.
+__device__ __forceinline__ float q4_inverse(float s) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+    return y * (1.f + 0x1p-12f);
 }
 
 // Bit at which a word holds channel c (0 .. 7)

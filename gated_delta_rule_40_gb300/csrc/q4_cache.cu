@@ -12,80 +12,109 @@ struct Q4Place {
     size_t codes, scales;
 };
 template <int D>
-__device__ __forceinline__ Q4Place q4_place(long long slot, int h, int H_kv, int block_log2) {
+__device__ __forceinline__ Q4Place q4_place(long long slot, uint32_t h, int H_kv, int block_log2) {
     const long long blk = slot >> block_log2, off = slot & ((1ll << block_log2) - 1);
     const size_t base = ((size_t)(blk * H_kv + h) << block_log2) * q4_row_bytes(D);
     return {base + (size_t)off * q4_code_bytes(D),
             base + ((size_t)q4_code_bytes(D) << block_log2) + (size_t)off * q4_scale_bytes(D)};
 }
 
-// One word of 8 channels, as codes under the common scale of the four lanes that hold a block of 32
-__device__ __forceinline__ uint32_t quantise(const uint4 &u, uint32_t *scale) {
+// Largest magnitude among the 32 channels that two lanes hold, as bf16 bits: magnitudes order as integers
+__device__ __forceinline__ uint32_t largest(const uint4 (&u)[2]) {
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        x = __vimax3_u16x2(__vimax3_u16x2(x, u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu), u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu);
+    const uint32_t m = max(x & 0xffffu, x >> 16);
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+}
+
+// A word's codes under scale s.  They are rounded by adding 1.5 2^23 and packed four at a time by products with powers of
+// 16, all exact, as the multiplier has room and the shifter has not: channels 2j in one half, 2j + 1 in the other.
+__device__ __forceinline__ uint32_t codes_of(const uint4 &u, float s, float inv, bool clamp) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float x[8], most = 0.f;
+    constexpr float ROUND = 12582912.f;
+    float2 sum = make_float2(ROUND + (float)0x8888, ROUND + (float)0x8888);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        x[2 * j] = bf16_lo(w[j]);
-        x[2 * j + 1] = bf16_hi(w[j]);
-        most = fmaxf(most, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
+        float2 x = make_float2(bf16_lo(w[j]), bf16_hi(w[j]));
+        if (clamp) {   // numbers past the largest scale's range
+            x.x = fminf(fmaxf(x.x, -7.f * s), 7.f * s);
+            x.y = fminf(fmaxf(x.y, -7.f * s), 7.f * s);
+        }
+        x = __fadd2_rn(__ffma2_rn(x, make_float2(inv, inv), make_float2(ROUND, ROUND)), make_float2(-ROUND, -ROUND));
+        sum = __ffma2_rn(x, make_float2((float)(1 << 4 * j), (float)(1 << 4 * j)), sum);
     }
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-    const uint32_t b = q4_scale_byte(most);
-    const float inv = __frcp_rn(q4_scale(b));
-    uint32_t word = 0;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) word |= q4_code(x[c], inv) << q4_bit(c);
-    *scale = b;
-    return word;
+    return __byte_perm(__float_as_uint(sum.x), __float_as_uint(sum.y), 0x5410);
 }
 
-// The scale bytes of a row, gathered in the row's first lane (a block of 32 is four lanes)
-template <int D>
-__device__ __forceinline__ uint32_t gather_scales(uint32_t b, int lane) {
-    uint32_t all = b;
-#pragma unroll
-    for (int i = 1; i < D / 32; ++i) all |= __shfl_down_sync(0xffffffffu, b, 4 * i) << (8 * i);
-    return all;
-}
-template <int D>
-__device__ __forceinline__ void store_scales(uint8_t *at, uint32_t all) {
-    if (D == 128) *reinterpret_cast<uint32_t *>(at) = all;
-    else *reinterpret_cast<uint16_t *>(at) = (uint16_t)all;
+// NaNs become 0
+__device__ __forceinline__ uint32_t no_nan(uint32_t w) {
+    if ((w & 0x7fffu) > 0x7f80u) w &= 0xffff0000u;
+    if ((w >> 16 & 0x7fffu) > 0x7f80u) w &= 0xffffu;
+    return w;
 }
 
-// A lane takes one word of a (token, head) of k and the same one of v.
+}  // namespace
+
+// A lane takes 16 channels of a (token, head) of k and the same ones of v: two words, half a block of 32.
 template <int D>
-__global__ __launch_bounds__(Q4_THREADS) void kv_write_q4_kernel(const Q4CacheArgs p, long long units) {
-    constexpr int L = D / 8;
-    const long long u = (long long)blockIdx.x * Q4_THREADS + threadIdx.x;
-    const int lane = threadIdx.x & 31;
-    const bool on = u < units;
-    const long long row = on ? u / L : 0, t = row / p.H_kv;
-    const int x = (int)(u % L), h = (int)(row - t * p.H_kv);
+__global__ __launch_bounds__(Q4_THREADS) void kv_write_q4_kernel(const Q4CacheArgs p, uint32_t rows) {
+    constexpr uint32_t L = D / 16;
+    const uint32_t row = blockIdx.x * (Q4_THREADS / L) + threadIdx.x / L, x = threadIdx.x % L;
+    const bool on = row < rows;
+    const uint32_t t = on ? row / (uint32_t)p.H_kv : 0, h = row - t * (uint32_t)p.H_kv;
     const long long slot = on ? p.slots[t] : -1;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (on) {
-        a = __ldcs(reinterpret_cast<const uint4 *>(p.k + t * p.k_stride + h * D) + x);
-        b = __ldcs(reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + h * D) + x);
+    uint4 u[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        u[0][i] = u[1][i] = make_uint4(0, 0, 0, 0);
+        if (on) {
+            u[0][i] = __ldcs(reinterpret_cast<const uint4 *>(p.k + t * p.k_stride + h * D) + 2 * x + i);
+            u[1][i] = __ldcs(reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + h * D) + 2 * x + i);
+        }
     }
-    uint32_t sk, sv;
-    const uint32_t wk = quantise(a, &sk), wv = quantise(b, &sv);
-    const uint32_t ak = gather_scales<D>(sk, lane), av = gather_scales<D>(sv, lane);
+    uint32_t most[2] = {largest(u[0]), largest(u[1])}, scale[2], word[2][2];
+    bool rare = max(most[0], most[1]) >= 0x7f80u;
+    if (__any_sync(0xffffffffu, rare)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                u[i][j] = make_uint4(no_nan(u[i][j].x), no_nan(u[i][j].y), no_nan(u[i][j].z), no_nan(u[i][j].w));
+            most[i] = largest(u[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) scale[i] = q4_scale_byte(__uint_as_float(most[i] << 16));
+    rare = max(scale[0], scale[1]) == 255;
+    rare = __any_sync(0xffffffffu, rare);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float s = q4_scale(scale[i]), inv = q4_inverse(s);
+        if (rare) {
+            word[i][0] = codes_of(u[i][0], s, inv, true);
+            word[i][1] = codes_of(u[i][1], s, inv, true);
+        } else {
+            word[i][0] = codes_of(u[i][0], s, inv, false);
+            word[i][1] = codes_of(u[i][1], s, inv, false);
+        }
+    }
     if (slot < 0) return;
     if (slot >= p.num_slots) {
         set_status(KDA_ERR_BAD_PAGES);
         return;
     }
     const Q4Place at = q4_place<D>(slot, h, p.H_kv, p.block_log2);
-    reinterpret_cast<uint32_t *>(p.k_cache + at.codes)[x] = wk;
-    reinterpret_cast<uint32_t *>(p.v_cache + at.codes)[x] = wv;
-    if (x == 0) {
-        store_scales<D>(p.k_cache + at.scales, ak);
-        store_scales<D>(p.v_cache + at.scales, av);
+    reinterpret_cast<uint2 *>(p.k_cache + at.codes)[x] = make_uint2(word[0][0], word[0][1]);
+    reinterpret_cast<uint2 *>(p.v_cache + at.codes)[x] = make_uint2(word[1][0], word[1][1]);
+    if ((x & 1) == 0) {
+        p.k_cache[at.scales + x / 2] = (uint8_t)scale[0];
+        p.v_cache[at.scales + x / 2] = (uint8_t)scale[1];
     }
 }
 
+namespace {
 // Word x of a row as 8 bf16 values
 template <int D>
 __device__ __forceinline__ uint4 values_of(uint32_t word, uint32_t b) {
@@ -94,13 +123,14 @@ __device__ __forceinline__ uint4 values_of(uint32_t word, uint32_t b) {
                       q4_value(q4_raw(word, 2), s2, o2), q4_value(q4_raw(word, 3), s2, o2));
 }
 
+}  // namespace
+
 template <int D>
-__global__ __launch_bounds__(Q4_THREADS) void kv_read_q4_kernel(const Q4CacheArgs p, long long units) {
-    constexpr int L = D / 8;
-    const long long u = (long long)blockIdx.x * Q4_THREADS + threadIdx.x;
-    if (u >= units) return;
-    const long long row = u / L, t = row / p.H_kv;
-    const int x = (int)(u % L), h = (int)(row - t * p.H_kv);
+__global__ __launch_bounds__(Q4_THREADS) void kv_read_q4_kernel(const Q4CacheArgs p, uint32_t rows) {
+    constexpr uint32_t L = D / 8;
+    const uint32_t row = blockIdx.x * (Q4_THREADS / L) + threadIdx.x / L, x = threadIdx.x % L;
+    if (row >= rows) return;
+    const uint32_t t = row / (uint32_t)p.H_kv, h = row - t * (uint32_t)p.H_kv;
     const long long slot = p.slots[t];
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
     if (slot >= p.num_slots) set_status(KDA_ERR_BAD_PAGES);
@@ -111,24 +141,28 @@ __global__ __launch_bounds__(Q4_THREADS) void kv_read_q4_kernel(const Q4CacheArg
         a = values_of<D>(wk, p.k_cache[at.scales + x / 4]);
         b = values_of<D>(wv, p.v_cache[at.scales + x / 4]);
     }
-    __stcs(reinterpret_cast<uint4 *>(p.k_out) + u, a);
-    __stcs(reinterpret_cast<uint4 *>(p.v_out) + u, b);
+    __stcs(reinterpret_cast<uint4 *>(p.k_out) + (size_t)row * L + x, a);
+    __stcs(reinterpret_cast<uint4 *>(p.v_out) + (size_t)row * L + x, b);
+}
+namespace {
+// Blocks for rows of which a lane takes `channels`
+unsigned grid_of(const Q4CacheArgs &a, int channels) {
+    const unsigned rows = Q4_THREADS / (a.D / channels);   // a block
+    return (unsigned)(((long long)a.T * a.H_kv + rows - 1) / rows);
 }
 }  // namespace
 
 cudaError_t launch_kv_write_q4(const Q4CacheArgs &a, cudaStream_t stream) {
-    const long long units = (long long)a.T * a.H_kv * (a.D / 8);
-    const unsigned grid = (unsigned)((units + Q4_THREADS - 1) / Q4_THREADS);
-    if (a.D == 64) kv_write_q4_kernel<64><<<grid, Q4_THREADS, 0, stream>>>(a, units);
-    else kv_write_q4_kernel<128><<<grid, Q4_THREADS, 0, stream>>>(a, units);
+    const uint32_t rows = (uint32_t)a.T * (uint32_t)a.H_kv;   // below 2^31, as the entry point checks
+    if (a.D == 64) kv_write_q4_kernel<64><<<grid_of(a, 16), Q4_THREADS, 0, stream>>>(a, rows);
+    else kv_write_q4_kernel<128><<<grid_of(a, 16), Q4_THREADS, 0, stream>>>(a, rows);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read_q4(const Q4CacheArgs &a, cudaStream_t stream) {
-    const long long units = (long long)a.T * a.H_kv * (a.D / 8);
-    const unsigned grid = (unsigned)((units + Q4_THREADS - 1) / Q4_THREADS);
-    if (a.D == 64) kv_read_q4_kernel<64><<<grid, Q4_THREADS, 0, stream>>>(a, units);
-    else kv_read_q4_kernel<128><<<grid, Q4_THREADS, 0, stream>>>(a, units);
+    const uint32_t rows = (uint32_t)a.T * (uint32_t)a.H_kv;
+    if (a.D == 64) kv_read_q4_kernel<64><<<grid_of(a, 8), Q4_THREADS, 0, stream>>>(a, rows);
+    else kv_read_q4_kernel<128><<<grid_of(a, 8), Q4_THREADS, 0, stream>>>(a, rows);
     return cudaGetLastError();
 }
 

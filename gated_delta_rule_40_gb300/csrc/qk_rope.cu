@@ -16,6 +16,8 @@
 #include "qk_rope.h"
 #include "kda_common.cuh"
 
+#include <type_traits>
+
 namespace kda {
 namespace {
 
@@ -130,9 +132,11 @@ __device__ __forceinline__ void load_weight(const float *w, const Lane &x, float
     for (int j = 0; j < 8; ++j) out[j] = w ? w[x.at[j >> 2] + (j & 3)] : 1.f;
 }
 
+}  // namespace
+
 // ---------------------------------------------------------------- forward
 template <int D, bool NORM, bool PAIRS>
-__global__ __launch_bounds__(QR_THREADS) void qk_rope_kernel(const QkRopeArgs p, int per, int chunks) {
+__global__ __launch_bounds__(QR_THREADS, 4) void qk_rope_kernel(const QkRopeArgs p, int per, int chunks) {
     constexpr int L = D / 8, ROWS = 32 / L, EACH = 4 / ROWS, UNROLL = 4;
     const int lane = threadIdx.x & 31, row = lane / L, l = lane - row * L;
     const long long item = (long long)blockIdx.x * QR_WARPS + (threadIdx.x >> 5);
@@ -154,27 +158,22 @@ __global__ __launch_bounds__(QR_THREADS) void qk_rope_kernel(const QkRopeArgs p,
     for (int part = 0; part < 2; ++part) {
         const int from = part ? max(g0, gq) : g0, to = part ? g1 : min(g1, gq), base = part ? gq : 0;
         if (from >= to) continue;
-        const int heads = part ? p.H_kv : p.H_q;
-        const uint16_t *in = part ? p.k + t * p.k_stride : p.q + t * p.q_stride;
-        uint16_t *out = (part ? p.k_out : p.q_out) + t * heads * D;
+        const int heads = part ? p.H_kv : p.H_q, h0 = (from - base) * ROWS + row;
+        const uint16_t *in = (part ? p.k + t * p.k_stride : p.q + t * p.q_stride) + h0 * D;
+        uint16_t *out = (part ? p.k_out : p.q_out) + (t * heads + h0) * D;
         float w[8];
         if (NORM) load_weight(part ? p.k_weight : p.q_weight, x, w);
-        for (int g = from; g < to; g += UNROLL) {
+        // UNROLL rows, all of which there are where ALL is true; addresses are the first's and constants
+        auto rows = [&](auto all, int left) {   // left: heads from the first row's on
+            constexpr bool ALL = decltype(all)::value;
             uint2 u[UNROLL][2];
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                const int h = (g + i - base) * ROWS + row;
-                if (g + i < to && h < heads) {
-                    u[i][0] = *reinterpret_cast<const uint2 *>(in + h * D + x.at[0]);
-                    u[i][1] = *reinterpret_cast<const uint2 *>(in + h * D + x.at[1]);
-                } else {
-                    u[i][0] = u[i][1] = make_uint2(0, 0);
-                }
-            }
+            for (int i = 0; i < UNROLL; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    u[i][b] = ALL || i * ROWS < left ? *reinterpret_cast<const uint2 *>(in + x.at[b] + i * ROWS * D) : make_uint2(0, 0);
 #pragma unroll
             for (int i = 0; i < UNROLL; ++i) {
-                if (g + i >= to) break;
-                const int h = (g + i - base) * ROWS + row;
                 float v[8];
                 unpack(u[i][0], v);
                 unpack(u[i][1], v + 4);
@@ -187,13 +186,21 @@ __global__ __launch_bounds__(QR_THREADS) void qk_rope_kernel(const QkRopeArgs p,
                     for (int j = 0; j < 8; ++j) v[j] = v[j] * r * w[j];
                 }
                 turn(v, c, s, PAIRS, x.turns);
-                if (h < heads) {
+                if (ALL || i * ROWS < left) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
-                        *reinterpret_cast<uint2 *>(out + h * D + x.at[b]) =
+                        *reinterpret_cast<uint2 *>(out + x.at[b] + i * ROWS * D) =
                             make_uint2(pack_bf16x2(v[4 * b], v[4 * b + 1]), pack_bf16x2(v[4 * b + 2], v[4 * b + 3]));
                 }
             }
+        };
+        const int end = min((to - base) * ROWS, heads);   // of this warp's heads
+        for (int g = from; g < to; g += UNROLL) {
+            const int first = (g - base) * ROWS;
+            if (first + UNROLL * ROWS <= end) rows(std::true_type{}, 0);
+            else rows(std::false_type{}, end - first - row);
+            in += UNROLL * ROWS * D;
+            out += UNROLL * ROWS * D;
         }
     }
 }
@@ -202,7 +209,7 @@ __global__ __launch_bounds__(QR_THREADS) void qk_rope_kernel(const QkRopeArgs p,
 // Each warp walks tokens with a fixed stride and keeps the weights' gradients of its rows in registers; a CTA
 // adds its warps' up in a fixed order, and qk_rope_dw_kernel the CTAs', so that bits repeat.
 template <int D, bool NORM, bool PAIRS>
-__global__ __launch_bounds__(QR_THREADS) void qk_rope_bwd_kernel(const QkRopeArgs p, int per, int chunks, float *partial) {
+__global__ __launch_bounds__(QR_THREADS, 3) void qk_rope_bwd_kernel(const QkRopeArgs p, int per, int chunks, float *partial) {
     constexpr int L = D / 8, ROWS = 32 / L, EACH = 4 / ROWS, UNROLL = 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane / L, l = lane - row * L;
     const Lane x = lane_of<D>(p, l);
@@ -320,7 +327,8 @@ __global__ __launch_bounds__(256) void qk_rope_dw_kernel(const float *partial, i
     }
 }
 
-constexpr int QR_BWD_CTAS = 152 * 4;
+namespace {
+constexpr int QR_BWD_CTAS = 152 * 3;
 
 // Row groups a warp takes: all of a token's where tokens alone fill the card, fewer where they do not
 void split(const QkRopeArgs &a, int *per, int *chunks) {
