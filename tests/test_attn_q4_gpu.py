@@ -71,6 +71,39 @@ def test_large_scores():
         _run([500, 64, 1], [1, 5, 40], 8, 2, 128, 16, seed=11, gain=gain)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 40])
+def test_values_of_any_size(D, new):
+    """Values near the ends of the format's range beside ordinary ones, whole requests of them, and queries with
+    channels far apart."""
+    for big in (2.0 ** -13, 300.0, 3000.0, 6.0e4, 8.0e5):
+        c = Q.PagedQ4([200, 90, 64], [new] * 3, 4, 1, D, 16, seed=21)
+        for n, rows in ((0, slice(50, 60)), (2, slice(0, None))):
+            import numpy as np
+            v = c.vs[n].clone()
+            v[rows] = (v[rows].float() * big / 3).to(torch.bfloat16)
+            codes, b = Q.quantise(v.double().numpy())
+            at_codes, at_b = Q.unpack(c.caches[1].numpy(), D)
+            for j in range(v.shape[0]):
+                blk = int(c.table[n, j // 16])
+                at_codes[blk, :, j % 16], at_b[blk, :, j % 16] = codes[j], b[j]
+            c.caches[1] = torch.from_numpy(np.ascontiguousarray(Q.pack(at_codes, at_b)))
+            c.vs[n] = Q.bf16_values(v)
+        c.q[0, 0, 1] = 40.0
+        c.q[0, 0, 2:9] = 0.001
+        c.q[0, 1] *= 1e-6
+        c.check(*c.run())
+
+
+def test_infinite_and_nan_queries():
+    c = Q.PagedQ4([100, 30], [1, 1], 8, 1, 128, 16)
+    c.q[0, 3, 5] = math.inf
+    c.q[1, 0, 7] = math.nan
+    out, lse = c.run()
+    assert torch.isnan(out[0, 3]).all() and torch.isnan(lse[0, 3]) and torch.isnan(out[1, 0]).all()
+    assert torch.isfinite(out[0, :3]).all() and torch.isfinite(out[0, 4:]).all() and torch.isfinite(out[1, 1:]).all()
+
+
 def test_rising_scores():
     """Keys whose scores rise from block to block, and then fall."""
     for sign in (1.0, -1.0):
