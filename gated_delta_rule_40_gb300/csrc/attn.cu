@@ -118,6 +118,7 @@ struct AttnParams {
     int G, tile_tokens;   // query heads a key/value head, tokens a tile
     int unit_cost;    // of a unit with two query tiles, in key tiles
     int few_tokens;   // requests with up to so many new tokens are another kernel's (0: none is)
+    bool after_few;       // that kernel was launched before
     uint32_t mask, bit;   // of a code in bits 3 .. 6: 16 + c (q4_masked)
 };
 
@@ -347,6 +348,8 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
     }
     if (warp == AT_LOADER) tmem_alloc(sbase + L::SLOT, 512);
     auto leave = [&]() {
+        // (launched while the kernel for few rows still runs: this one does not end before it)
+        if (Q4) grid_dep_wait();
         if (warp == AT_LOADER) tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(sm + L::SLOT), 512);
     };
 
@@ -941,7 +944,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == AT_LOADER) tmem_dealloc(tmem, 512);
+    leave();
 }
 
 // Joins the pieces of a unit that several CTAs worked on: with M the largest reference maximum,
@@ -952,6 +955,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
 template <int D>
 __global__ __launch_bounds__(256, 4) void attn_join_kernel(const AttnParams p) {
     const int cta = blockIdx.x;
+    grid_dep_launch();
     grid_dep_wait();   // launched while the pieces are still being computed
     const JoinDesc d = p.join[cta];
     if (d.pieces == 0) return;
@@ -1086,18 +1090,30 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         ready[dev & 63] = true;
     }
-    attn_kernel<D, MODE><<<grid, L::THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess || !p.join) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
+    if (MODE == AT_PAGES_Q4) {
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(L::THREADS);
+        cfg.dynamicSmemBytes = L::BYTES;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = p.after_few ? 1 : 0;
+        e = cudaLaunchKernelEx(&cfg, attn_kernel<D, MODE>, mq, mk, mv, p);
+    } else {
+        attn_kernel<D, MODE><<<grid, L::THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || !p.join) return e;
+    cfg = {};
     // rows that a unit can have: a tile's, and those of the next one behind it
     const int tokens = a.T < p.tile_tokens * AT_TILES ? a.T : p.tile_tokens * AT_TILES;
     const int unit_rows = tokens <= p.tile_tokens ? tokens * p.G : AT_ROWS + (tokens - p.tile_tokens) * p.G;
     cfg.gridDim = dim3(grid, (unit_rows + 31) / 32, D / 64);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p);
@@ -1114,7 +1130,7 @@ size_t attn_workspace_bytes(int D) {
            sizeof(float) * 256 * D * 2 * AT_MAX_CTAS;
 }
 
-static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, void *ws, cudaStream_t stream, int *launches) {
+static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, bool after_few, void *ws, cudaStream_t stream, int *launches) {
     const int sms = sm_count();
     if (sms == 0) return cudaErrorInvalidDevice;
     AttnParams p;
@@ -1135,6 +1151,7 @@ static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, void *ws, 
     p.tile_tokens = AT_ROWS / p.G;
     p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
     p.few_tokens = few_tokens;
+    p.after_few = after_few;
     p.mask = 0x00780078u;
     p.bit = 0x41804180u;
     *launches += cut ? 2 : 1;
@@ -1144,11 +1161,12 @@ static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, void *ws, 
 }
 
 cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches) {
-    return launch(a, false, 0, ws, stream, launches);
+    return launch(a, false, 0, false, ws, stream, launches);
 }
 
-cudaError_t launch_attn_q4_many(const AttnArgs &a, int few_tokens, void *ws, cudaStream_t stream, int *launches) {
-    return launch(a, true, few_tokens, ws, stream, launches);
+cudaError_t launch_attn_q4_many(const AttnArgs &a, int few_tokens, bool after_few, void *ws, cudaStream_t stream,
+                                int *launches) {
+    return launch(a, true, few_tokens, after_few, ws, stream, launches);
 }
 
 }  // namespace kda

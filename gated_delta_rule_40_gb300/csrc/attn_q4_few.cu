@@ -692,9 +692,13 @@ cudaError_t run(const F4Params &p, int grid, cudaStream_t stream) {
         ready[dev & 63] = true;
     }
     attn_q4_few_kernel<D, ROWS><<<grid, L::THREADS, L::BYTES, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t join(const F4Params &p, int rows, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, ROWS * (D / 4) / 128 > 0 ? ROWS * (D / 4) / 128 : 1);
+    cfg.gridDim = dim3(grid, (rows * (D / 4) + 127) / 128);
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -704,16 +708,15 @@ cudaError_t run(const F4Params &p, int grid, cudaStream_t stream) {
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_q4_join_kernel<D>, p);
 }
-}  // namespace
 
-size_t attn_q4_few_workspace_bytes(int D) {
-    return align256_f4(sizeof(F4Join) * F4_MAX_CTAS) + align256_f4(sizeof(float2) * 2 * F4_MAX_CTAS * F4_MAX_ROWS) +
-           sizeof(float) * 2 * F4_MAX_CTAS * F4_MAX_ROWS * D;
+// Rows a unit has: those that a request has on average, or a single token's where the average is the other kernel's
+int unit_rows(const AttnQ4Args &a, int most_rows) {
+    const int G = a.H_q / a.H_kv;
+    const long long rows = ((long long)a.T + a.N - 1) / a.N * G;
+    return (rows > most_rows ? G : rows) <= 8 ? 8 : 16;
 }
 
-cudaError_t launch_attn_q4_few(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches) {
-    const int sms = sm_count();
-    if (sms == 0) return cudaErrorInvalidDevice;
+F4Params params(const AttnQ4Args &a, int most_rows, void *ws) {
     F4Params p;
     p.a = a;
     char *base = static_cast<char *>(ws);
@@ -732,12 +735,29 @@ cudaError_t launch_attn_q4_few(const AttnQ4Args &a, int most_rows, void *ws, cud
     p.two7 = 1u << 7;
     p.mask_low = 0x000f000fu; p.bit_low = 0x64006400u;     // codes in bits 0 .. 3: fp16 1024 + c
     p.mask_high = 0x00f000f0u; p.bit_high = 0x54005400u;   // codes in bits 4 .. 7: fp16 64 + c
-    // rows a request has on average, or a single token's where the average is not this kernel's
-    long long rows = ((long long)a.T + a.N - 1) / a.N * p.G;
-    if (rows > most_rows) rows = p.G;
-    *launches += 2;
-    if (a.D == 64) return rows <= 8 ? run<64, 8>(p, sms, stream) : run<64, 16>(p, sms, stream);
-    return rows <= 8 ? run<128, 8>(p, sms, stream) : run<128, 16>(p, sms, stream);
+    return p;
+}
+}  // namespace
+
+size_t attn_q4_few_workspace_bytes(int D) {
+    return align256_f4(sizeof(F4Join) * F4_MAX_CTAS) + align256_f4(sizeof(float2) * 2 * F4_MAX_CTAS * F4_MAX_ROWS) +
+           sizeof(float) * 2 * F4_MAX_CTAS * F4_MAX_ROWS * D;
+}
+
+cudaError_t launch_attn_q4_few(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches) {
+    const int sms = sm_count();
+    if (sms == 0) return cudaErrorInvalidDevice;
+    const F4Params p = params(a, most_rows, ws);
+    ++*launches;
+    if (unit_rows(a, most_rows) == 8) return a.D == 64 ? run<64, 8>(p, sms, stream) : run<128, 8>(p, sms, stream);
+    return a.D == 64 ? run<64, 16>(p, sms, stream) : run<128, 16>(p, sms, stream);
+}
+
+cudaError_t launch_attn_q4_few_join(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches) {
+    const F4Params p = params(a, most_rows, ws);
+    const int rows = unit_rows(a, most_rows), sms = sm_count();
+    ++*launches;
+    return a.D == 64 ? join<64>(p, rows, sms, stream) : join<128>(p, rows, sms, stream);
 }
 
 }  // namespace kda
