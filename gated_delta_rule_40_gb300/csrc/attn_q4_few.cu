@@ -22,6 +22,9 @@ __device__ __forceinline__ float2 lds_f2(uint32_t a) {
 __device__ __forceinline__ void sts_f4(uint32_t a, float4 x) {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
 }
+__device__ __forceinline__ void cp16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+}
 template <int TO, int FROM>
 __device__ __forceinline__ void cp16_at(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;\n" ::"r"(to), "l"(from), "n"(TO), "n"(FROM) : "memory");
@@ -107,11 +110,44 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
         }
     }
 
-    // ---- loads: STAGES - 1 chunks ahead of the one that is worked on.  A run is the chunks of a piece in one block, whose
-    // addresses follow each other (with blocks of 16 rows, one chunk in two); the next run's blocks are looked up when
-    // one begins.
+    // ---- loads: STAGES - 1 chunks ahead of the one that is worked on; the block ids are looked up a chunk earlier still
     const uint32_t ring = sbase + warp * L::RING;
-    const int bs = 1 << p.a.block_log2, box = min(F4_KEYS, bs);   // box: rows of a chunk in one block
+    const int box = min(F4_KEYS, 1 << p.a.block_log2);   // rows of a chunk in one block
+    F4Walk &ahead = s_ahead[warp];
+    int ahead_c = 0, ahead_end = 0, ahead_seen = 0, ahead_hk = 0;
+    const int32_t *ahead_table = nullptr;
+    bool more;
+    auto next_piece = [&](F4Walk &x) {
+        more = x.next(p, ROWS);
+        __syncwarp();
+        if (lane == 0) ahead = x;
+        __syncwarp();
+        ahead_c = x.a;
+        ahead_end = x.b;
+        ahead_seen = x.seen;
+        ahead_hk = x.hk;
+        ahead_table = p.a.table + (size_t)x.n * p.a.max_blocks;
+    };
+    {
+        F4Walk x = w;
+        next_piece(x);
+    }
+    int id[2], id_row = 0, id_hk = 0;   // blocks of the next chunk's halves (-2: nothing to load)
+    auto look_up = [&]() {
+        const int key = ahead_c * F4_KEYS;
+        id[0] = id[1] = -2;
+        if (more && key < ahead_seen) {
+            const int e = key >> p.a.block_log2;
+            id[0] = max(ahead_table[e], -1);
+            if (box != F4_KEYS && key + box < ahead_seen) id[1] = max(ahead_table[e + 1], -1);
+        }
+        id_row = key & ((1 << p.a.block_log2) - 1);
+        id_hk = ahead_hk;
+        if (more && ++ahead_c == ahead_end) {
+            F4Walk x = ahead;
+            next_piece(x);
+        }
+    };
     // 16-byte pieces of codes: a lane's row and place, exchanged so that neither product's reads collide
     constexpr int PER_ROW = ROWB / 16, COPIES = F4_KEYS * PER_ROW / 32;
     const uint32_t copy_row = lane / PER_ROW, copy_at = lane % PER_ROW;
@@ -120,106 +156,59 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
     // scales: the first lanes for keys, as many behind them for values
     const int scale_lanes = box * (D / 32) / 16, scale_v = lane >= scale_lanes, scale_x = lane - (scale_v ? scale_lanes : 0);
     const uint32_t scale_to = 2 * L::CODES + scale_v * L::SCALES + 16 * scale_x;
-    const bool has_scales = lane < 2 * scale_lanes;
-    F4Walk &ahead = s_ahead[warp];
-    int run = 0, behind = 0, e = 0, next_id[2] = {-2, -2};   // chunks of the run, of the piece after it; the run's block
-    bool good = false, none = false;                        // whether there is that block; whether nothing is to be loaded
-    const uint8_t *k_from = nullptr, *v_from = nullptr, *scale_from = nullptr;
-    int id[2] = {-2, -2};   // the run's blocks: -1 none that can be had, -2 none
-    if (lane == 0) ahead = w;
-    __syncwarp();
-    auto next_run = [&]() {
-        const int32_t *table;
-        int row = 0, seen;
-        if (behind == 0) {   // the next piece
-            F4Walk x = ahead;
-            const bool more = x.next(p, ROWS);
-            __syncwarp();
-            if (lane == 0) ahead = x;
-            __syncwarp();
-            if (!more) return;
-            table = p.a.table + (size_t)x.n * p.a.max_blocks;
-            seen = x.seen;
-            behind = x.b - x.a;
-            e = x.a * F4_KEYS >> p.a.block_log2;
-            row = (x.a * F4_KEYS) & (bs - 1);
-            none = seen <= 0;
-            id[0] = none ? -2 : max(table[e], -1);
-            id[1] = !none && box < F4_KEYS && (e + 1) * box < seen ? max(table[e + 1], -1) : -2;
-        } else {
-            table = p.a.table + (size_t)ahead.n * p.a.max_blocks;
-            seen = ahead.seen;
-            e += F4_KEYS / box;
-            id[0] = next_id[0];
-            id[1] = next_id[1];
-        }
-        run = min(box < F4_KEYS ? 1 : (bs - row) / F4_KEYS, behind);
-        behind -= run;
-        if (behind > 0) {   // keys of the piece's next chunk, so there is a block
-            const int next = e + F4_KEYS / box;
-            next_id[0] = max(table[next], -1);
-            next_id[1] = box < F4_KEYS && (next + 1) * box < seen ? max(table[next + 1], -1) : -2;
-        }
-        good = (uint32_t)id[0] < (uint32_t)p.a.num_blocks;
-        if (!good && !none) set_status(KDA_ERR_BAD_PAGES);
-        const size_t slab = (size_t)((uint32_t)(good ? id[0] : 0) * (uint32_t)p.a.H_kv + (uint32_t)ahead.hk) * slab_bytes;
-        const size_t codes = slab + (size_t)row * ROWB + 16 * lane;
-        k_from = p.a.k + codes;
-        v_from = p.a.v + codes;
-        scale_from = (scale_v ? p.a.v : p.a.k) + slab + ((size_t)ROWB << p.a.block_log2) + row * (D / 32) + 16 * scale_x;
-    };
-    auto load = [&](uint32_t to) {   // the next chunk, into the stage at `to`
-        if (run == 0) next_run();
-        if (run > 0) {
-            --run;
+    const uint8_t *k_from = p.a.k + 16 * lane, *v_from = p.a.v + 16 * lane;
+    const uint8_t *scale_from = (scale_v ? p.a.v : p.a.k) + ((size_t)ROWB << p.a.block_log2) + 16 * scale_x;
+    auto load = [&](uint32_t to) {   // the chunk that look_up found, into the stage at `to`
+        const bool plain = box == F4_KEYS && (uint32_t)id[0] < (uint32_t)p.a.num_blocks;
+        if (plain) {
+            const size_t slab = (size_t)((uint32_t)id[0] * (uint32_t)p.a.H_kv + (uint32_t)id_hk) * slab_bytes;
+            const uint8_t *k = k_from + slab + id_row * ROWB, *v = v_from + slab + id_row * ROWB;
             const uint32_t at = to + copy_to;
-            if (good && box == F4_KEYS) {
-                cp16_at<0, 0>(at, k_from);
-                cp16_at<512, 512>(at, k_from);
-                cp16_at<L::CODES, 0>(at, v_from);
-                cp16_at<L::CODES + 512, 512>(at, v_from);
-                if constexpr (COPIES == 4) {
-                    cp16_at<1024, 1024>(at, k_from);
-                    cp16_at<1536, 1536>(at, k_from);
-                    cp16_at<L::CODES + 1024, 1024>(at, v_from);
-                    cp16_at<L::CODES + 1536, 1536>(at, v_from);
-                }
-                if (has_scales) cp16_at<0, 0>(to + scale_to, scale_from);
-                k_from += F4_KEYS * ROWB;
-                v_from += F4_KEYS * ROWB;
-                scale_from += F4_KEYS * (D / 32);
-            } else if (!none) {
+            cp16_at<0, 0>(at, k);
+            cp16_at<512, 512>(at, k);
+            cp16_at<L::CODES, 0>(at, v);
+            cp16_at<L::CODES + 512, 512>(at, v);
+            if constexpr (COPIES == 4) {
+                cp16_at<1024, 1024>(at, k);
+                cp16_at<1536, 1536>(at, k);
+                cp16_at<L::CODES + 1024, 1024>(at, v);
+                cp16_at<L::CODES + 1536, 1536>(at, v);
+            }
+            if (lane < 2 * scale_lanes) cp16(to + scale_to, scale_from + slab + id_row * (D / 32));
+        } else {
 #pragma unroll 1
-                for (int h = 0; h < F4_KEYS / box; ++h) {
-                    const int b = h ? id[1] : id[0];
-                    if (b == -2) continue;
-                    const bool there = (uint32_t)b < (uint32_t)p.a.num_blocks;
-                    if (!there) set_status(KDA_ERR_BAD_PAGES);
-                    const size_t slab = (size_t)((uint32_t)(there ? b : 0) * (uint32_t)p.a.H_kv + (uint32_t)ahead.hk) * slab_bytes;
-                    const float zeros = __uint_as_float(0x88888888u);   // codes of zeros, for rows without a block
-                    for (int i = 0; i < box * PER_ROW / 32; ++i) {
-                        const uint32_t dst = at + h * box * ROWB + 512 * i;
-                        const size_t from = slab + 16 * lane + 512 * i;
-                        if (there) {
-                            cp16_at<0, 0>(dst, p.a.k + from);
-                            cp16_at<L::CODES, 0>(dst, p.a.v + from);
-                        } else {
-                            sts_f4(dst, make_float4(zeros, zeros, zeros, zeros));
-                            sts_f4(dst + L::CODES, make_float4(zeros, zeros, zeros, zeros));
-                        }
+            for (int h = 0; h < 2; ++h) {
+                const int b = h ? id[1] : id[0];
+                if (b == -2) continue;
+                const bool good = (uint32_t)b < (uint32_t)p.a.num_blocks;
+                if (!good) set_status(KDA_ERR_BAD_PAGES);
+                const size_t slab = (size_t)((uint32_t)(good ? b : 0) * (uint32_t)p.a.H_kv + (uint32_t)id_hk) * slab_bytes;
+                const uint8_t *k = k_from + slab + id_row * ROWB, *v = v_from + slab + id_row * ROWB;
+                const uint32_t at = to + copy_to + h * box * ROWB, scales = to + scale_to + h * box * (D / 32);
+                const float zeros = __uint_as_float(0x88888888u);   // codes of zeros, for rows without a block
+                for (int i = 0; i < box * PER_ROW / 32; ++i) {
+                    if (good) {
+                        cp16(at + 512 * i, k + 512 * i);
+                        cp16(at + 512 * i + L::CODES, v + 512 * i);
+                    } else {
+                        sts_f4(at + 512 * i, make_float4(zeros, zeros, zeros, zeros));
+                        sts_f4(at + 512 * i + L::CODES, make_float4(zeros, zeros, zeros, zeros));
                     }
-                    if (has_scales) {
-                        const uint32_t dst = to + scale_to + h * box * (D / 32);
-                        if (there) cp16_at<0, 0>(dst, (scale_v ? p.a.v : p.a.k) + slab + ((size_t)ROWB << p.a.block_log2) + 16 * scale_x);
-                        else sts_f4(dst, make_float4(0.f, 0.f, 0.f, 0.f));
-                    }
+                }
+                if (lane < 2 * scale_lanes) {
+                    if (good) cp16(scales, scale_from + slab + id_row * (D / 32));
+                    else sts_f4(scales, make_float4(0.f, 0.f, 0.f, 0.f));
                 }
             }
         }
         cp_async_commit();
     };
-#pragma unroll 1
-    for (int i = 0; i < S - 1; ++i) load(ring + i * L::STAGE);
+    look_up();
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        load(ring + i * L::STAGE);
+        look_up();
+    }
     uint32_t to = (S - 1) * L::STAGE, at = 0;   // places in the ring of the next chunk to load, to work on
     auto advance = [](uint32_t &place) { place = place == L::RING - L::STAGE ? 0 : place + L::STAGE; };
 
@@ -239,58 +228,33 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
             v_at[i] = L::CODES + r * ROWB +
                       (D == 128 ? (((g >> 1) ^ (r >> 1 & 3)) << 4) + 8 * (g & 1) : (((g >> 2) ^ (r >> 2 & 1)) << 4) + 4 * (g & 3));
         }
-        // Pair j of a word as fp16: 1024 + c where the code is in bits 0 .. 3 of each half (j = 0, and j = 2 8 bits further
-        // down), 64 + c where it is in bits 4 .. 7 (j = 1, 3)
-        auto codes_f16 = [&](uint32_t word, int j) {
-            const uint32_t x = j < 2 ? word : word >> 8;
-            return j & 1 ? q4_masked(x, p.mask_high, p.bit_high) : q4_masked(x, p.mask_low, p.bit_low);
-        };
         // which scale bytes of two keys' words make a pair
         const uint32_t blk = D == 128 ? g >> 1 : g >> 2, second = D == 128 ? 4 + blk : 2 + blk;
         const uint32_t sel = odd ? second | blk << 8 : blk | second << 8;
 
         while (w.next(p, ROWS)) {
             {
-                // ---- queries: columns g of the products, as fp16 with the row's largest magnitude between 2^14 and 2^15, so
-                // that a channel is itself down to 2^-28 of that.  A lane's channels are those of its words of a key, 8 in
-                // each block of 32.  Codes come as 1024 + c and 64 + c, so that a block's product is off by 1032 and 72 times the
-                // queries' sums.
+                // ---- queries: columns g of the products.  A lane's channels are those of its words of a key, 8 in each block
+                // of 32.  Codes come as 128 + c (a word's first pair) and 16 + c (the others), so that a block's product is
+                // off by 136 and 24 times the queries' sums.
                 uint32_t q[TILES][BLOCKS][4];
-                float2 excess[TILES][BLOCKS], m[TILES], l[TILES], factor[TILES];
+                float2 excess[TILES][BLOCKS], m[TILES], l[TILES];
                 int limit[TILES][2];
                 float o[MT][TILES][4], z[TILES][4];
 #pragma unroll
                 for (int n = 0; n < TILES; ++n) {
                     const bool real = 8 * n + g < w.rows;
                     const uint16_t *src = p.a.q + out_row(p, w.r, w.hk, w.first + 8 * n + g) * D;
-                    uint32_t most = 0;
 #pragma unroll
                     for (int b = 0; b < BLOCKS; ++b) {
                         const uint4 u = real ? *reinterpret_cast<const uint4 *>(src + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
                         q[n][b][0] = u.x; q[n][b][1] = u.y; q[n][b][2] = u.z; q[n][b][3] = u.w;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) most = max(most, max(q[n][b][j] << 16 & 0x7fff0000u, q[n][b][j] & 0x7fff0000u));
-                    }
-                    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                    // up and down are reciprocal powers of two; exponent fields from 14 to 253
-                    const uint32_t e = most ? min(268u - (most >> 23), 253u) : 127u;
-                    const float up = __uint_as_float(e << 23);
-                    const float down = most >= 0x7f800000u ? NAN : __uint_as_float((254u - e) << 23);
-                    // queries 2t and 2t + 1 are the columns of this lane's scores
-                    factor[n] = make_float2(p.c * __shfl_sync(0xffffffffu, down, 8 * t), p.c * __shfl_sync(0xffffffffu, down, 8 * t + 4));
-#pragma unroll
-                    for (int b = 0; b < BLOCKS; ++b) {
-                        float sum = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x0 = bf16_lo(q[n][b][j]) * up, x1 = bf16_hi(q[n][b][j]) * up;
-                            q[n][b][j] = pack_f16x2(x0, x1);
-                            sum = fmaf(j & 1 ? -72.f : -1032.f, x0 + x1, sum);
-                        }
+                        float sum = 136.f * (bf16_lo(u.x) + bf16_hi(u.x)) +
+                                    24.f * ((bf16_lo(u.y) + bf16_hi(u.y)) + (bf16_lo(u.z) + bf16_hi(u.z)) + (bf16_lo(u.w) + bf16_hi(u.w)));
                         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                        excess[n][b] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
+                        // queries 2t and 2t + 1, the columns of this lane's scores
+                        excess[n][b] = make_float2(-__shfl_sync(0xffffffffu, sum, 8 * t), -__shfl_sync(0xffffffffu, sum, 8 * t + 4));
                     }
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
@@ -309,6 +273,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                 for (int c = w.a; c < w.b; ++c) {
                     load(ring + to);
                     advance(to);
+                    look_up();
                     cp_async_wait<S - 1>();
                     __syncwarp();
                     // plain loads, whose offsets go into the instructions
@@ -338,14 +303,14 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             uint32_t a[8];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                a[2 * j] = codes_f16(x0, j);
-                                a[2 * j + 1] = codes_f16(x1, j);
+                                a[2 * j] = j ? q4_masked(x0 >> (4 * j - 3), p.high, p.high_bit) : q4_masked(x0, p.low, p.low_bit);
+                                a[2 * j + 1] = j ? q4_masked(x1 >> (4 * j - 3), p.high, p.high_bit) : q4_masked(x1, p.low, p.low_bit);
                             }
 #pragma unroll
                             for (int n = 0; n < TILES; ++n) {
                                 float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_f16(d, a[0], a[1], a[2], a[3], q[n][b][0], q[n][b][1]);
-                                mma_f16(d, a[4], a[5], a[6], a[7], q[n][b][2], q[n][b][3]);
+                                mma_bf16(d, a[0], a[1], a[2], a[3], q[n][b][0], q[n][b][1]);
+                                mma_bf16(d, a[4], a[5], a[6], a[7], q[n][b][2], q[n][b][3]);
                                 const float2 d0 = __fadd2_rn(make_float2(d[0], d[1]), excess[n][b]);
                                 const float2 d1 = __fadd2_rn(make_float2(d[2], d[3]), excess[n][b]);
                                 s[n][2 * mt] = b ? __ffma2_rn(make_float2(s0, s0), d0, s[n][2 * mt]) : __fmul2_rn(make_float2(s0, s0), d0);
@@ -355,34 +320,31 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     }
                     // ---- weights
                     const bool edge = (c + 1) * F4_KEYS > lowest;
-                    float2 fac[TILES];
-#pragma unroll
-                    for (int n = 0; n < TILES; ++n) fac[n] = factor[n];
-                    if (edge) {   // keys that a row does not see; scores in units of log 2 from here on
+                    if (edge) {   // keys that a row does not see (in the scores' units of log 2 from here on)
 #pragma unroll
                         for (int n = 0; n < TILES; ++n)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int key = c * F4_KEYS + 16 * (i >> 1) + kr + 8 * (i & 1);
-                                s[n][i].x = key >= limit[n][0] ? -INFINITY : s[n][i].x * factor[n].x;
-                                s[n][i].y = key >= limit[n][1] ? -INFINITY : s[n][i].y * factor[n].y;
-                                fac[n] = make_float2(1.f, 1.f);
+                                s[n][i].x = key >= limit[n][0] ? -INFINITY : s[n][i].x * p.c;
+                                s[n][i].y = key >= limit[n][1] ? -INFINITY : s[n][i].y * p.c;
                             }
                     }
+                    const float factor = edge ? 1.f : p.c;
                     uint32_t pk[TILES][4];
                     float2 sum[TILES];
-                    auto weights = [&](bool wide) {   // as fp16, or as bf16 beside values that fp16 does not hold
+                    auto weights = [&]() {
 #pragma unroll
                         for (int n = 0; n < TILES; ++n) {
                             const float2 base = make_float2(m[n].x == -INFINITY ? 0.f : -m[n].x, m[n].y == -INFINITY ? 0.f : -m[n].y);
                             sum[n] = make_float2(0.f, 0.f);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                float2 y = __ffma2_rn(s[n][i], fac[n], base);
+                                float2 y = __ffma2_rn(s[n][i], make_float2(factor, factor), base);
                                 y.x = ex2(y.x);
                                 y.y = ex2(y.y);
                                 sum[n] = __fadd2_rn(sum[n], y);
-                                pk[n][i] = wide ? pack_bf16x2(y.x, y.y) : pack_f16x2(y.x, y.y);
+                                pk[n][i] = pack_bf16x2(y.x, y.y);
                             }
                         }
                     };
@@ -391,7 +353,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     for (int n = 0; n < TILES; ++n) look |= fminf(m[n].x, m[n].y) == -INFINITY;
                     look = __any_sync(0xffffffffu, look);
                     if (!look) {
-                        weights(false);
+                        weights();
 #pragma unroll
                         for (int n = 0; n < TILES; ++n) look |= !(sum[n].x <= F4_MOST) || !(sum[n].y <= F4_MOST);
                         look = __any_sync(0xffffffffu, look);
@@ -402,6 +364,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                         for (int n = 0; n < TILES; ++n) {
                             auto raise = [&](float top, float &m, float &l) {   // the factor by which what is there shrinks
+                                top *= factor;
 #pragma unroll
                                 for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
                                 if (!(top > m + 8.f)) return 1.f;
@@ -411,11 +374,12 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                                 move = true;
                                 return f;
                             };
-                            float2 top = make_float2(-INFINITY, -INFINITY);
+                            // (a negative scale turns the order round)
+                            float2 top = s[n][0];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                top.x = fmaxf(top.x, s[n][i].x * fac[n].x);
-                                top.y = fmaxf(top.y, s[n][i].y * fac[n].y);
+                            for (int i = 1; i < 4; ++i) {
+                                top.x = factor < 0.f ? fminf(top.x, s[n][i].x) : fmaxf(top.x, s[n][i].x);
+                                top.y = factor < 0.f ? fminf(top.y, s[n][i].y) : fmaxf(top.y, s[n][i].y);
                             }
                             f[n].x = raise(top.x, m[n].x, l[n].x);
                             f[n].y = raise(top.y, m[n].y, l[n].y);
@@ -431,28 +395,11 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                                     for (int i = 0; i < MT; ++i) o[i][n][x] *= fx;
                                 }
                         }
-                        weights(false);
+                        weights();
                     }
 #pragma unroll
                     for (int n = 0; n < TILES; ++n) l[n] = __fadd2_rn(l[n], sum[n]);
-                    // ---- outputs, of values times 2: a byte's scale, doubled, is an fp16 number.  The codes 1024 + c give c s, of
-                    // which 8 times the sum of p s, a product of its own, is taken off at the end; 64 + c give (c - 8) s at once.
-                    // 1024 s has to be an fp16 number too: a chunk with a doubled scale above 60 (values above 200) takes bf16
-                    // products instead.
-                    uint32_t pair_of[4];   // scale bytes of keys 16 (i / 2) + 8 (i % 2) + 2t (+ 1), of this lane's block
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (D == 128) {
-                            const uint2 x = pair(v_scales + 8 * i * 4);
-                            pair_of[i] = __byte_perm(x.x, x.y, sel) & 0x00ff00ffu;
-                        } else {
-                            pair_of[i] = __byte_perm(word(v_scales + 8 * i * 2), 0, sel) & 0x00ff00ffu;
-                        }
-                    }
-                    // bit 15 of a half where the byte is above 159
-                    const uint32_t above = (pair_of[0] + 0x7f607f60u) | (pair_of[1] + 0x7f607f60u) | (pair_of[2] + 0x7f607f60u) | (pair_of[3] + 0x7f607f60u);
-                    const bool wide = __any_sync(0xffffffffu, (above & 0x80008000u) != 0);
-                    if (wide) weights(true);   // the same weights again
+                    // ---- outputs: codes times scale in bf16 (exact), 8 times the scales' own sum taken off at the end
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
                         uint32_t bq[TILES][2];
@@ -461,6 +408,17 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             bq[n][0] = transpose_8x8(pk[n][2 * mt]);
                             bq[n][1] = transpose_8x8(pk[n][2 * mt + 1]);
                         }
+                        uint32_t s2[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (D == 128) {
+                                const uint2 x = pair(v_scales + (16 * mt + 8 * i) * 4);
+                                s2[i] = (__byte_perm(x.x, x.y, sel) & 0x00ff00ffu) * p.two4 + 0x38003800u;
+                            } else {
+                                s2[i] = (__byte_perm(word(v_scales + (16 * mt + 8 * i) * 2), 0, sel) & 0x00ff00ffu) * p.two4 + 0x38003800u;
+                            }
+                        }
+                        const uint32_t off[2] = {s2[0] + 0x83808380u, s2[1] + 0x83808380u};   // -128 s
                         uint32_t v[4][D / 64];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -472,46 +430,20 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                                 v[i][0] = word(stage + v_at[i & 1] + (16 * mt + 8 * (i >> 1)) * ROWB);
                             }
                         }
-                        if (!wide) {
-                            uint32_t s2[2], off[2][2];
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                s2[i] = pair_of[2 * mt + i] * p.two7 + 0x04000400u;
-                                off[i][0] = s2[i] + 0xa800a800u;                       // -1024 s
-                                off[i][1] = fma_f16x2(s2[i], 0xd480d480u, 0u);         // -72 s
-                            }
+                        for (int n = 0; n < TILES; ++n) mma_bf16(z[n], s2[0], s2[0], s2[1], s2[1], bq[n][0], bq[n][1]);
 #pragma unroll
-                            for (int n = 0; n < TILES; ++n) mma_f16(z[n], s2[0], s2[0], s2[1], s2[1], bq[n][0], bq[n][1]);
+                        for (int x = 0; x < D / 64; ++x) {
+                            const uint32_t lo01 = __byte_perm(v[0][x], v[1][x], 0x5410), hi01 = __byte_perm(v[0][x], v[1][x], 0x7632);
+                            const uint32_t lo23 = __byte_perm(v[2][x], v[3][x], 0x5410), hi23 = __byte_perm(v[2][x], v[3][x], 0x7632);
 #pragma unroll
-                            for (int x = 0; x < D / 64; ++x) {
-                                const uint32_t lo01 = __byte_perm(v[0][x], v[1][x], 0x5410), hi01 = __byte_perm(v[0][x], v[1][x], 0x7632);
-                                const uint32_t lo23 = __byte_perm(v[2][x], v[3][x], 0x5410), hi23 = __byte_perm(v[2][x], v[3][x], 0x7632);
+                            for (int j = 0; j < 4; ++j) {
+                                auto value = [&](uint32_t word, int pair) {
+                                    return q4_value(q4_masked(word >> (4 * j), p.low, p.low_bit), s2[pair], off[pair]);
+                                };
+                                const uint32_t a0 = value(lo01, 0), a1 = value(hi01, 0), a2 = value(lo23, 1), a3 = value(hi23, 1);
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    auto value = [&](uint32_t word, int i) { return fma_f16x2(codes_f16(word, j), s2[i], off[i][j & 1]); };
-                                    const uint32_t a0 = value(lo01, 0), a1 = value(hi01, 0), a2 = value(lo23, 1), a3 = value(hi23, 1);
-#pragma unroll
-                                    for (int n = 0; n < TILES; ++n) mma_f16(o[4 * x + j][n], a0, a1, a2, a3, bq[n][0], bq[n][1]);
-                                }
-                            }
-                        } else {
-                            uint32_t s2[2], off[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                s2[i] = pair_of[2 * mt + i] * p.two4 + 0x38803880u;   // doubled
-                                off[i] = q4_offset2(s2[i]);
-                            }
-#pragma unroll
-                            for (int x = 0; x < D / 64; ++x) {
-                                const uint32_t lo01 = __byte_perm(v[0][x], v[1][x], 0x5410), hi01 = __byte_perm(v[0][x], v[1][x], 0x7632);
-                                const uint32_t lo23 = __byte_perm(v[2][x], v[3][x], 0x5410), hi23 = __byte_perm(v[2][x], v[3][x], 0x7632);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const uint32_t a0 = q4_value(q4_raw(lo01, j), s2[0], off[0]), a1 = q4_value(q4_raw(hi01, j), s2[0], off[0]);
-                                    const uint32_t a2 = q4_value(q4_raw(lo23, j), s2[1], off[1]), a3 = q4_value(q4_raw(hi23, j), s2[1], off[1]);
-#pragma unroll
-                                    for (int n = 0; n < TILES; ++n) mma_bf16(o[4 * x + j][n], a0, a1, a2, a3, bq[n][0], bq[n][1]);
-                                }
+                                for (int n = 0; n < TILES; ++n) mma_bf16(o[4 * x + j][n], a0, a1, a2, a3, bq[n][0], bq[n][1]);
                             }
                         }
                     }
@@ -531,12 +463,12 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                         for (int lanes = 4; lanes < 32; lanes <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, lanes);
                         const int row = 8 * n + 2 * t + x;
-                        const float zz = 4.f * z[n][x];
-                        float y[D / 8];   // channels (D / 8) g .., halved
+                        const float zz = 8.f * z[n][x];
+                        float y[D / 8];   // channels (D / 8) g ..
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            y[2 * i] = 0.5f * o[i][n][x] - (i & 1 ? 0.f : zz);
-                            y[2 * i + 1] = 0.5f * o[i][n][2 + x] - (i & 1 ? 0.f : zz);
+                            y[2 * i] = o[i][n][x] - zz;
+                            y[2 * i + 1] = o[i][n][2 + x] - zz;
                         }
                         if (!whole) {
                             if (g == 0) sts_f2(sbase + L::ML + ((warp * 2 + part) * ROWS + row) * 8, make_float2(ref, sum));
@@ -732,9 +664,8 @@ F4Params params(const AttnQ4Args &a, int most_rows, void *ws) {
     p.unit_cost = 2;   // 4000 cycles of a warp, whose chunks take 3100 (0, 1, 2, 4: 159, 143, 136, 140 us for 256 decoded tokens)
     p.two20 = 1u << 20;
     p.two4 = 1u << 4;
-    p.two7 = 1u << 7;
-    p.mask_low = 0x000f000fu; p.bit_low = 0x64006400u;     // codes in bits 0 .. 3: fp16 1024 + c
-    p.mask_high = 0x00f000f0u; p.bit_high = 0x54005400u;   // codes in bits 4 .. 7: fp16 64 + c
+    p.low = 0x000f000fu; p.low_bit = 0x43004300u;     // codes in bits 0 .. 3: 128 + c
+    p.high = 0x00780078u; p.high_bit = 0x41804180u;   // codes in bits 3 .. 6: 16 + c
     return p;
 }
 }  // namespace

@@ -11,14 +11,14 @@ constexpr long long F4_MAX_KEYS = 0x7fffff00;
 constexpr int F4_SHARE = 4;            // chunks a CTA has at least
 constexpr int F4_MAX_CTAS = 160;
 constexpr int F4_MAX_ROWS = 16;        // rows a unit can have
-constexpr float F4_MOST = 32768.0f;    // sum of a lane's weights that makes a warp look at its maximum: fp16 holds 65504
+constexpr float F4_MOST = 65536.0f;    // sum of a lane's weights that makes a warp look at its maximum
 
 // Rows a unit has at most, and how a CTA is made for them
 template <int D, int ROWS>
 struct F4Layout {
     static constexpr int WARPS = ROWS == 16 ? 8 : 12;
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int STAGES = ROWS == 16 ? 4 : 3;             // a warp's ring of chunks
+    static constexpr int STAGES = 2;                              // a warp's ring of chunks
     static constexpr int TILES = ROWS / 8;                        // of 8 queries, the columns of a product
     // A chunk: codes of keys and values, then their scales
     static constexpr uint32_t CODES = F4_KEYS * (D / 2), SCALES = F4_KEYS * (D / 32);
@@ -49,7 +49,7 @@ struct F4Params {
     int unit_cost;    // of a unit, in chunks
     // Constants that the compiler does not know: a product with a power of two stays one (the multiplier has room, the
     // shifter has not), and a mask with a leading bit stays one instruction.
-    uint32_t two20, two4, two7, mask_low, bit_low, mask_high, bit_high;
+    uint32_t two20, two4, low, low_bit, high, high_bit;
 };
 
 // Token of a request's row (exact: row < 512, G <= 128)
@@ -128,23 +128,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// lo, hi as fp16, rounded to nearest
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t y;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(y) : "f"(hi), "f"(lo));
-    return y;
-}
-__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t y;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(y) : "r"(a), "r"(b), "r"(c));
-    return y;
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t y;

@@ -796,16 +796,17 @@ def kda_qk_norm_rope_bwd(q, k, positions, freqs, dq_out, dk_out, q_weight=None, 
     g = {"dq": _new((T, H_q, D), f32, at, stream), "dk": _new((T, H_kv, D), f32, at, stream),
          "dq_weight": None if q_weight is None else _new((D,), f32, at, stream),
          "dk_weight": None if k_weight is None else _new((D,), f32, at, stream)}
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = _new((kda_qk_norm_rope_bwd_workspace_size(D),), torch.uint8, at, stream)
-    size = 0
-    if workspace is not None:
+    outs = [None if x is None else x.data_ptr() for x in g.values()]
+    if workspace is None and stream is None and torch._C._cuda_isCurrentStreamCapturing():
+        # under capture the workspace is torch's, whose graphs keep their memory
+        workspace = torch.empty(kda_qk_norm_rope_bwd_workspace_size(D), dtype=torch.uint8, device=at)
+    if workspace is None:
+        rc = lib.kda_qk_norm_rope_bwd(*args, *outs, _raw_stream(stream, dev))
+    else:
         _check(workspace, "workspace", torch.uint8)
-        size = workspace.numel()
-    rc = lib.kda_qk_norm_rope_bwd_ws(*args, *(None if x is None else x.data_ptr() for x in g.values()),
-                                     None if workspace is None else workspace.data_ptr(), size, _raw_stream(stream, dev))
+        rc = lib.kda_qk_norm_rope_bwd_ws(*args, *outs, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc:
-        _raise(rc, "kda_qk_norm_rope_bwd_ws")
+        _raise(rc, "kda_qk_norm_rope_bwd")
     return g
 
 
