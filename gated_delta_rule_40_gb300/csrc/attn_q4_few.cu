@@ -228,39 +228,64 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
             v_at[i] = L::CODES + r * ROWB +
                       (D == 128 ? (((g >> 1) ^ (r >> 1 & 3)) << 4) + 8 * (g & 1) : (((g >> 2) ^ (r >> 2 & 1)) << 4) + 4 * (g & 3));
         }
+        // Pair j of a word as fp16: 1024 + c where the code is in bits 0 .. 3 of each half (j = 0, and j = 2 8 bits further
+        // down), 64 + c where it is in bits 4 .. 7 (j = 1, 3)
+        auto codes_f16 = [&](uint32_t word, int j) {
+            const uint32_t x = j < 2 ? word : word >> 8;
+            return j & 1 ? q4_masked(x, p.mask_high, p.bit_high) : q4_masked(x, p.mask_low, p.bit_low);
+        };
         // which scale bytes of two keys' words make a pair
         const uint32_t blk = D == 128 ? g >> 1 : g >> 2, second = D == 128 ? 4 + blk : 2 + blk;
         const uint32_t sel = odd ? second | blk << 8 : blk | second << 8;
 
         while (w.next(p, ROWS)) {
             {
-                // ---- queries: columns g of the products.  A lane's channels are those of its words of a key, 8 in each block
-                // of 32.  Codes come as 128 + c (a word's first pair) and 16 + c (the others), so that a block's product is
-                // off by 136 and 24 times the queries' sums.
+                // ---- queries: columns g of the products, as fp16 with the row's largest magnitude between 2^14 and 2^15, so
+                // that a channel is itself down to 2^-28 of that.  A lane's channels are those of its words of a key, 8 in
+                // each block of 32.  Codes come as 1024 + c and 64 + c, so that a block's product is off by 1032 and 72 times
+                // the queries' sums.
                 uint32_t q[TILES][BLOCKS][4];
-                float2 excess[TILES][BLOCKS], m[TILES], l[TILES];
+                float2 excess[TILES][BLOCKS], m[TILES], minus_m[TILES], l[TILES], factor[TILES];   // minus_m: 0 for -infinity
                 int limit[TILES][2];
                 float o[MT][TILES][4], z[TILES][4];
 #pragma unroll
                 for (int n = 0; n < TILES; ++n) {
                     const bool real = 8 * n + g < w.rows;
                     const uint16_t *src = p.a.q + out_row(p, w.r, w.hk, w.first + 8 * n + g) * D;
+                    uint32_t most = 0;
 #pragma unroll
                     for (int b = 0; b < BLOCKS; ++b) {
                         const uint4 u = real ? *reinterpret_cast<const uint4 *>(src + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
                         q[n][b][0] = u.x; q[n][b][1] = u.y; q[n][b][2] = u.z; q[n][b][3] = u.w;
-                        float sum = 136.f * (bf16_lo(u.x) + bf16_hi(u.x)) +
-                                    24.f * ((bf16_lo(u.y) + bf16_hi(u.y)) + (bf16_lo(u.z) + bf16_hi(u.z)) + (bf16_lo(u.w) + bf16_hi(u.w)));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) most = max(most, max(q[n][b][j] << 16 & 0x7fff0000u, q[n][b][j] & 0x7fff0000u));
+                    }
+                    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                    // up and down are reciprocal powers of two; exponent fields from 14 to 253
+                    const uint32_t e = most ? min(268u - (most >> 23), 253u) : 127u;
+                    const float up = __uint_as_float(e << 23);
+                    const float down = most >= 0x7f800000u ? NAN : __uint_as_float((254u - e) << 23);
+                    // queries 2t and 2t + 1 are the columns of this lane's scores
+                    factor[n] = make_float2(p.c * __shfl_sync(0xffffffffu, down, 8 * t), p.c * __shfl_sync(0xffffffffu, down, 8 * t + 4));
+#pragma unroll
+                    for (int b = 0; b < BLOCKS; ++b) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float x0 = bf16_lo(q[n][b][j]) * up, x1 = bf16_hi(q[n][b][j]) * up;
+                            q[n][b][j] = pack_f16x2(x0, x1);
+                            sum = fmaf(j & 1 ? -72.f : -1032.f, x0 + x1, sum);
+                        }
                         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                        // queries 2t and 2t + 1, the columns of this lane's scores
-                        excess[n][b] = make_float2(-__shfl_sync(0xffffffffu, sum, 8 * t), -__shfl_sync(0xffffffffu, sum, 8 * t + 4));
+                        excess[n][b] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
                     }
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
                         limit[n][x] = w.r.keys - w.r.fresh + f4_token(p, min(w.first + 8 * n + 2 * t + x, w.first + w.rows - 1)) + 1;
                     m[n] = make_float2(-INFINITY, -INFINITY);
-                    l[n] = make_float2(0.f, 0.f);
+                    minus_m[n] = l[n] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         z[n][x] = 0.f;
@@ -303,14 +328,14 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             uint32_t a[8];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                a[2 * j] = j ? q4_masked(x0 >> (4 * j - 3), p.high, p.high_bit) : q4_masked(x0, p.low, p.low_bit);
-                                a[2 * j + 1] = j ? q4_masked(x1 >> (4 * j - 3), p.high, p.high_bit) : q4_masked(x1, p.low, p.low_bit);
+                                a[2 * j] = codes_f16(x0, j);
+                                a[2 * j + 1] = codes_f16(x1, j);
                             }
 #pragma unroll
                             for (int n = 0; n < TILES; ++n) {
                                 float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_bf16(d, a[0], a[1], a[2], a[3], q[n][b][0], q[n][b][1]);
-                                mma_bf16(d, a[4], a[5], a[6], a[7], q[n][b][2], q[n][b][3]);
+                                mma_f16(d, a[0], a[1], a[2], a[3], q[n][b][0], q[n][b][1]);
+                                mma_f16(d, a[4], a[5], a[6], a[7], q[n][b][2], q[n][b][3]);
                                 const float2 d0 = __fadd2_rn(make_float2(d[0], d[1]), excess[n][b]);
                                 const float2 d1 = __fadd2_rn(make_float2(d[2], d[3]), excess[n][b]);
                                 s[n][2 * mt] = b ? __ffma2_rn(make_float2(s0, s0), d0, s[n][2 * mt]) : __fmul2_rn(make_float2(s0, s0), d0);
@@ -320,27 +345,30 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     }
                     // ---- weights
                     const bool edge = (c + 1) * F4_KEYS > lowest;
-                    if (edge) {   // keys that a row does not see (in the scores' units of log 2 from here on)
+                    float2 fac[TILES];
 #pragma unroll
-                        for (int n = 0; n < TILES; ++n)
+                    for (int n = 0; n < TILES; ++n) fac[n] = factor[n];
+                    if (edge) {   // keys that a row does not see; scores in units of log 2 from here on
+#pragma unroll
+                        for (int n = 0; n < TILES; ++n) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int key = c * F4_KEYS + 16 * (i >> 1) + kr + 8 * (i & 1);
-                                s[n][i].x = key >= limit[n][0] ? -INFINITY : s[n][i].x * p.c;
-                                s[n][i].y = key >= limit[n][1] ? -INFINITY : s[n][i].y * p.c;
+                                s[n][i].x = key >= limit[n][0] ? -INFINITY : s[n][i].x * factor[n].x;
+                                s[n][i].y = key >= limit[n][1] ? -INFINITY : s[n][i].y * factor[n].y;
                             }
+                            fac[n] = make_float2(1.f, 1.f);
+                        }
                     }
-                    const float factor = edge ? 1.f : p.c;
                     uint32_t pk[TILES][4];
                     float2 sum[TILES];
                     auto weights = [&]() {
 #pragma unroll
                         for (int n = 0; n < TILES; ++n) {
-                            const float2 base = make_float2(m[n].x == -INFINITY ? 0.f : -m[n].x, m[n].y == -INFINITY ? 0.f : -m[n].y);
                             sum[n] = make_float2(0.f, 0.f);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                float2 y = __ffma2_rn(s[n][i], make_float2(factor, factor), base);
+                                float2 y = __ffma2_rn(s[n][i], fac[n], minus_m[n]);
                                 y.x = ex2(y.x);
                                 y.y = ex2(y.y);
                                 sum[n] = __fadd2_rn(sum[n], y);
@@ -348,41 +376,39 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             }
                         }
                     };
-                    bool look = false;
-#pragma unroll
-                    for (int n = 0; n < TILES; ++n) look |= fminf(m[n].x, m[n].y) == -INFINITY;
-                    look = __any_sync(0xffffffffu, look);
+                    // A row that sees no key of the piece's first chunk sees none of the piece: its reference stays -infinity
+                    bool look = c == w.a;
                     if (!look) {
                         weights();
+                        float most = sum[0].x + sum[0].y;
 #pragma unroll
-                        for (int n = 0; n < TILES; ++n) look |= !(sum[n].x <= F4_MOST) || !(sum[n].y <= F4_MOST);
-                        look = __any_sync(0xffffffffu, look);
+                        for (int n = 1; n < TILES; ++n) most += sum[n].x + sum[n].y;
+                        look = __any_sync(0xffffffffu, !(most <= F4_MOST));
                     }
                     if (look) {
                         bool move = false;
                         float2 f[TILES];
 #pragma unroll
                         for (int n = 0; n < TILES; ++n) {
-                            auto raise = [&](float top, float &m, float &l) {   // the factor by which what is there shrinks
-                                top *= factor;
+                            auto raise = [&](float top, float &m, float &minus_m, float &l) {   // returns what is there's factor
 #pragma unroll
                                 for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
                                 if (!(top > m + 8.f)) return 1.f;
                                 const float f = ex2(m - top);
                                 m = top;
+                                minus_m = -top;
                                 l *= f;
                                 move = true;
                                 return f;
                             };
-                            // (a negative scale turns the order round)
-                            float2 top = s[n][0];
+                            float2 top = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-                            for (int i = 1; i < 4; ++i) {
-                                top.x = factor < 0.f ? fminf(top.x, s[n][i].x) : fmaxf(top.x, s[n][i].x);
-                                top.y = factor < 0.f ? fminf(top.y, s[n][i].y) : fmaxf(top.y, s[n][i].y);
+                            for (int i = 0; i < 4; ++i) {
+                                top.x = fmaxf(top.x, s[n][i].x * fac[n].x);
+                                top.y = fmaxf(top.y, s[n][i].y * fac[n].y);
                             }
-                            f[n].x = raise(top.x, m[n].x, l[n].x);
-                            f[n].y = raise(top.y, m[n].y, l[n].y);
+                            f[n].x = raise(top.x, m[n].x, minus_m[n].x, l[n].x);
+                            f[n].y = raise(top.y, m[n].y, minus_m[n].y, l[n].y);
                         }
                         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -439,7 +465,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 auto value = [&](uint32_t word, int pair) {
-                                    return q4_value(q4_masked(word >> (4 * j), p.low, p.low_bit), s2[pair], off[pair]);
+                                    return q4_value(q4_masked(word >> (4 * j), p.mask_low, p.bit_bf16), s2[pair], off[pair]);
                                 };
                                 const uint32_t a0 = value(lo01, 0), a1 = value(hi01, 0), a2 = value(lo23, 1), a3 = value(hi23, 1);
 #pragma unroll
@@ -664,8 +690,9 @@ F4Params params(const AttnQ4Args &a, int most_rows, void *ws) {
     p.unit_cost = 2;   // 4000 cycles of a warp, whose chunks take 3100 (0, 1, 2, 4: 159, 143, 136, 140 us for 256 decoded tokens)
     p.two20 = 1u << 20;
     p.two4 = 1u << 4;
-    p.low = 0x000f000fu; p.low_bit = 0x43004300u;     // codes in bits 0 .. 3: 128 + c
-    p.high = 0x00780078u; p.high_bit = 0x41804180u;   // codes in bits 3 .. 6: 16 + c
+    p.mask_low = 0x000f000fu; p.bit_low = 0x64006400u;     // codes in bits 0 .. 3: fp16 1024 + c
+    p.mask_high = 0x00f000f0u; p.bit_high = 0x54005400u;   // codes in bits 4 .. 7: fp16 64 + c
+    p.bit_bf16 = 0x43004300u;                              // codes in bits 0 .. 3: bf16 128 + c
     return p;
 }
 }  // namespace

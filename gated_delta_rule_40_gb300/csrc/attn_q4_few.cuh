@@ -49,7 +49,7 @@ struct F4Params {
     int unit_cost;    // of a unit, in chunks
     // Constants that the compiler does not know: a product with a power of two stays one (the multiplier has room, the
     // shifter has not), and a mask with a leading bit stays one instruction.
-    uint32_t two20, two4, low, low_bit, high, high_bit;
+    uint32_t two20, two4, mask_low, bit_low, mask_high, bit_high, bit_bf16;
 };
 
 // Token of a request's row (exact: row < 512, G <= 128)
@@ -128,6 +128,18 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// lo, hi as fp16, rounded to nearest
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t y;

@@ -69,9 +69,9 @@ def bf16_values(x):
 def reference(q, k, v, scale, first=0):
     """A.reference, with room for what computing with the codes themselves adds:
 
-    * A block's product of q with codes 128 + c and 16 + c, less what the 128 + 8 and 16 + 8 add: at most three
-      roundings of 2^-24 (two products of 16 channels, the difference), of at most 143 sum|q|.  A score is off by
-      e = scale 2^-22 143 sum over blocks of s sum|q|, a weight by a factor of 2 e more.  A block's s is at most a sixth
+    * A block's product of q with codes 1024 + c and 64 + c, less what the 1024 + 8 and 64 + 8 add: at most three
+      roundings of 2^-24 (two products of 16 channels, the difference), of at most 1039 sum|q|.  A score is off by
+      e = scale 2^-22 1039 sum over blocks of s sum|q|, a weight by a factor of 2 e more.  A block's s is at most a sixth
       of its largest value (its largest n is 6 or 7, as scales are 1.125 apart or less), or 2^-15 for a block of zeros.
     * The sums over codes c = 8 + n, less 8 times the sum of p s, are off by 2^-19 of 16 sum p s (chains of up to 32
       fp32 additions, 2^-24 each).
@@ -87,7 +87,7 @@ def reference(q, k, v, scale, first=0):
     s = torch.einsum("ahd,lhd->ahl", q, k.repeat_interleave(G, 1)) * scale
     p = torch.where(seen[:, None, :], torch.exp(s - torch.where(torch.isfinite(l), l, 0.0)[..., None]), 0.0)
     ks = torch.where(seen[:, :, None, None], (k.unflatten(-1, (-1, 32)).abs().amax(-1) / 6 + 2.0 ** -15)[None], 0.0).amax(1)
-    e = scale * 2.0 ** -22 * 143 * (ks.repeat_interleave(G, 1) * q.unflatten(-1, (-1, 32)).abs().sum(-1)).sum(-1)
+    e = scale * 2.0 ** -22 * 1039 * (ks.repeat_interleave(G, 1) * q.unflatten(-1, (-1, 32)).abs().sum(-1)).sum(-1)
     steps = v.unflatten(-1, (-1, 32)).abs().amax(-1) / 6 + 2.0 ** -15
     ps = torch.einsum("ahl,lhb->ahb", p, steps.repeat_interleave(G, 1)).repeat_interleave(32, -1)
     sums = torch.einsum("ahl,lhd->ahd", p, v.abs().repeat_interleave(G, 1))
