@@ -209,9 +209,10 @@ __global__ __launch_bounds__(QR_THREADS, 4) void qk_rope_kernel(const QkRopeArgs
 // Each warp walks tokens with a fixed stride and keeps the weights' gradients of its rows in registers; a CTA
 // adds its warps' up in a fixed order, and qk_rope_dw_kernel the CTAs', so that bits repeat.
 template <int D, bool NORM, bool PAIRS>
-__global__ __launch_bounds__(QR_THREADS, 3) void qk_rope_bwd_kernel(const QkRopeArgs p, int per, int chunks, float *partial) {
-    constexpr int L = D / 8, ROWS = 32 / L, EACH = 4 / ROWS, UNROLL = 2;
+__global__ __launch_bounds__(QR_THREADS, 2) void qk_rope_bwd_kernel(const QkRopeArgs p, int per, int chunks, float *partial) {
+    constexpr int L = D / 8, ROWS = 32 / L, EACH = 4 / ROWS, UNROLL = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane / L, l = lane - row * L;
+    grid_dep_launch();   // the sum of the weights' gradients may come as soon as CTAs leave
     const Lane x = lane_of<D>(p, l);
     unsigned long long turns[EACH];
     bool wild[EACH];
@@ -234,28 +235,26 @@ __global__ __launch_bounds__(QR_THREADS, 3) void qk_rope_bwd_kernel(const QkRope
         for (int part = 0; part < 2; ++part) {
             const int from = part ? max(g0, gq) : g0, to = part ? g1 : min(g1, gq), base = part ? gq : 0;
             if (from >= to) continue;
-            const int heads = part ? p.H_kv : p.H_q;
-            const uint16_t *in = part ? p.k + t * p.k_stride : p.q + t * p.q_stride;
-            const uint16_t *dy = (part ? p.dk_out : p.dq_out) + t * heads * D;
-            float *out = (part ? p.dk : p.dq) + t * heads * D;
+            const int heads = part ? p.H_kv : p.H_q, h0 = (from - base) * ROWS + row;
+            const uint16_t *in = (part ? p.k + t * p.k_stride : p.q + t * p.q_stride) + h0 * D;
+            const uint16_t *dy = (part ? p.dk_out : p.dq_out) + (t * heads + h0) * D;
+            float *out = (part ? p.dk : p.dq) + (t * heads + h0) * D;
             float w[8];
             if (NORM) load_weight(part ? p.k_weight : p.q_weight, x, w);
-            for (int g = from; g < to; g += UNROLL) {
+            // as in the forward
+            auto rows = [&](auto all, int left) {
+                constexpr bool ALL = decltype(all)::value;
                 uint2 u[UNROLL][2], d[UNROLL][2];
 #pragma unroll
-                for (int i = 0; i < UNROLL; ++i) {
-                    const int h = (g + i - base) * ROWS + row;
-                    const bool on = g + i < to && h < heads;
+                for (int i = 0; i < UNROLL; ++i)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        d[i][b] = on ? *reinterpret_cast<const uint2 *>(dy + h * D + x.at[b]) : make_uint2(0, 0);
-                        if (NORM) u[i][b] = on ? *reinterpret_cast<const uint2 *>(in + h * D + x.at[b]) : make_uint2(0, 0);
+                        const bool on = ALL || i * ROWS < left;
+                        d[i][b] = on ? *reinterpret_cast<const uint2 *>(dy + x.at[b] + i * ROWS * D) : make_uint2(0, 0);
+                        if (NORM) u[i][b] = on ? *reinterpret_cast<const uint2 *>(in + x.at[b] + i * ROWS * D) : make_uint2(0, 0);
                     }
-                }
 #pragma unroll
                 for (int i = 0; i < UNROLL; ++i) {
-                    if (g + i >= to) break;
-                    const int h = (g + i - base) * ROWS + row;
                     float v[8];
                     unpack(d[i][0], v);
                     unpack(d[i][1], v + 4);
@@ -270,7 +269,7 @@ __global__ __launch_bounds__(QR_THREADS, 3) void qk_rope_bwd_kernel(const QkRope
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             y[j] *= r;
-                            if (h < heads) dw[part][j] += v[j] * y[j];
+                            if (ALL || i * ROWS < left) dw[part][j] += v[j] * y[j];
                             v[j] *= w[j];
                             dot += v[j] * y[j];
                         }
@@ -278,13 +277,22 @@ __global__ __launch_bounds__(QR_THREADS, 3) void qk_rope_bwd_kernel(const QkRope
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] = r * (v[j] - y[j] * dot);
                     }
-                    if (h < heads) {
+                    if (ALL || i * ROWS < left) {
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
-                            *reinterpret_cast<float4 *>(out + h * D + x.at[b]) =
+                            *reinterpret_cast<float4 *>(out + x.at[b] + i * ROWS * D) =
                                 make_float4(v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]);
                     }
                 }
+            };
+            const int end = min((to - base) * ROWS, heads);
+            for (int g = from; g < to; g += UNROLL) {
+                const int first = (g - base) * ROWS;
+                if (first + UNROLL * ROWS <= end) rows(std::true_type{}, 0);
+                else rows(std::false_type{}, end - first - row);
+                in += UNROLL * ROWS * D;
+                dy += UNROLL * ROWS * D;
+                out += UNROLL * ROWS * D;
             }
         }
     }
@@ -315,6 +323,7 @@ __global__ __launch_bounds__(256) void qk_rope_dw_kernel(const float *partial, i
     __shared__ float s[32][8];
     const int col = blockIdx.x * 8 + (threadIdx.x & 7), r = threadIdx.x >> 3;
     float v = 0.f;
+    grid_dep_wait();
     for (int i = r; i < n; i += 32) v += partial[(size_t)i * 2 * D + col];
     s[r][threadIdx.x & 7] = v;
     __syncthreads();
@@ -328,7 +337,7 @@ __global__ __launch_bounds__(256) void qk_rope_dw_kernel(const float *partial, i
 }
 
 namespace {
-constexpr int QR_BWD_CTAS = 152 * 3;
+constexpr int QR_BWD_CTAS = 152 * 2;
 
 // Row groups a warp takes: all of a token's where tokens alone fill the card, fewer where they do not
 void split(const QkRopeArgs &a, int *per, int *chunks) {
@@ -385,9 +394,17 @@ cudaError_t launch_qk_rope_bwd(const QkRopeArgs &a, void *ws, cudaStream_t strea
         ++*launches;
     }
     if (!weights) return cudaSuccess;
-    qk_rope_dw_kernel<<<2 * a.D / 8, 256, 0, stream>>>(partial, n, a.D, a.dq_weight, a.dk_weight);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * a.D / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = n > 0 ? 1 : 0;
     ++*launches;
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, qk_rope_dw_kernel, (const float *)partial, n, a.D, a.dq_weight, a.dk_weight);
 }
 
 }  // namespace kda

@@ -185,6 +185,25 @@ def test_backward(D, rot, pairs, norm):
                 assert err.max() <= 0, f"d{name}_weight off its bound by {err.max():.3e}"
 
 
+def test_backward_without_eps():
+    """eps = 0: rows beside the last head, which are nobody's, have no say in the weights' gradients."""
+    kda = _kda()
+    for H, Hkv, D in ((3, 1, 128), (5, 2, 64)):
+        q, k, dq, dk, pos, w = _case(3, H, Hkv, D, seed=8)
+        freqs = freqs_of(D)
+        g = torch.Generator().manual_seed(4)
+        do = [torch.randn(x.shape, generator=g).to(torch.bfloat16) for x in (q, k)]
+        args = (pos.cuda(), freqs.cuda())
+        got = kda.kda_qk_norm_rope_bwd(dq, dk, *args, do[0].cuda(), do[1].cuda(), w[0].cuda(), w[1].cuda(), eps=0.0)
+        for name, x, d, weight in (("q", q[:2], do[0][:2], w[0]), ("k", k[:2], do[1][:2], w[1])):
+            dx, _ = gradients(x, pos[:2], freqs, weight, 0.0, True, False, d)
+            tol, _ = grad_bounds(x, pos[:2], freqs, weight, 0.0, True, False, d)
+            assert ((got["d" + name][:2].double().cpu() - dx).abs() - tol).max() <= 0
+        assert torch.isfinite(got["dq_weight"]).all() and torch.isfinite(got["dk_weight"]).all()
+        qo, _ = kda.kda_qk_norm_rope(dq, dk, *args, w[0].cuda(), w[1].cuda(), eps=0.0)
+        assert torch.isfinite(qo).all()
+
+
 def test_backward_sizes_and_bits():
     kda = _kda()
     for T, H, Hkv, D in ((3000, 8, 2, 128), (2001, 6, 3, 64), (1, 33, 1, 128)):
