@@ -12,7 +12,14 @@
 // Layout.  A row (a head's D channels) is D / 8 lanes with two runs of four channels each: a lane that turns
 // holds both channels of its four pairs (half-split pairs: 4l .. and R / 2 + 4l ..; neighbours: 8l ..), so a
 // rotation needs no exchange between lanes.  A warp takes 2 (D = 128) or 4 rows at a time of one token, whose
-// four frequencies a lane its rows compute together once.
+// four frequencies a lane its rows compute together once, and has four such groups' loads in flight, at
+// addresses that are one and constants.  Warps walk the tokens; where there are few, a token's rows are
+// shared out among several.
+//
+// What bounds it, and what it measured on the GPU: DRAM.  32768 tokens x 40 heads of 128 in 107 us, 6.3 TB/s (0.93 of
+// a copy; a warp a token 112 us, with an address for each row 122 us); gradients of 16384 tokens, which leave as
+// fp32, in 104 us and 2 us for the weights' sum, 6.4 TB/s.  Packed fp32 pairs took 146 us: pairs of registers for
+// them cost more moves than they save.  A call of 64 tokens takes 3.7 us, of which the host needs 17.
 #include "qk_rope.h"
 #include "kda_common.cuh"
 
@@ -136,71 +143,71 @@ __device__ __forceinline__ void load_weight(const float *w, const Lane &x, float
 
 // ---------------------------------------------------------------- forward
 template <int D, bool NORM, bool PAIRS>
-__global__ __launch_bounds__(QR_THREADS, 4) void qk_rope_kernel(const QkRopeArgs p, int per, int chunks) {
+__global__ __launch_bounds__(QR_THREADS, 3) void qk_rope_kernel(const QkRopeArgs p, int per, int chunks) {
     constexpr int L = D / 8, ROWS = 32 / L, EACH = 4 / ROWS, UNROLL = 4;
     const int lane = threadIdx.x & 31, row = lane / L, l = lane - row * L;
-    const long long item = (long long)blockIdx.x * QR_WARPS + (threadIdx.x >> 5);
-    const long long t = item / chunks;
-    if (t >= p.T) return;
-    const int pos = p.positions[t];
-    if (pos < 0) return;   // a padded token
     const Lane x = lane_of<D>(p, l);
-    float c[4], s[4];
-    {
-        unsigned long long turns[EACH];
-        bool wild[EACH];
-        load_turns<D>(p, lane, x.turns, turns, wild);
+    unsigned long long turns[EACH];
+    bool wild[EACH];
+    load_turns<D>(p, lane, x.turns, turns, wild);
+    const long long items = (long long)p.T * chunks;
+    for (long long item = (long long)blockIdx.x * QR_WARPS + (threadIdx.x >> 5); item < items;
+         item += (long long)gridDim.x * QR_WARPS) {
+        const long long t = item / chunks;
+        const int pos = p.positions[t];
+        if (pos < 0) continue;   // a padded token
+        float c[4], s[4];
         angles<D>(p, turns, wild, pos, lane, x.turns, c, s);
-    }
-    const int gq = (p.H_q + ROWS - 1) / ROWS, gk = (p.H_kv + ROWS - 1) / ROWS;
-    const int g0 = (int)(item - t * chunks) * per, g1 = min(g0 + per, gq + gk);
+        const int gq = (p.H_q + ROWS - 1) / ROWS, gk = (p.H_kv + ROWS - 1) / ROWS;
+        const int g0 = (int)(item - t * chunks) * per, g1 = min(g0 + per, gq + gk);
 #pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-        const int from = part ? max(g0, gq) : g0, to = part ? g1 : min(g1, gq), base = part ? gq : 0;
-        if (from >= to) continue;
-        const int heads = part ? p.H_kv : p.H_q, h0 = (from - base) * ROWS + row;
-        const uint16_t *in = (part ? p.k + t * p.k_stride : p.q + t * p.q_stride) + h0 * D;
-        uint16_t *out = (part ? p.k_out : p.q_out) + (t * heads + h0) * D;
-        float w[8];
-        if (NORM) load_weight(part ? p.k_weight : p.q_weight, x, w);
-        // UNROLL rows, all of which there are where ALL is true; addresses are the first's and constants
-        auto rows = [&](auto all, int left) {   // left: heads from the first row's on
-            constexpr bool ALL = decltype(all)::value;
-            uint2 u[UNROLL][2];
+        for (int part = 0; part < 2; ++part) {
+            const int from = part ? max(g0, gq) : g0, to = part ? g1 : min(g1, gq), base = part ? gq : 0;
+            if (from >= to) continue;
+            const int heads = part ? p.H_kv : p.H_q, h0 = (from - base) * ROWS + row;
+            const uint16_t *in = (part ? p.k + t * p.k_stride : p.q + t * p.q_stride) + h0 * D;
+            uint16_t *out = (part ? p.k_out : p.q_out) + (t * heads + h0) * D;
+            float w[8];
+            if (NORM) load_weight(part ? p.k_weight : p.q_weight, x, w);
+            // UNROLL rows, all of which there are where ALL is true; addresses are the first's and constants
+            auto rows = [&](auto all, int left) {   // left: heads from the first row's on
+                constexpr bool ALL = decltype(all)::value;
+                uint2 u[UNROLL][2];
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    u[i][b] = ALL || i * ROWS < left ? *reinterpret_cast<const uint2 *>(in + x.at[b] + i * ROWS * D) : make_uint2(0, 0);
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i) {
-                float v[8];
-                unpack(u[i][0], v);
-                unpack(u[i][1], v + 4);
-                if (NORM) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum += v[j] * v[j];
-                    const float r = rsqrtf(row_sum<L>(sum) * (1.f / D) + p.eps);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = v[j] * r * w[j];
-                }
-                turn(v, c, s, PAIRS, x.turns);
-                if (ALL || i * ROWS < left) {
+                for (int i = 0; i < UNROLL; ++i)
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
-                        *reinterpret_cast<uint2 *>(out + x.at[b] + i * ROWS * D) =
-                            make_uint2(pack_bf16x2(v[4 * b], v[4 * b + 1]), pack_bf16x2(v[4 * b + 2], v[4 * b + 3]));
+                        u[i][b] = ALL || i * ROWS < left ? *reinterpret_cast<const uint2 *>(in + x.at[b] + i * ROWS * D) : make_uint2(0, 0);
+#pragma unroll
+                for (int i = 0; i < UNROLL; ++i) {
+                    float v[8];
+                    unpack(u[i][0], v);
+                    unpack(u[i][1], v + 4);
+                    if (NORM) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum += v[j] * v[j];
+                        const float r = rsqrtf(row_sum<L>(sum) * (1.f / D) + p.eps);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = v[j] * r * w[j];
+                    }
+                    turn(v, c, s, PAIRS, x.turns);
+                    if (ALL || i * ROWS < left) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            *reinterpret_cast<uint2 *>(out + x.at[b] + i * ROWS * D) =
+                                make_uint2(pack_bf16x2(v[4 * b], v[4 * b + 1]), pack_bf16x2(v[4 * b + 2], v[4 * b + 3]));
+                    }
                 }
+            };
+            const int end = min((to - base) * ROWS, heads);   // of this warp's heads
+            for (int g = from; g < to; g += UNROLL) {
+                const int first = (g - base) * ROWS;
+                if (first + UNROLL * ROWS <= end) rows(std::true_type{}, 0);
+                else rows(std::false_type{}, end - first - row);
+                in += UNROLL * ROWS * D;
+                out += UNROLL * ROWS * D;
             }
-        };
-        const int end = min((to - base) * ROWS, heads);   // of this warp's heads
-        for (int g = from; g < to; g += UNROLL) {
-            const int first = (g - base) * ROWS;
-            if (first + UNROLL * ROWS <= end) rows(std::true_type{}, 0);
-            else rows(std::false_type{}, end - first - row);
-            in += UNROLL * ROWS * D;
-            out += UNROLL * ROWS * D;
         }
     }
 }
@@ -337,7 +344,7 @@ __global__ __launch_bounds__(256) void qk_rope_dw_kernel(const float *partial, i
 }
 
 namespace {
-constexpr int QR_BWD_CTAS = 152 * 2;
+constexpr int QR_FWD_CTAS = 152 * 3, QR_BWD_CTAS = 152 * 2;   // resident at once
 
 // Row groups a warp takes: all of a token's where tokens alone fill the card, fewer where they do not
 void split(const QkRopeArgs &a, int *per, int *chunks) {
@@ -352,7 +359,7 @@ template <int D, bool NORM, bool PAIRS>
 cudaError_t forward(const QkRopeArgs &a, cudaStream_t stream) {
     int per, chunks;
     split(a, &per, &chunks);
-    const long long grid = ((long long)a.T * chunks + QR_WARPS - 1) / QR_WARPS;
+    const long long want = ((long long)a.T * chunks + QR_WARPS - 1) / QR_WARPS, grid = want < QR_FWD_CTAS ? want : QR_FWD_CTAS;
     qk_rope_kernel<D, NORM, PAIRS><<<(unsigned)grid, QR_THREADS, 0, stream>>>(a, per, chunks);
     return cudaGetLastError();
 }
