@@ -11,7 +11,7 @@
 // output).  So a long cache with few rows, ragged lengths and the triangle of a causal prompt all divide
 // evenly, without a schedule in memory: each CTA sums the requests' lengths itself.
 //
-// One CTA, 12 warps (an online softmax over steps of 64 keys, both products on the tensor cores):
+// One CTA, 12 warps (16 with 4-bit pages; an online softmax over steps of 64 keys, both products on the tensor cores):
 //   loader    TMA: the query tiles (two slots) and key / value tiles of 128 keys (a ring) into
 //             128-byte-swizzled shared memory; with pages, one box a page
 //   cleaner   zeros in the value rows past a unit's last key, which may hold anything (another prompt, an
@@ -36,6 +36,9 @@
 //             and moves only when a step's sum of p passes 2^16: a larger p costs no precision in floating
 //             point, a common factor cancels in o, and neither the maximum nor a rescaling of O is needed
 //             in most steps.
+// 4-bit pages (chunks of prompts; attn_q4_few.cu has the requests with few rows).  The cleaner is a copier, which brings a
+// tile's codes and scales to shared memory by cp.async, and four warps more expand them into the ring as the bf16 values
+// that they stand for, 1000 cycles a key or value tile, two of which the rest takes 3700 for.
 // Keys past a row's own position are masked in s.
 //
 // What bounds it, and what it measured (on the GPU, without a call's host side).  Prompts: the tensor cores, whose N = 64 products wait for shared
@@ -47,6 +50,10 @@
 // which the start and the joining take 10 us.  The ring's 160 KiB (heads of 128) cover DRAM's latency at the 45 GB/s
 // that an SM gets of its bandwidth.  Decode with heads of 64 (a ring of 128 KiB): 256 requests, 16 heads over 8, with
 // 1.1 GB in 0.208 ms, 5.3 TB/s.
+// 4-bit pages: 24 requests with chunks of up to 512 tokens among single ones, 28 heads over 4, blocks of 16, in 142 us for
+// the chunks, where bf16 pages take 117 us: the expanding warps take issue slots and shared-memory bandwidth from the
+// softmax.  (Expanding warps that load codes into registers themselves: 187 us; by cp.async: 163 us; with fewer
+// instructions 147 us.)
 //
 // Every wait is bounded; a timeout records KDA_ERR_DEVICE_TIMEOUT and all roles stop.
 #include "attn.h"

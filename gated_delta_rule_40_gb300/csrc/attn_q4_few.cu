@@ -1,4 +1,35 @@
-// Attention of few query rows over the 4-bit cache (see attn_q4.cu for which requests these are).
+// Attention of few query rows over the 4-bit cache: requests with up to F4_MOST_ROWS (attn_q4.cu) rows, decoded and
+// drafted tokens.  s = scale q.k, o = sum exp(s - lse) v over the values that the cache stands for.
+//
+// Work.  A unit is up to 8 or 16 rows (tokens x query heads of a group) of one (request, key/value head), over the chunks
+// of 32 keys that its last row sees.  The chunks of all units, and a constant for each unit's own cost, form one line, cut
+// into equal shares: one a warp, so that few units are shared at all.  (With the warps of a CTA all on one unit, every one
+// of them pays for every unit's beginning and end: 518 against 166 us for 256 decoded tokens, at the time.)  What a share's
+// ends cut is joined in shared memory among a CTA's warps, and by attn_q4_join_kernel among CTAs, in a fixed order.
+//
+// A warp by itself, with no barrier until the end: cp.async of a chunk into one of two stages, the next but one in flight
+// while it works.  Both products are small ones (mma.sync) with the keys as rows: 16 keys x 16 channels times 8 queries
+// for the scores, 16 channels x 16 keys times 8 queries for the outputs, whose operands are expanded from codes in
+// registers.  tcgen05, whose rows are 128, would take operands from shared or tensor memory, which costs more here than
+// what they compute.
+//   scores   codes as fp16 in place, 1024 + c or 64 + c, one shift a word of 8; q as fp16 times a power of two, which keeps
+//            every channel (bf16 has fewer bits); the sums of q that the 1032 and 72 add are taken off, and the keys'
+//            scale is applied, for each block of 32 channels in fp32
+//   weights  2^(s c - m), c = scale log2(e), with the reference m of the piece's first chunk, which moves when a sum of
+//            weights passes 2^16; rounded to bf16 as operands, like attn.cu's
+//   outputs  codes of two keys in the halves of a register, 128 + c, times the keys' scales less 128 of them: c s, a bf16
+//            number; 8 times the sum of p s, a product of its own, is taken off at the end.  Values reach to 9e5, which
+//            fp16 does not hold (tried with bf16 for what it does not: the same time)
+// Lanes read what they expand from 16-byte pieces that are exchanged by the row's place, without bank conflicts.
+//
+// What bounds it, and what it measured on the GPU.  256 decoded tokens with 0.59 GB of cache in 130 us, 4.5 TB/s: expanding
+// and multiplying take 120 us by themselves, the loads 100 us (the floor is 87 us).  A chunk costs an SM 246 cycles and 604
+// instructions, 285 of them on the logic and shift units (148 cycles at their rate) and 34 products (69); without the
+// outputs, or the scores, the loads bound it (102, 106 us), without the products themselves 128 us.  12 warps of 168
+// registers beat 16 of 128 (147 against 154 us, at the time) and 8 of 255, whose outputs and next scores were interleaved
+// (154 against 136 us).  8-bit products (e4m3 holds a code as it is) turn their operands into fp16 first on this chip.
+// 4 drafted tokens over 131072 keys, 16 rows: 51 us; 100 decoded tokens with heads of 64 35 us (the smaller chunks' own
+// cost); 4 decoded tokens over up to 1000 keys 8.5 us, all latency.
 #include "attn_q4_few.cuh"
 
 namespace kda {
