@@ -10,6 +10,10 @@
     python -m gated_delta_rule_40_gb300.profile_case --method decode_tokens --B 256 --T 4 --H 64 --iters 4
     python -m gated_delta_rule_40_gb300.profile_case --method attn --B 1 --T 8192 --H 32 --iters 3
     python -m gated_delta_rule_40_gb300.profile_case --method attn_decode --B 64 --T 4096 --H 32 --iters 3
+    python -m gated_delta_rule_40_gb300.profile_case --method attn_decode_q4 --B 128 --T 4096 --H 32 --iters 3
+    python -m gated_delta_rule_40_gb300.profile_case --method attn_chunk_q4 --B 2 --T 8192 --H 32 --iters 3
+    python -m gated_delta_rule_40_gb300.profile_case --method rope --B 1 --T 16384 --H 32 --iters 3
+    python -m gated_delta_rule_40_gb300.profile_case --method rope_bwd --B 1 --T 8192 --H 32 --iters 3
 
 Inputs come from ``kda_inputs`` (same recipe as the tests and the benchmark);
 the workspace is allocated once, so every iteration is exactly the three
@@ -20,7 +24,9 @@ bwdc_gradk_kernel, bwdc_jacobian_kernel and bwdc_dalog_kernel; one for ``kda_dec
 ``--T`` is the token count Tq of the step and whose state is fp32 unless
 ``--bf16-state``; one for ``kda_decode_step``; two for ``kda_attn_fwd`` and ``kda_attn_paged``:
 attn_kernel and attn_join_kernel, with a key/value head to four query heads; ``attn_decode``
-gives each of ``--B`` requests one token over a cache of ``--T``).  A profiler then selects launches by kernel name and index (e.g.
+gives each of ``--B`` requests one token over a cache of ``--T``, ``attn_decode_q4`` over one held in 4 bits,
+``attn_chunk_q4`` a chunk of 1024 tokens; four with the 4-bit cache: attn_q4_few_kernel, attn_kernel,
+attn_join_kernel and attn_q4_join_kernel).  A profiler then selects launches by kernel name and index (e.g.
 ``ncu -k regex:intra_kernel -s 2 -c 1``).  ``--kernel-times`` (kda and bwd) times the
 last iteration's kernels with the library's CUDA events instead and prints them.
 """
@@ -43,7 +49,7 @@ def main() -> None:
     ap.add_argument("--iters", type=int, default=4)
     ap.add_argument("--seed", type=int, default=0)
     ap.add_argument("--method", choices=["kda", "gdn", "la", "bwd", "la_decode", "decode_tokens", "decode", "attn",
-                                         "attn_decode"],
+                                         "attn_decode", "attn_decode_q4", "attn_chunk_q4", "rope", "rope_bwd"],
                     default="kda")
     ap.add_argument("--bf16-state", action="store_true", help="decode_tokens: bf16 state")
     ap.add_argument("--kernel-times", action="store_true",
@@ -92,6 +98,41 @@ def main() -> None:
         torch.cuda.synchronize()
         print(f"kda_la_fwd B={a.B} T={a.T} H={a.H} x{a.iters}: |out| {float(out.float().abs().mean()):.6f} "
               f"|S| {float(fin.abs().mean()):.6f}")
+        return
+    if a.method in ("rope", "rope_bwd"):
+        g = torch.Generator(device="cuda").manual_seed(a.seed)
+        rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+        T, Hkv = a.B * a.T, max(1, a.H // 4)
+        q, k, _ = rnd(T, a.H + 2 * Hkv, 128).split([a.H, Hkv, Hkv], 1)
+        args = (q, k, torch.arange(T, dtype=torch.int32, device="cuda"), 1e4 ** (-torch.arange(64, device="cuda") / 64))
+        w = torch.ones(128, device="cuda")
+        do = (rnd(T, a.H, 128), rnd(T, Hkv, 128))
+        for _ in range(a.iters):
+            if a.method == "rope":
+                out, _ = kda.kda_qk_norm_rope(*args, w, w)
+            else:
+                out = kda.kda_qk_norm_rope_bwd(*args, *do, w, w)["dq"]
+        torch.cuda.synchronize()
+        print(f"{a.method} T={T} H={a.H}/{Hkv} x{a.iters}: {float(out.float().abs().mean()):.6f}")
+        return
+    if a.method in ("attn_decode_q4", "attn_chunk_q4"):
+        g = torch.Generator(device="cuda").manual_seed(a.seed)
+        rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+        Hkv, bs, new = max(1, a.H // 4), 64, 1 if a.method == "attn_decode_q4" else 1024
+        nb = -(-a.T // bs)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        caches = [torch.empty((a.B * nb, Hkv, bs, kda.q4_row_bytes(128)), dtype=torch.uint8, device="cuda") for _ in "kv"]
+        for b in range(a.B):
+            slots = torch.arange(b * nb * bs, (b + 1) * nb * bs, **i32)
+            kda.kda_kv_write_q4(rnd(nb * bs, Hkv, 128), rnd(nb * bs, Hkv, 128), slots, *caches)
+        q = rnd(a.B * new, a.H, 128)
+        table = torch.randperm(a.B * nb, generator=g, device="cuda").to(torch.int32).reshape(a.B, nb)
+        lens, cu = torch.full((a.B,), a.T, **i32), torch.arange(a.B + 1, **i32) * new
+        for _ in range(a.iters):
+            out, lse = kda.kda_attn_paged_q4(q, *caches, table, lens, cu, 128 ** -0.5)
+        torch.cuda.synchronize()
+        print(f"{a.method} B={a.B} T={a.T} H={a.H}/{Hkv} x{a.iters}: |out| {float(out.float().abs().mean()):.6f} "
+              f"lse {float(lse.mean()):.6f}")
         return
     if a.method in ("attn", "attn_decode"):
         g = torch.Generator(device="cuda").manual_seed(a.seed)
