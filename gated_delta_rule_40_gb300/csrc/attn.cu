@@ -555,7 +555,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
         const int piece_row = lane * (AT_KEYS / PIECES);
         const size_t in_codes = r * (D / 2) + 16 * x, in_scales = (size_t)(D / 2) << p.a.block_log2;
         const uint32_t slab_bytes = (uint32_t)q4_row_bytes(D) << p.a.block_log2;
-        uint32_t n = 0;
+        uint32_t slot = 0, use = 0;
         while (ok && w.next(p)) {
             const int keys = w.keys(p);
             // block of the 16 rows that lane h < 8 answers for, of tile t: -1 none that can be had, -2 none wanted
@@ -578,8 +578,8 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                 const size_t piece = __shfl_sync(0xffffffffu, scales_at, piece_row >> 4 & 7) + (piece_row & 15) * PARTS;
                 const bool has_piece = lane < PIECES && (good >> (piece_row >> 4) & 1u);
 #pragma unroll 1
-                for (int which = 0; which < 2; ++which, ++n) {
-                    const uint32_t slot = n % L::PACKED, use = n / L::PACKED, at = slot * L::PACKED_TILE;
+                for (int which = 0; which < 2; ++which) {
+                    const uint32_t at = slot * L::PACKED_TILE;
                     if (use > 0 && !wait(L::CE + slot, (use - 1) & 1)) break;
                     const uint8_t *cache = reinterpret_cast<const uint8_t *>(which ? p.a.v : p.a.k);
 #pragma unroll
@@ -593,6 +593,10 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                     if (lane == 0) {
                         *reinterpret_cast<volatile uint32_t *>(sm + L::GOOD + 4 * slot) = good;
                         mbar_arrive(bar + 8 * (L::CF + slot));
+                    }
+                    if (++slot == (uint32_t)L::PACKED) {
+                        slot = 0;
+                        ++use;
                     }
                 }
                 id = next_id;
@@ -609,7 +613,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
             const int keys = w.keys(p);
             // block id of this lane's box of tile t; looked at only when the tile is loaded, a tile later
             auto page = [&](int t) {
-                if (!PAGED || Q4) return 0;
+                if (!PAGED) return 0;
                 const int key = t * AT_KEYS + lane * box;
                 if (lane >= boxes || key >= keys || t >= w.b) return 0;
                 return p.a.table[(size_t)w.n * p.a.max_blocks + (key >> p.a.block_log2)];

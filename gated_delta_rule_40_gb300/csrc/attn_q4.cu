@@ -15,7 +15,10 @@ cudaError_t launch_attn_q4_few(const AttnQ4Args &a, int most_rows, void *ws, cud
 cudaError_t launch_attn_q4_few_join(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches);
 
 namespace {
-// Rows of a request up to which it is one with few
+// Rows of a request up to which it is one with few.  The kernel for few takes as long for each 16 rows more, the other
+// one as long for any number up to 128.  128 requests over 4096 keys, 32 heads over 8, with 16 rows 188 against 340 us,
+// with 32 350 against 342, with 64 674 against 348; over 1024 keys with 32 rows 110 against 143 us, with 64 194 against
+// 145; a single request over 131072 keys with 32 rows 93 against 105 us, with 64 176 against 106.
 constexpr int F4_MOST_ROWS = 32;
 }  // namespace
 

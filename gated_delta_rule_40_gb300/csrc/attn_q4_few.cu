@@ -698,7 +698,10 @@ cudaError_t join(const F4Params &p, int rows, int grid, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, attn_q4_join_kernel<D>, p);
 }
 
-// Rows a unit has: those that a request has on average, or a single token's where the average is the other kernel's
+// Rows a unit has, 8 or 16: those that a request has on average, or a single token's where the average is the other
+// kernel's.  A key's codes are expanded once a unit, but tiles of 16 columns leave registers for fewer warps.  128
+// requests over 4096 keys, 8 and 16: with 8 rows over 4 heads 77 and 102 us, with 9 131 and 103, with 12 over 8 heads 242
+// and 187, with 32 460 and 350.
 int unit_rows(const AttnQ4Args &a, int most_rows) {
     const int G = a.H_q / a.H_kv;
     const long long rows = ((long long)a.T + a.N - 1) / a.N * G;
@@ -718,7 +721,9 @@ F4Params params(const AttnQ4Args &a, int most_rows, void *ws) {
     p.G = a.H_q / a.H_kv;
     p.over_g = (65536u + p.G - 1) / p.G;
     p.most_rows = most_rows;
-    p.unit_cost = 2;   // 4000 cycles of a warp, whose chunks take 3100 (0, 1, 2, 4: 159, 143, 136, 140 us for 256 decoded tokens)
+    // About 4000 cycles of a warp, whose chunks take 3100.  0, 2 and 4: 256 decoded tokens over 300 keys 39.7, 38.7 and 38.4
+    // us, over 1040 81.2, 80.2 and 80.3; 128 x 16 rows over 1024 67.5, 66.8 and 68.4
+    p.unit_cost = 2;
     p.two20 = 1u << 20;
     p.two4 = 1u << 4;
     p.mask_low = 0x000f000fu; p.bit_low = 0x64006400u;     // codes in bits 0 .. 3: fp16 1024 + c

@@ -38,15 +38,13 @@ __device__ __forceinline__ float q4_inverse(float s) {
     return y * (1.f + 0x1p-12f);
 }
 
-// Bit at which a word holds channel c (0 .. 7)
-__host__ __device__ constexpr int q4_bit(int c) { return 4 * (c >> 1) + 16 * (c & 1); }
-
 // Pair j (channels 2j, 2j + 1) of a word as bf16 16 + c: the code below the leading bit of 16's mantissa
 __device__ __forceinline__ uint32_t q4_raw(uint32_t word, int j) {
     const uint32_t x = j == 0 ? word << 3 : word >> (4 * j - 3);
     return (x & 0x00780078u) | 0x41804180u;
 }
-// (x & mask) | bit, with a mask and a bit that the compiler does not know (it makes two instructions of two it knows)
+// (x & mask) | bit in one instruction: with a mask and a bit that the compiler knows it makes two, so they are arguments
+// of the kernels
 __device__ __forceinline__ uint32_t q4_masked(uint32_t x, uint32_t mask, uint32_t bit) {
     uint32_t y;
     asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(y) : "r"(x), "r"(mask), "r"(bit));

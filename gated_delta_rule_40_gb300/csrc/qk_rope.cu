@@ -19,7 +19,7 @@
 // What bounds it, and what it measured on the GPU: DRAM.  32768 tokens x 40 heads of 128 in 107 us, 6.3 TB/s (0.93 of
 // a copy; a warp a token 112 us, with an address for each row 122 us); gradients of 16384 tokens, which leave as
 // fp32, in 104 us and 2 us for the weights' sum, 6.4 TB/s.  Packed fp32 pairs took 146 us: pairs of registers for
-// them cost more moves than they save.  A call of 64 tokens takes 3.7 us, of which the host needs 17.
+// them cost more moves than they save.  A call of 64 tokens takes 3.1 us, and the host 17.
 #include "qk_rope.h"
 #include "kda_common.cuh"
 
@@ -345,20 +345,34 @@ __global__ __launch_bounds__(256) void qk_rope_dw_kernel(const float *partial, i
 
 namespace {
 constexpr int QR_FWD_CTAS = 152 * 3, QR_BWD_CTAS = 152 * 2;   // resident at once
+constexpr int QR_MAX_CHUNKS = 32;   // looked at
+constexpr int QR_ITEM_COST = 8, QR_LEAST = 4;
 
-// Row groups a warp takes: all of a token's where tokens alone fill the card, fewer where they do not
-void split(const QkRopeArgs &a, int *per, int *chunks) {
+// Row groups a warp takes of a token, and the number of warps that its groups are shared out among: what makes the
+// warps' rounds, each of which costs an item's start and angles (QR_ITEM_COST groups; 2 to 16 do as well) beside its
+// groups, shortest for `warps` resident ones.  Fewer groups than QR_LEAST, those in flight together, make no round
+// shorter: 64 tokens x 40 heads in 3.1 us with 4, 3.6 with 1 and 4.0 with 8, 150 tokens in 3.4, 4.4 and 4.3 us; 4096
+// tokens in 16.1 us, with all groups of a token in one warp 19.9 us.
+void split(const QkRopeArgs &a, int warps, int *per, int *chunks) {
     const int rows = a.D == 128 ? 2 : 4;
     const int groups = (a.H_q + rows - 1) / rows + (a.H_kv + rows - 1) / rows;
-    const long long want = (long long)groups * a.T / (152 * 32);
-    *per = (int)(want < 1 ? 1 : want > groups ? groups : want);
-    *chunks = (groups + *per - 1) / *per;
+    *per = groups;
+    *chunks = 1;
+    long long best = ((long long)a.T + warps - 1) / warps * (max(groups, QR_LEAST) + QR_ITEM_COST);
+    for (int c = 2; c <= groups && c <= QR_MAX_CHUNKS; ++c) {
+        const int each = (groups + c - 1) / c;
+        const long long cost = ((long long)a.T * c + warps - 1) / warps * (max(each, QR_LEAST) + QR_ITEM_COST);
+        if (cost >= best) continue;
+        best = cost;
+        *per = each;
+        *chunks = (groups + each - 1) / each;
+    }
 }
 
 template <int D, bool NORM, bool PAIRS>
 cudaError_t forward(const QkRopeArgs &a, cudaStream_t stream) {
     int per, chunks;
-    split(a, &per, &chunks);
+    split(a, QR_FWD_CTAS * QR_WARPS, &per, &chunks);
     const long long want = ((long long)a.T * chunks + QR_WARPS - 1) / QR_WARPS, grid = want < QR_FWD_CTAS ? want : QR_FWD_CTAS;
     qk_rope_kernel<D, NORM, PAIRS><<<(unsigned)grid, QR_THREADS, 0, stream>>>(a, per, chunks);
     return cudaGetLastError();
@@ -367,7 +381,7 @@ cudaError_t forward(const QkRopeArgs &a, cudaStream_t stream) {
 template <int D, bool NORM, bool PAIRS>
 cudaError_t backward(const QkRopeArgs &a, float *partial, int *n, cudaStream_t stream) {
     int per, chunks;
-    split(a, &per, &chunks);
+    split(a, QR_BWD_CTAS * QR_WARPS, &per, &chunks);
     const long long want = ((long long)a.T * chunks + QR_WARPS - 1) / QR_WARPS;
     *n = (int)(want < QR_BWD_CTAS ? want : QR_BWD_CTAS);
     qk_rope_bwd_kernel<D, NORM, PAIRS><<<(unsigned)*n, QR_THREADS, 0, stream>>>(a, per, chunks, partial);
