@@ -59,7 +59,7 @@
 #include "attn.h"
 #include "kda_common.cuh"
 #include "kda_tma.cuh"
-#include "q4.cuh"
+#include "attn_q4_few.cuh"
 
 namespace kda {
 
@@ -125,7 +125,6 @@ struct AttnParams {
     int G, tile_tokens;   // query heads a key/value head, tokens a tile
     int unit_cost;    // of a unit with two query tiles, in key tiles
     int few_tokens;   // requests with up to so many new tokens are another kernel's (0: none is)
-    bool after_few;       // that kernel was launched before
     uint32_t mask, bit;   // of a code in bits 3 .. 6: 16 + c (q4_masked)
 };
 
@@ -332,10 +331,19 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
     __shared__ int s_n, s_unit;
     __shared__ Request s_req;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    grid_dep_launch();   // the joining kernel may come as soon as CTAs leave
+    if (Q4 && p.few_tokens > 0) {   // all requests with few tokens, as when decoding: 1 us sooner than by the sums below
+        bool any = false;
+        for (int n = tid; n < p.a.N; n += THREADS) any |= p.a.cu[n + 1] - p.a.cu[n] > p.few_tokens;
+        if (!__syncthreads_or(any)) {
+            if (tid == 0) p.join[blockIdx.x].pieces = 0;
+            grid_dep_wait();   // (lengths are checked by the kernel for few)
+            return;
+        }
+    }
     const uint32_t sbase = smem_u32(sm), bar = sbase + L::BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::FLAG);
     const int nseq = p.a.cu ? p.a.N : p.a.B;
-    grid_dep_launch();   // the joining kernel may come as soon as CTAs leave
 
     // barriers and tensor memory, under the latency of the lengths' loads
     bool bad = false;
@@ -964,10 +972,8 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
 // channels of one row; the pieces are laid out with rows innermost, so a warp's loads are whole lines.  Bound by
 // latency, and by L2 where every share cuts a unit of 256 rows (39 MB, 8 us); 2 us for a few decoded tokens.
 template <int D>
-__global__ __launch_bounds__(256, 4) void attn_join_kernel(const AttnParams p) {
+__device__ __forceinline__ void join_units(const AttnParams &p) {
     const int cta = blockIdx.x;
-    grid_dep_launch();
-    grid_dep_wait();   // launched while the pieces are still being computed
     const JoinDesc d = p.join[cta];
     if (d.pieces == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1016,6 +1022,21 @@ __global__ __launch_bounds__(256, 4) void attn_join_kernel(const AttnParams p) {
     if (c8 == 0 && p.a.lse) p.a.lse[out_row] = l != 0.f ? (M + lg2(l)) * (1.f / LOG2E) : -INFINITY;
 }
 
+template <int D>
+__global__ __launch_bounds__(256, 4) void attn_join_kernel(const AttnParams p) {
+    grid_dep_wait();   // launched while the pieces are still being computed
+    join_units<D>(p);
+}
+
+// This kernel's pieces (blockIdx.y below `mine`) and those of the kernel for few rows, which a launch of its own would
+// take 2 us more for
+template <int D>
+__global__ __launch_bounds__(256, 4) void attn_q4_join_both_kernel(const AttnParams p, const F4Params few, int mine) {
+    grid_dep_wait();
+    if ((int)blockIdx.y < mine) join_units<D>(p);
+    else if (blockIdx.z == 0) f4_join<D>(few, blockIdx.x, (blockIdx.y - mine) * 256 + threadIdx.x);
+}
+
 // ---------------------------------------------------------------- host side
 namespace {
 constexpr int AT_MAX_CTAS = 160;
@@ -1056,7 +1077,7 @@ cudaError_t tensor_map(CUtensorMap *m, const void *base, int n, const long long 
 size_t align256_at(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <int D, int MODE>
-cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
+cudaError_t run(const AttnParams &p, const F4Params *few, int few_rows, int grid, cudaStream_t stream) {
     using L = AttnLayout<D, MODE>;
     constexpr bool PAGED = L::PAGED;
     const AttnArgs &a = p.a;
@@ -1098,6 +1119,8 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
         }
         // the same split of an SM's memory for both kernels, so that it is not rearranged between them
         e = cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e == cudaSuccess && MODE == AT_PAGES_Q4)
+            e = cudaFuncSetAttribute(attn_q4_join_both_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e != cudaSuccess) return e;
         ready[dev & 63] = true;
     }
@@ -1111,7 +1134,7 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
         cfg.dynamicSmemBytes = L::BYTES;
         cfg.stream = stream;
         cfg.attrs = attr;
-        cfg.numAttrs = p.after_few ? 1 : 0;
+        cfg.numAttrs = few ? 1 : 0;
         e = cudaLaunchKernelEx(&cfg, attn_kernel<D, MODE>, mq, mk, mv, p);
     } else {
         attn_kernel<D, MODE><<<grid, L::THREADS, L::BYTES, stream>>>(mq, mk, mv, p);
@@ -1127,6 +1150,11 @@ cudaError_t run(const AttnParams &p, int grid, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (few) {
+        const int mine = cfg.gridDim.y;
+        cfg.gridDim.y += (few_rows * (D / 4) + 255) / 256;
+        return cudaLaunchKernelEx(&cfg, attn_q4_join_both_kernel<D>, p, *few, mine);
+    }
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p);
 }
 }  // namespace
@@ -1141,7 +1169,8 @@ size_t attn_workspace_bytes(int D) {
            sizeof(float) * 256 * D * 2 * AT_MAX_CTAS;
 }
 
-static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, bool after_few, void *ws, cudaStream_t stream, int *launches) {
+static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, const F4Params *few, int few_rows, void *ws,
+                          cudaStream_t stream, int *launches) {
     const int sms = sm_count();
     if (sms == 0) return cudaErrorInvalidDevice;
     AttnParams p;
@@ -1162,22 +1191,22 @@ static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, bool after
     p.tile_tokens = AT_ROWS / p.G;
     p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
     p.few_tokens = few_tokens;
-    p.after_few = after_few;
     p.mask = 0x00780078u;
     p.bit = 0x41804180u;
     *launches += cut ? 2 : 1;
-    if (q4) return a.D == 64 ? run<64, AT_PAGES_Q4>(p, sms, stream) : run<128, AT_PAGES_Q4>(p, sms, stream);
-    if (a.lens) return a.D == 64 ? run<64, AT_PAGES>(p, sms, stream) : run<128, AT_PAGES>(p, sms, stream);
-    return a.D == 64 ? run<64, AT_PROMPT>(p, sms, stream) : run<128, AT_PROMPT>(p, sms, stream);
+    auto go = [&](auto run64, auto run128) { return (a.D == 64 ? run64 : run128)(p, few, few_rows, sms, stream); };
+    if (q4) return go(run<64, AT_PAGES_Q4>, run<128, AT_PAGES_Q4>);
+    if (a.lens) return go(run<64, AT_PAGES>, run<128, AT_PAGES>);
+    return go(run<64, AT_PROMPT>, run<128, AT_PROMPT>);
 }
 
 cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches) {
-    return launch(a, false, 0, false, ws, stream, launches);
+    return launch(a, false, 0, nullptr, 0, ws, stream, launches);
 }
 
-cudaError_t launch_attn_q4_many(const AttnArgs &a, int few_tokens, bool after_few, void *ws, cudaStream_t stream,
-                                int *launches) {
-    return launch(a, true, few_tokens, after_few, ws, stream, launches);
+cudaError_t launch_attn_q4_many(const AttnArgs &a, int few_tokens, const F4Params *few, int few_rows, void *ws,
+                                cudaStream_t stream, int *launches) {
+    return launch(a, true, few_tokens, few, few_rows, ws, stream, launches);
 }
 
 }  // namespace kda

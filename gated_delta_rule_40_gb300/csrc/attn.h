@@ -22,9 +22,5 @@ struct AttnArgs {
 bool attn_may_cut(const AttnArgs &a);
 size_t attn_workspace_bytes(int D);
 cudaError_t launch_attn(const AttnArgs &a, void *ws, cudaStream_t stream, int *launches);   // adds to *launches
-// Over a cache held in 4 bits (k and v point to its bytes): the requests with more than few_tokens new tokens.  after_few:
-// the kernel for the others is the stream's latest.
-cudaError_t launch_attn_q4_many(const AttnArgs &a, int few_tokens, bool after_few, void *ws, cudaStream_t stream,
-                                int *launches);
 
 }  // namespace kda

@@ -4,16 +4,12 @@
 // cache's bytes, the others (prompts' chunks) by the products.  Two kernels, each of which finds its own requests
 // among the lengths on the device: attn_q4_few.cu expands codes in registers, as operands of small products, and
 // attn.cu's attn_kernel expands tiles of 128 keys into shared memory for tcgen05.  The second is launched while the
-// first runs and takes over its SMs as they become free; where it finds nothing to do it costs next to nothing.
+// first runs and takes over its SMs as they become free; where it finds nothing to do it costs 2 to 4 us.  One more kernel
+// joins what both have cut.
 #include "attn.h"
-#include "attn_q4.h"
-#include "kda_common.cuh"
+#include "attn_q4_few.cuh"
 
 namespace kda {
-size_t attn_q4_few_workspace_bytes(int D);
-cudaError_t launch_attn_q4_few(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches);
-cudaError_t launch_attn_q4_few_join(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches);
-
 namespace {
 // Rows of a request up to which it is one with few.  The kernel for few takes as long for each 16 rows more, the other
 // one as long for any number up to 128.  128 requests over 4096 keys, 32 heads over 8, with 16 rows 188 against 340 us,
@@ -27,17 +23,22 @@ size_t attn_q4_workspace_bytes(int D) { return attn_q4_few_workspace_bytes(D) + 
 cudaError_t launch_attn_q4(const AttnQ4Args &a, void *ws, cudaStream_t stream, int *launches) {
     const int G = a.H_q / a.H_kv;
     const bool few = G <= F4_MOST_ROWS, many = (long long)a.T * G > F4_MOST_ROWS;
-    cudaError_t e = cudaSuccess;
-    if (few) e = launch_attn_q4_few(a, F4_MOST_ROWS, ws, stream, launches);
-    if (e == cudaSuccess && many) {
+    const F4Params p = attn_q4_few_params(a, F4_MOST_ROWS, ws);
+    const int rows = attn_q4_few_rows(a, F4_MOST_ROWS);
+    if (few) {
+        const cudaError_t e = launch_attn_q4_few(p, rows, stream, launches);
+        if (e != cudaSuccess) return e;
+    }
+    if (many) {
         AttnArgs b = {};
         b.q = a.q; b.k = reinterpret_cast<const uint16_t *>(a.k); b.v = reinterpret_cast<const uint16_t *>(a.v);
         b.out = a.out; b.lse = a.lse; b.cu = a.cu; b.table = a.table; b.lens = a.lens; b.scale = a.scale;
         b.N = a.N; b.B = 1; b.T = a.T; b.H_q = a.H_q; b.H_kv = a.H_kv; b.D = a.D;
         b.num_blocks = a.num_blocks; b.block_log2 = a.block_log2; b.max_blocks = a.max_blocks;
-        e = launch_attn_q4_many(b, F4_MOST_ROWS / G, few, static_cast<char *>(ws) + attn_q4_few_workspace_bytes(a.D), stream, launches);
+        return launch_attn_q4_many(b, F4_MOST_ROWS / G, few ? &p : nullptr, rows,
+                                   static_cast<char *>(ws) + attn_q4_few_workspace_bytes(a.D), stream, launches);
     }
-    return e == cudaSuccess && few ? launch_attn_q4_few_join(a, F4_MOST_ROWS, ws, stream, launches) : e;
+    return launch_attn_q4_few_join(p, rows, stream, launches);
 }
 
 }  // namespace kda

@@ -26,8 +26,9 @@
 // and multiplying take 120 us by themselves, the loads 100 us (the floor is 87 us).  A chunk costs an SM 246 cycles and 604
 // instructions, 285 of them on the logic and shift units (148 cycles at their rate) and 34 products (69); without the
 // outputs, or the scores, the loads bound it (102, 106 us), without the products themselves 128 us.  12 warps of 168
-// registers beat 16 of 128 (147 against 154 us, at the time) and 8 of 255, whose outputs and next scores were interleaved
-// (154 against 136 us).  8-bit products (e4m3 holds a code as it is) turn their operands into fp16 first on this chip.
+// registers beat 16 of 128 (126.8 against 135.5 us for 128 tokens over 4096 keys; 54.6 against 55.4 with heads of 64, which
+// lose no register to memory), so that it is not latency, and 8 of 255, whose outputs and next scores were interleaved (154
+// against 136 us at the time).  8-bit products (e4m3 holds a code as it is) turn their operands into fp16 first on this chip.
 // 4 drafted tokens over 131072 keys, 16 rows: 51 us; 100 decoded tokens with heads of 64 35 us (the smaller chunks' own
 // cost); 4 decoded tokens over up to 1000 keys 8.5 us, all latency.
 #include "attn_q4_few.cuh"
@@ -606,50 +607,10 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
     }
 }
 
-// Joins the pieces of a unit that several CTAs worked on, in the order of the CTAs.
 template <int D>
-__global__ __launch_bounds__(128) void attn_q4_join_kernel(const F4Params p) {
-    const int cta = blockIdx.x;
+__global__ __launch_bounds__(256) void attn_q4_join_kernel(const F4Params p) {
     grid_dep_wait();   // launched while the pieces are still being computed
-    const F4Join d = p.join[cta];
-    const int i = blockIdx.y * 128 + threadIdx.x, row = i / (D / 4), piece = i % (D / 4);
-    if (d.pieces == 0 || row >= d.rows) return;
-    auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
-    float M = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < d.pieces; k0 += 4) {   // four at a time, so that their loads are in flight together
-        float2 ml[4];
-        float4 x[4];
-        float top = M;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            ml[k] = make_float2(-INFINITY, 0.f);
-            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k0 + k < d.pieces) {
-                ml[k] = p.ml[slot(k0 + k) * F4_MAX_ROWS + row];
-                x[k] = *reinterpret_cast<const float4 *>(p.o + (slot(k0 + k) * F4_MAX_ROWS + row) * D + 4 * piece);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
-        const float ref = top == -INFINITY ? 0.f : top, f0 = ex2(M - ref);
-        l *= f0;
-        o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
-        M = top;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float f = ex2(ml[k].x - ref);
-            l += f * ml[k].y;
-            o.x += f * x[k].x; o.y += f * x[k].y; o.z += f * x[k].z; o.w += f * x[k].w;
-        }
-    }
-    const int row0 = p.a.cu[d.n], fresh = p.a.cu[d.n + 1] - row0, flat = d.row0 + row, tok = flat / p.G;
-    const size_t at = (size_t)(row0 + tok) * p.a.H_q + d.hk * p.G + (flat - tok * p.G);
-    if (p.a.lens[d.n] - fresh + tok + 1 <= 0) l = 0.f;
-    const float inv = l != 0.f ? 1.f / l : 0.f, ref = M == -INFINITY ? 0.f : M;
-    *reinterpret_cast<uint2 *>(p.a.out + at * D + 4 * piece) =
-        l == 0.f ? make_uint2(0, 0) : make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (piece == 0 && p.a.lse) p.a.lse[at] = l == 0.f ? -INFINITY : (ref + lg2(l)) * (1.f / LOG2E);
+    f4_join<D>(p, blockIdx.x, blockIdx.y * 256 + threadIdx.x);
 }
 
 // ---------------------------------------------------------------- host side
@@ -687,8 +648,8 @@ cudaError_t run(const F4Params &p, int grid, cudaStream_t stream) {
 template <int D>
 cudaError_t join(const F4Params &p, int rows, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, (rows * (D / 4) + 127) / 128);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(grid, (rows * (D / 4) + 255) / 256);
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -697,18 +658,19 @@ cudaError_t join(const F4Params &p, int rows, int grid, cudaStream_t stream) {
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_q4_join_kernel<D>, p);
 }
+}  // namespace
 
 // Rows a unit has, 8 or 16: those that a request has on average, or a single token's where the average is the other
 // kernel's.  A key's codes are expanded once a unit, but tiles of 16 columns leave registers for fewer warps.  128
 // requests over 4096 keys, 8 and 16: with 8 rows over 4 heads 77 and 102 us, with 9 131 and 103, with 12 over 8 heads 242
 // and 187, with 32 460 and 350.
-int unit_rows(const AttnQ4Args &a, int most_rows) {
+int attn_q4_few_rows(const AttnQ4Args &a, int most_rows) {
     const int G = a.H_q / a.H_kv;
     const long long rows = ((long long)a.T + a.N - 1) / a.N * G;
     return (rows > most_rows ? G : rows) <= 8 ? 8 : 16;
 }
 
-F4Params params(const AttnQ4Args &a, int most_rows, void *ws) {
+F4Params attn_q4_few_params(const AttnQ4Args &a, int most_rows, void *ws) {
     F4Params p;
     p.a = a;
     char *base = static_cast<char *>(ws);
@@ -731,27 +693,24 @@ F4Params params(const AttnQ4Args &a, int most_rows, void *ws) {
     p.bit_bf16 = 0x43004300u;                              // codes in bits 0 .. 3: bf16 128 + c
     return p;
 }
-}  // namespace
 
 size_t attn_q4_few_workspace_bytes(int D) {
     return align256_f4(sizeof(F4Join) * F4_MAX_CTAS) + align256_f4(sizeof(float2) * 2 * F4_MAX_CTAS * F4_MAX_ROWS) +
            sizeof(float) * 2 * F4_MAX_CTAS * F4_MAX_ROWS * D;
 }
 
-cudaError_t launch_attn_q4_few(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches) {
+cudaError_t launch_attn_q4_few(const F4Params &p, int rows, cudaStream_t stream, int *launches) {
     const int sms = sm_count();
     if (sms == 0) return cudaErrorInvalidDevice;
-    const F4Params p = params(a, most_rows, ws);
     ++*launches;
-    if (unit_rows(a, most_rows) == 8) return a.D == 64 ? run<64, 8>(p, sms, stream) : run<128, 8>(p, sms, stream);
-    return a.D == 64 ? run<64, 16>(p, sms, stream) : run<128, 16>(p, sms, stream);
+    if (rows == 8) return p.a.D == 64 ? run<64, 8>(p, sms, stream) : run<128, 8>(p, sms, stream);
+    return p.a.D == 64 ? run<64, 16>(p, sms, stream) : run<128, 16>(p, sms, stream);
 }
 
-cudaError_t launch_attn_q4_few_join(const AttnQ4Args &a, int most_rows, void *ws, cudaStream_t stream, int *launches) {
-    const F4Params p = params(a, most_rows, ws);
-    const int rows = unit_rows(a, most_rows), sms = sm_count();
+cudaError_t launch_attn_q4_few_join(const F4Params &p, int rows, cudaStream_t stream, int *launches) {
+    const int sms = sm_count();
     ++*launches;
-    return a.D == 64 ? join<64>(p, rows, sms, stream) : join<128>(p, rows, sms, stream);
+    return p.a.D == 64 ? join<64>(p, rows, sms, stream) : join<128>(p, rows, sms, stream);
 }
 
 }  // namespace kda

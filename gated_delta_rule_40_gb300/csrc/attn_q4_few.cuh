@@ -147,4 +147,62 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 
+// Joins the pieces of a unit that several CTAs worked on, in the order of the CTAs.
+// Thread i of D / 4 for each row.
+template <int D>
+__device__ __forceinline__ void f4_join(const F4Params &p, int cta, int i) {
+    const F4Join d = p.join[cta];
+    const int row = i / (D / 4), piece = i % (D / 4);
+    if (d.pieces == 0 || row >= d.rows) return;
+    auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)); };
+    float M = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < d.pieces; k0 += 4) {   // four at a time, so that their loads are in flight together
+        float2 ml[4];
+        float4 x[4];
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k < d.pieces) {
+                ml[k] = p.ml[slot(k0 + k) * F4_MAX_ROWS + row];
+                x[k] = *reinterpret_cast<const float4 *>(p.o + (slot(k0 + k) * F4_MAX_ROWS + row) * D + 4 * piece);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+        const float ref = top == -INFINITY ? 0.f : top, f0 = ex2(M - ref);
+        l *= f0;
+        o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+        M = top;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float f = ex2(ml[k].x - ref);
+            l += f * ml[k].y;
+            o.x += f * x[k].x; o.y += f * x[k].y; o.z += f * x[k].z; o.w += f * x[k].w;
+        }
+    }
+    const int row0 = p.a.cu[d.n], fresh = p.a.cu[d.n + 1] - row0, flat = d.row0 + row, tok = flat / p.G;
+    const size_t at = (size_t)(row0 + tok) * p.a.H_q + d.hk * p.G + (flat - tok * p.G);
+    if (p.a.lens[d.n] - fresh + tok + 1 <= 0) l = 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f, ref = M == -INFINITY ? 0.f : M;
+    *reinterpret_cast<uint2 *>(p.a.out + at * D + 4 * piece) =
+        l == 0.f ? make_uint2(0, 0) : make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (piece == 0 && p.a.lse) p.a.lse[at] = l == 0.f ? -INFINITY : (ref + lg2(l)) * (1.f / LOG2E);
+}
+
+int attn_q4_few_rows(const AttnQ4Args &a, int most_rows);   // of a unit
+F4Params attn_q4_few_params(const AttnQ4Args &a, int most_rows, void *ws);
+size_t attn_q4_few_workspace_bytes(int D);
+// The kernel for few rows, and the joining of its pieces where no kernel for chunks follows
+cudaError_t launch_attn_q4_few(const F4Params &p, int rows, cudaStream_t stream, int *launches);
+cudaError_t launch_attn_q4_few_join(const F4Params &p, int rows, cudaStream_t stream, int *launches);
+// Attention of the requests with more than few_tokens new tokens (k and v of `a` point to the cache's bytes).  Where the
+// kernel for the others is the stream's latest, `few` has its arguments, and its pieces are joined together with this
+// one's; NULL: none was launched.
+struct AttnArgs;
+cudaError_t launch_attn_q4_many(const AttnArgs &a, int few_tokens, const F4Params *few, int few_rows, void *ws,
+                                cudaStream_t stream, int *launches);
+
 }  // namespace kda

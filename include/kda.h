@@ -26,7 +26,8 @@
  * Conventions for every entry point
  * ---------------------------------
  *  - All tensor pointers are DEVICE pointers (kda_fwd_host's are host
- *    pointers) to contiguous row-major data, owned by the caller; the library
+ *    pointers) to contiguous row-major data (tokens may lie apart where a call takes
+ *    a stride), owned by the caller; the library
  *    keeps no pointer after a call returns.  bf16 data is passed as its 16-bit
  *    pattern (kda_bf16_t).
  *  - Kernels run on the calling thread's current CUDA device: the device
@@ -61,7 +62,8 @@ enum {
                                     cu_seqlens with B != 1, misaligned pointer, more than
                                     2^31 - 1 tokens (B * T), sequences * H_v above
                                     2^29 - 1 (chunked calls) or B * H_v above 2^31 - 1
-                                    (decode calls): work items carry 32-bit indices */
+                                    (decode calls) or T * H_kv above it (the 4-bit cache's
+                                    store and read): work items carry 32-bit indices */
     KDA_ERR_UNSUPPORTED = -2,    /* K != 128 or V != 128 */
     KDA_ERR_CUDA = -3,           /* a CUDA runtime call or kernel launch failed */
     KDA_ERR_DEVICE_TIMEOUT = -4, /* (status word) a bounded device-side wait gave up */
@@ -569,7 +571,8 @@ int kda_kernel_times(float *ms, const char **names, int max_n);
 
 /*
  * The allocating entry points (kda_fwd, kda_fwd_bf16_state,
- * kda_fwd_scalar_gate, kda_fwd_host, kda_bwd, kda_la_fwd) take their device
+ * kda_fwd_scalar_gate, kda_fwd_host, kda_bwd, kda_la_fwd, kda_attn_fwd,
+ * kda_attn_paged, kda_attn_paged_q4, kda_qk_norm_rope_bwd) take their device
  * workspace from one stream-ordered memory pool per device, created on first
  * use with an unbounded release threshold: what a call frees on its stream
  * stays mapped in the pool after the caller synchronises, and the next call

@@ -245,6 +245,53 @@ def test_bits_repeat_streams_workspaces_and_graphs():
         c.check(o, None)
 
 
+def test_streams_at_once():
+    """Calls that overlap on two streams, eager ones and graphs, have a workspace each."""
+    kda = _kda()
+    cs = [Q.PagedQ4([3000, 40, 0, 900], [1, 30, 5, 2], 8, 2, 128, 16, seed=s) for s in (1, 2)]
+    want = [c.run() for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    args = [(c.q.cuda(), *(x.cuda() for x in c.caches), c.table.cuda(), c.lens.cuda(),
+             torch.tensor(c.cu, dtype=torch.int32, device="cuda"), c.scale) for c in cs]
+    graphs = []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, kda.kda_attn_paged_q4(*a)))
+    torch.cuda.synchronize()
+    got = [[kda.kda_attn_paged_q4(*a, stream=s) for a, s in zip(args, streams)] for _ in range(10)]
+    for _ in range(10):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for pair in got + [[o for _, o in graphs]]:
+        for (o, l), (wo, wl) in zip(pair, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_blocks_past_32_bits_of_bytes(D):
+    """A cache of more than 2^32 bytes whose last blocks hold what a small one's do: the same bits."""
+    kda = _kda()
+    c = Q.PagedQ4([300, 40, 130, 500], [1, 60, 4, 100], 8, 2, D, 64, seed=5)
+    out, lse = c.run()
+    c.check(out, lse)
+    small = [x.cuda() for x in c.caches]
+    n = small[0].shape[0]
+    blocks = 2 ** 32 // small[0][0].numel() + n + 5
+    first = blocks - n
+    assert first * small[0][0].numel() >= 2 ** 32
+    far = []
+    for x in small:
+        far.append(torch.full((blocks, *x.shape[1:]), 255, dtype=torch.uint8, device="cuda"))
+        far[-1][first:] = x
+    o, l = kda.kda_attn_paged_q4(c.q.cuda(), *far, (c.table + first).cuda(), c.lens.cuda(),
+                                 torch.tensor(c.cu, dtype=torch.int32, device="cuda"), c.scale)
+    assert torch.equal(o, out) and torch.equal(l, lse)
+
+
 def test_after_the_store():
     """Plan, store, attention, step by step: a prompt in one step or in chunks gives the same cache and answers
     within the bounds."""

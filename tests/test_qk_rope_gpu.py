@@ -269,3 +269,52 @@ def test_feeds_store_and_attention():
     # 4 2^-8 sqrt(D) / 4 = 2^-8 11.4 at most, the weights by a factor e^(2 x that), the outputs' own rounding is 2 x 2^-8
     bound = (math.exp(2 * 2.0 ** -8 * 11.4) - 1 + 4 * 2.0 ** -8) * f[:, H + Hkv:].double().abs().max()
     assert (outs[0] - outs[1]).abs().max() <= bound
+
+
+def test_tokens_past_32_bits_of_elements():
+    """Rows past 2^31 elements of the inputs and outputs, and stored from there: the same bits as alone."""
+    kda = _kda()
+    H, Hkv, D = 32, 8, 128
+    T = 2 ** 31 // (H * D) + 3000
+    x = torch.zeros((T, H + 2 * Hkv, D), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    n = 2900
+    x[-n:] = torch.randn((n, H + 2 * Hkv, D), generator=g, device="cuda").to(torch.bfloat16)
+    q, k, v = x.split([H, Hkv, Hkv], 1)
+    pos = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    pos[-n:] = torch.arange(n, dtype=torch.int32, device="cuda") + 7
+    freqs, w = torch.rand(32, generator=g, device="cuda"), torch.rand(128, generator=g, device="cuda")
+    assert q.stride(0) * (T - n) >= 2 ** 31 and H * D * (T - n) >= 2 ** 31
+    oq, ok = kda.kda_qk_norm_rope(q, k, pos, freqs, w, w)
+    aq, ak = kda.kda_qk_norm_rope(q[-n:], k[-n:], pos[-n:], freqs, w, w)
+    assert torch.equal(oq[-n:], aq) and torch.equal(ok[-n:], ak)
+    far = kda.kda_qk_norm_rope_bwd(q, k, pos, freqs, oq, ok, w, w)
+    near = kda.kda_qk_norm_rope_bwd(q[-n:], k[-n:], pos[-n:], freqs, aq, ak, w, w)
+    assert torch.equal(far["dq"][-n:], near["dq"]) and torch.equal(far["dk"][-n:], near["dk"])
+    for name, heads in (("dq_weight", H), ("dk_weight", Hkv)):
+        # sums in other orders, each a chain of at most 200 additions of 2^-24, of terms whose absolute values add to at
+        # most 128 for each of n heads rows (two rows' norms, sqrt(128) at most)
+        assert (far[name] - near[name]).abs().max() <= 2 * 200 * 2.0 ** -24 * 128 * n * heads
+    caches = [torch.zeros((64, Hkv, 64, kda.q4_row_bytes(D)), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    kda.kda_kv_write_q4(ok, v, pos, *caches[:2])
+    kda.kda_kv_write_q4(ak, v[-n:], pos[-n:], *caches[2:])
+    assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3]) and caches[0].any()
+
+
+def test_streams_at_once():
+    kda = _kda()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    freqs, w = torch.rand(32, generator=g, device="cuda"), torch.rand(128, generator=g, device="cuda")
+    args = []
+    for T in (3000, 777):
+        x = torch.randn((T, 24, 128), generator=g, device="cuda").to(torch.bfloat16)
+        q, k, _ = x.split([16, 4, 4], 1)
+        args.append((q, k, torch.arange(T, dtype=torch.int32, device="cuda"), freqs, q.contiguous(), k.contiguous(), w, w))
+    want = [kda.kda_qk_norm_rope_bwd(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = [[kda.kda_qk_norm_rope_bwd(*a, stream=s) for a, s in zip(args, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert all(torch.equal(a[name], b[name]) for name in b)
