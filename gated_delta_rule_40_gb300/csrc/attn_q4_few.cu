@@ -12,9 +12,10 @@
 // for the scores, 16 channels x 16 keys times 8 queries for the outputs, whose operands are expanded from codes in
 // registers.  tcgen05, whose rows are 128, would take operands from shared or tensor memory, which costs more here than
 // what they compute.
-//   scores   codes as fp16 in place, 1024 + c or 64 + c, one shift a word of 8; q as fp16 times a power of two, which keeps
-//            every channel (bf16 has fewer bits); the sums of q that the 1032 and 72 add are taken off, and the keys'
-//            scale is applied, for each block of 32 channels in fp32
+//   scores   codes as fp16 in place, without an exponent (2^-24 c or 2^-20 c), one mask each and one shift a word of 8; q as
+//            fp16 times a power of two, which keeps every channel; 8 times the sum of q is taken off, and the keys' scale
+//            is applied, for each block of 32 channels in fp32.  (With an exponent, 1024 + c and 64 + c, the sums are
+//            exact to 2^-22 of 1039 instead of 15 times the queries' sum: lse was 1e-4 off.)
 //   weights  2^(s c - m), c = scale log2(e), with the reference m of the piece's first chunk, which moves when a sum of
 //            weights passes 2^16; rounded to bf16 as operands, like attn.cu's
 //   outputs  codes of two keys in the halves of a register, 128 + c, times the keys' scales less 128 of them: c s, a bf16
@@ -260,12 +261,9 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
             v_at[i] = L::CODES + r * ROWB +
                       (D == 128 ? (((g >> 1) ^ (r >> 1 & 3)) << 4) + 8 * (g & 1) : (((g >> 2) ^ (r >> 2 & 1)) << 4) + 4 * (g & 3));
         }
-        // Pair j of a word as fp16: 1024 + c where the code is in bits 0 .. 3 of each half (j = 0, and j = 2 8 bits further
-        // down), 64 + c where it is in bits 4 .. 7 (j = 1, 3)
-        auto codes_f16 = [&](uint32_t word, int j) {
-            const uint32_t x = j < 2 ? word : word >> 8;
-            return j & 1 ? q4_masked(x, p.mask_high, p.bit_high) : q4_masked(x, p.mask_low, p.bit_low);
-        };
+        // Pair j of a word as fp16, below the normal numbers: 2^-24 c where the code is in bits 0 .. 3 of each half (j = 0,
+        // and j = 2 8 bits further down), 2^-20 c where it is in bits 4 .. 7 (j = 1, 3)
+        auto codes_f16 = [](uint32_t word, int j) { return (j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu); };
         // which scale bytes of two keys' words make a pair
         const uint32_t blk = D == 128 ? g >> 1 : g >> 2, second = D == 128 ? 4 + blk : 2 + blk;
         const uint32_t sel = odd ? second | blk << 8 : blk | second << 8;
@@ -273,9 +271,9 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
         while (w.next(p, ROWS)) {
             {
                 // ---- queries: columns g of the products, as fp16 with the row's largest magnitude between 2^14 and 2^15, so
-                // that a channel is itself down to 2^-28 of that.  A lane's channels are those of its words of a key, 8 in
-                // each block of 32.  Codes come as 1024 + c and 64 + c, so that a block's product is off by 1032 and 72 times
-                // the queries' sums.
+                // that a channel is itself down to 2^-27 of that.  A lane's channels are those of its words of a key, 8 in
+                // each block of 32.  Codes come as 2^-24 c and 2^-20 c = 2^-24 (c 2^4), whose queries are 2^-4 of the others,
+                // and c is 8 + n: a block's product is off by 2^-24 8 times the queries' sum.
                 uint32_t q[TILES][BLOCKS][4];
                 float2 excess[TILES][BLOCKS], m[TILES], minus_m[TILES], l[TILES], factor[TILES];   // minus_m: 0 for -infinity
                 int limit[TILES][2];
@@ -306,8 +304,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float x0 = bf16_lo(q[n][b][j]) * up, x1 = bf16_hi(q[n][b][j]) * up;
-                            q[n][b][j] = pack_f16x2(x0, x1);
-                            sum = fmaf(j & 1 ? -72.f : -1032.f, x0 + x1, sum);
+                            q[n][b][j] = j & 1 ? pack_f16x2(x0 * 0x1p-4f, x1 * 0x1p-4f) : pack_f16x2(x0, x1);
+                            sum = fmaf(-0x1p-21f, x0 + x1, sum);
                         }
                         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -355,8 +353,9 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                         for (int b = 0; b < BLOCKS; ++b) {
                             const uint32_t x0 = word(stage + k_at[b] + 16 * mt * ROWB), x1 = word(stage + k_at[b] + (16 * mt + 8) * ROWB);
-                            const float s0 = __uint_as_float(__byte_perm(w0, 0, 0x4440 | b) * p.two20 + 0x38000000u);
-                            const float s1 = __uint_as_float(__byte_perm(w1, 0, 0x4440 | b) * p.two20 + 0x38000000u);
+                            // the scales times 2^24
+                            const float s0 = __uint_as_float(__byte_perm(w0, 0, 0x4440 | b) * p.two20 + 0x44000000u);
+                            const float s1 = __uint_as_float(__byte_perm(w1, 0, 0x4440 | b) * p.two20 + 0x44000000u);
                             uint32_t a[8];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -497,7 +496,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 auto value = [&](uint32_t word, int pair) {
-                                    return q4_value(q4_masked(word >> (4 * j), p.mask_low, p.bit_bf16), s2[pair], off[pair]);
+                                    return q4_value(q4_masked(word >> (4 * j), p.mask, p.bit), s2[pair], off[pair]);
                                 };
                                 const uint32_t a0 = value(lo01, 0), a1 = value(hi01, 0), a2 = value(lo23, 1), a3 = value(hi23, 1);
 #pragma unroll
@@ -688,9 +687,7 @@ F4Params attn_q4_few_params(const AttnQ4Args &a, int most_rows, void *ws) {
     p.unit_cost = 2;
     p.two20 = 1u << 20;
     p.two4 = 1u << 4;
-    p.mask_low = 0x000f000fu; p.bit_low = 0x64006400u;     // codes in bits 0 .. 3: fp16 1024 + c
-    p.mask_high = 0x00f000f0u; p.bit_high = 0x54005400u;   // codes in bits 4 .. 7: fp16 64 + c
-    p.bit_bf16 = 0x43004300u;                              // codes in bits 0 .. 3: bf16 128 + c
+    p.mask = 0x000f000fu; p.bit = 0x43004300u;   // codes in bits 0 .. 3: bf16 128 + c
     return p;
 }
 

@@ -49,7 +49,7 @@ struct F4Params {
     int unit_cost;    // of a unit, in chunks
     // Constants that the compiler does not know: a product with a power of two stays one (the multiplier has room, the
     // shifter has not), and a mask with a leading bit stays one instruction.
-    uint32_t two20, two4, mask_low, bit_low, mask_high, bit_high, bit_bf16;
+    uint32_t two20, two4, mask, bit;
 };
 
 // Token of a request's row (exact: row < 512, G <= 128)
