@@ -18,9 +18,10 @@
 //            exact to 2^-22 of 1039 instead of 15 times the queries' sum: lse was 1e-4 off.)
 //   weights  2^(s c - m), c = scale log2(e), with the reference m of the piece's first chunk, which moves when a sum of
 //            weights passes 2^16; rounded to bf16 as operands, like attn.cu's
-//   outputs  codes of two keys in the halves of a register, 128 + c, times the keys' scales less 128 of them: c s, a bf16
-//            number; 8 times the sum of p s, a product of its own, is taken off at the end.  Values reach to 9e5, which
-//            fp16 does not hold (tried with bf16 for what it does not: the same time)
+//   outputs  codes of two keys in the halves of a register, as bf16 without an exponent, times the keys' scales less 8 of
+//            them: 2^-23 n s, a bf16 number, for weights that are 2^23 times as large.  (With an exponent, 128 + c, whose
+//            offset a product of its own takes off: two shifts more a pair of words.)  Values reach to 9e5, which fp16
+//            does not hold (tried with bf16 for what it does not: the same time)
 // Lanes read what they expand from 16-byte pieces that are exchanged by the row's place, without bank conflicts.
 //
 // What bounds it, and what it measured on the GPU.  256 decoded tokens with 0.59 GB of cache in 130 us, 4.5 TB/s: expanding
@@ -277,7 +278,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                 uint32_t q[TILES][BLOCKS][4];
                 float2 excess[TILES][BLOCKS], m[TILES], minus_m[TILES], l[TILES], factor[TILES];   // minus_m: 0 for -infinity
                 int limit[TILES][2];
-                float o[MT][TILES][4], z[TILES][4];
+                float o[MT][TILES][4];
 #pragma unroll
                 for (int n = 0; n < TILES; ++n) {
                     const bool real = 8 * n + g < w.rows;
@@ -317,11 +318,9 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     m[n] = make_float2(-INFINITY, -INFINITY);
                     minus_m[n] = l[n] = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        z[n][x] = 0.f;
+                    for (int x = 0; x < 4; ++x)
 #pragma unroll
                         for (int i = 0; i < MT; ++i) o[i][n][x] = 0.f;
-                    }
                 }
                 const int lowest = w.r.keys - w.r.fresh + f4_token(p, w.first) + 1;   // of the rows' limits
 
@@ -438,8 +437,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                                 top.x = fmaxf(top.x, s[n][i].x * fac[n].x);
                                 top.y = fmaxf(top.y, s[n][i].y * fac[n].y);
                             }
-                            f[n].x = raise(top.x, m[n].x, minus_m[n].x, l[n].x);
-                            f[n].y = raise(top.y, m[n].y, minus_m[n].y, l[n].y);
+                            f[n].x = raise(top.x - F4_LOG_UP, m[n].x, minus_m[n].x, l[n].x);
+                            f[n].y = raise(top.y - F4_LOG_UP, m[n].y, minus_m[n].y, l[n].y);
                         }
                         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -447,7 +446,6 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                                 for (int x = 0; x < 4; ++x) {
                                     const float fx = x & 1 ? f[n].y : f[n].x;
-                                    z[n][x] *= fx;
 #pragma unroll
                                     for (int i = 0; i < MT; ++i) o[i][n][x] *= fx;
                                 }
@@ -456,7 +454,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     }
 #pragma unroll
                     for (int n = 0; n < TILES; ++n) l[n] = __fadd2_rn(l[n], sum[n]);
-                    // ---- outputs: codes times scale in bf16 (exact), 8 times the scales' own sum taken off at the end
+                    // ---- outputs: 2^-23 n s as bf16 (exact) from codes in place.  Bits 0 .. 7 of a bf16 alone are an integer times
+                    // 2^-133, below the normal numbers and in the first ones alike: 2^-133 c, or 2^-129 c from bits 4 .. 7.
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
                         uint32_t bq[TILES][2];
@@ -465,17 +464,20 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             bq[n][0] = transpose_8x8(pk[n][2 * mt]);
                             bq[n][1] = transpose_8x8(pk[n][2 * mt + 1]);
                         }
-                        uint32_t s2[2];
+                        uint32_t s_even[2], s_odd[2], off[2];   // 2^110 s, 2^106 s, -8 2^-23 s
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
+                            uint32_t x;
                             if (D == 128) {
-                                const uint2 x = pair(v_scales + (16 * mt + 8 * i) * 4);
-                                s2[i] = (__byte_perm(x.x, x.y, sel) & 0x00ff00ffu) * p.two4 + 0x38003800u;
+                                const uint2 y = pair(v_scales + (16 * mt + 8 * i) * 4);
+                                x = __byte_perm(y.x, y.y, sel) & 0x00ff00ffu;
                             } else {
-                                s2[i] = (__byte_perm(word(v_scales + (16 * mt + 8 * i) * 2), 0, sel) & 0x00ff00ffu) * p.two4 + 0x38003800u;
+                                x = __byte_perm(word(v_scales + (16 * mt + 8 * i) * 2), 0, sel) & 0x00ff00ffu;
                             }
+                            s_even[i] = x * p.two4 + 0x6f006f00u;
+                            s_odd[i] = x * p.two4 + 0x6d006d00u;
+                            off[i] = x * p.two4 + 0xae00ae00u;
                         }
-                        const uint32_t off[2] = {s2[0] + 0x83808380u, s2[1] + 0x83808380u};   // -128 s
                         uint32_t v[4][D / 64];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -488,15 +490,14 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             }
                         }
 #pragma unroll
-                        for (int n = 0; n < TILES; ++n) mma_bf16(z[n], s2[0], s2[0], s2[1], s2[1], bq[n][0], bq[n][1]);
-#pragma unroll
                         for (int x = 0; x < D / 64; ++x) {
                             const uint32_t lo01 = __byte_perm(v[0][x], v[1][x], 0x5410), hi01 = __byte_perm(v[0][x], v[1][x], 0x7632);
                             const uint32_t lo23 = __byte_perm(v[2][x], v[3][x], 0x5410), hi23 = __byte_perm(v[2][x], v[3][x], 0x7632);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 auto value = [&](uint32_t word, int pair) {
-                                    return q4_value(q4_masked(word >> (4 * j), p.mask, p.bit), s2[pair], off[pair]);
+                                    const uint32_t x = (j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
+                                    return q4_value(x, j & 1 ? s_odd[pair] : s_even[pair], off[pair]);
                                 };
                                 const uint32_t a0 = value(lo01, 0), a1 = value(hi01, 0), a2 = value(lo23, 1), a3 = value(hi23, 1);
 #pragma unroll
@@ -520,12 +521,11 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                         for (int lanes = 4; lanes < 32; lanes <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, lanes);
                         const int row = 8 * n + 2 * t + x;
-                        const float zz = 8.f * z[n][x];
                         float y[D / 8];   // channels (D / 8) g ..
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            y[2 * i] = o[i][n][x] - zz;
-                            y[2 * i + 1] = o[i][n][2 + x] - zz;
+                            y[2 * i] = o[i][n][x] * F4_UP;
+                            y[2 * i + 1] = o[i][n][2 + x] * F4_UP;
                         }
                         if (!whole) {
                             if (g == 0) sts_f2(sbase + L::ML + ((warp * 2 + part) * ROWS + row) * 8, make_float2(ref, sum));
@@ -687,7 +687,6 @@ F4Params attn_q4_few_params(const AttnQ4Args &a, int most_rows, void *ws) {
     p.unit_cost = 2;
     p.two20 = 1u << 20;
     p.two4 = 1u << 4;
-    p.mask = 0x000f000fu; p.bit = 0x43004300u;   // codes in bits 0 .. 3: bf16 128 + c
     return p;
 }
 

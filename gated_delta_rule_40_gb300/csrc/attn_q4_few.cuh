@@ -11,7 +11,8 @@ constexpr long long F4_MAX_KEYS = 0x7fffff00;
 constexpr int F4_SHARE = 4;            // chunks a CTA has at least
 constexpr int F4_MAX_CTAS = 160;
 constexpr int F4_MAX_ROWS = 16;        // rows a unit can have
-constexpr float F4_MOST = 65536.0f;    // sum of a lane's weights that makes a warp look at its maximum
+constexpr float F4_LOG_UP = 23.f, F4_UP = 8388608.f;   // weights are 2^23 and more, values 2^-23 of what they are
+constexpr float F4_MOST = 65536.f * F4_UP;             // sum of a lane's weights that makes a warp look at its maximum
 
 // Rows a unit has at most, and how a CTA is made for them
 template <int D, int ROWS>
@@ -47,9 +48,9 @@ struct F4Params {
     uint32_t over_g;  // 2^16 / G, rounded up: (row over_g) >> 16 is row / G for the rows of this kernel's requests
     int most_rows;    // requests with more rows are another kernel's
     int unit_cost;    // of a unit, in chunks
-    // Constants that the compiler does not know: a product with a power of two stays one (the multiplier has room, the
-    // shifter has not), and a mask with a leading bit stays one instruction.
-    uint32_t two20, two4, mask, bit;
+    // Powers of two that the compiler does not know, so that products with them stay products: the multiplier has room, the
+    // shifter has not
+    uint32_t two20, two4;
 };
 
 // Token of a request's row (exact: row < 512, G <= 128)
