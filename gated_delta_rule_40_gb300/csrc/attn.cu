@@ -125,7 +125,7 @@ struct AttnParams {
     int G, tile_tokens;   // query heads a key/value head, tokens a tile
     int unit_cost;    // of a unit with two query tiles, in key tiles
     int few_tokens;   // requests with up to so many new tokens are another kernel's (0: none is)
-    uint32_t mask, bit;   // of a code in bits 3 .. 6: 16 + c (q4_masked)
+    uint32_t two4;    // 16 (q4_scales)
 };
 
 // Sum of floor((a i + b) / m) over 0 <= i < n, a, m >= 1 (Euclid's descent on the lattice points under a
@@ -500,7 +500,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
     }
     if (Q4 && warp >= AT_THREADS / 32) {
         // ------------------------------------------------------------ expander (4-bit pages)
-        // 4 warps write a tile's values as bf16, which they are, into the ring.  A lane takes 16 bytes of codes, 32
+        // 4 warps write 2^-23 of a tile's values as bf16, exactly, into the ring.  A lane takes 16 bytes of codes, 32
         // channels under one scale, of row 8 i + lane % 8 of its warp's 32 rows: 8 lanes with neighbouring rows write
         // to different banks.  Rows past the unit's last key, and rows without a block, become zeros.
         constexpr int PARTS = D / 32, ROWS_AT_ONCE = 32 / PARTS, TIMES = 32 / ROWS_AT_ONCE;   // 16-byte parts of a row
@@ -527,14 +527,14 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                             codes = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
                             scale = 0;
                         }
-                        const uint32_t s2 = q4_scale2(scale * 0x00010001u), o2 = q4_offset2(s2);
+                        const Q4Scale s2 = q4_scales(scale * 0x00010001u, p.two4);
                         const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {   // 8 channels, 16 bytes
                             uint32_t y[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                y[j] = q4_value(q4_masked(j ? word[x] >> (4 * j - 3) : word[x] << 3, p.mask, p.bit), s2, o2);
+                                y[j] = q4_pair(word[x], j, s2);
                             *reinterpret_cast<uint4 *>(tile + (at >> 3) * 1024 + (at & 7) * 128 + ((((part & 1) * 4 + x) ^ (at & 7)) << 4)) =
                                 make_uint4(y[0], y[1], y[2], y[3]);
                         }
@@ -794,6 +794,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
         // with heads of 128.  (2 x 4001 tokens x 16 heads of 64: 98 against 103 us; with heads of 128 the factor costs
         // prompts 0 to 2 % and pages 4 %.)
         constexpr bool FOLD = D == 64;
+        constexpr float UP = Q4 ? Q4_LOG_UP : 0.f;   // 4-bit values are 2^-23 of themselves, weights 2^23
         const float c = p.c, factor = FOLD && p.neg ? -c : c;
         const uint32_t sign = FOLD && p.neg ? 0x80000000u : 0u, nothing = 0xff800000u ^ sign;   // -infinity
         while (ok && w.next(p)) {
@@ -840,7 +841,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                                 if (32 * b + j >= seen) x[b][j] = nothing;
                     }
                     auto weights = [&]() {
-                        const float base = m == -INFINITY ? 0.f : m * c;
+                        const float base = (m == -INFINITY ? 0.f : m * c) - UP;
                         const float2 c2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
                         float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -862,7 +863,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                         // written on trust: the check's latency runs under the store's
 #pragma unroll
                         for (int b = 0; b < 2; ++b) tmem_st16(s_at + AT_STEP * buf + 16 * b, pk[b]);
-                        look = __any_sync(0xffffffffu, real && !(sum.x + sum.y <= AT_MOST));
+                        look = __any_sync(0xffffffffu, real && !(sum.x + sum.y <= (Q4 ? AT_MOST * Q4_UP : AT_MOST)));
                     }
                     if (look) {
                         float mx[4];
@@ -916,8 +917,8 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                 const int piece = 2 * blockIdx.x + (w.a > 0 ? 0 : 1), prow = i * AT_ROWS + row;
                 const bool any = w.active(i);
                 if (limit <= 0) l = 0.f;   // no key: 0 and -infinity, under a NaN scale too
-                const float inv = l != 0.f ? 1.f / l : 0.f;
-                const float base = m == -INFINITY ? 0.f : m * c;
+                const float inv = (l != 0.f ? 1.f / l : 0.f) * (Q4 ? Q4_UP : 1.f);
+                const float base = (m == -INFINITY ? 0.f : m * c) - UP;
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b) {
                     uint32_t y[2][32];
@@ -928,6 +929,10 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                     } else {
 #pragma unroll
                         for (int j = 0; j < 64; ++j) y[j >> 5][j & 31] = 0;
+                    }
+                    if (Q4 && !closed) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) y[j >> 5][j & 31] = __float_as_uint(__uint_as_float(y[j >> 5][j & 31]) * Q4_UP);
                     }
                     if (real && closed) {
                         uint32_t o[32];
@@ -1185,14 +1190,13 @@ static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, const F4Pa
     p.neg = a.scale < 0.f;
     p.whole = ((uintptr_t)a.out & 31u) == 0;
     // a scale of 0 keeps a vanishing factor instead: the masked scores' -infinity x 0 would be NaN.  A NaN stays one.
-    p.c = fabsf(a.scale) * LOG2E;
+    p.c = fabsf(a.scale) * LOG2E * (q4 ? Q4_UP : 1.f);
     if (p.c < 1e-36f) p.c = 1e-36f;
     p.G = a.H_q / a.H_kv;
     p.tile_tokens = AT_ROWS / p.G;
     p.unit_cost = a.D == 128 ? 3 : 2;   // about 4 us, measured on packed prompts (a tile 1.3 us)
     p.few_tokens = few_tokens;
-    p.mask = 0x00780078u;
-    p.bit = 0x41804180u;
+    p.two4 = 16u;
     *launches += cut ? 2 : 1;
     auto go = [&](auto run64, auto run128) { return (a.D == 64 ? run64 : run128)(p, few, few_rows, sms, stream); };
     if (q4) return go(run<64, AT_PAGES_Q4>, run<128, AT_PAGES_Q4>);

@@ -201,6 +201,7 @@ int paged_q4(const kda_bf16_t *q, const uint8_t *k_cache, const uint8_t *v_cache
     if (lg < 0) return KDA_ERR_UNSUPPORTED;
     const int rc = validate_attn(c);
     if (rc != KDA_OK) return rc;
+    if (fabsf(scale) > 0x1p100f) return KDA_ERR_INVALID_ARG;   // times 2^23 it has to be a number (a NaN stays one)
     if (!cache_ok(num_blocks, lg) || (long long)num_blocks * H_kv > 0x7ffffffeLL || max_blocks < 0) return KDA_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return nothing_to_do();
     if ((!block_table && max_blocks > 0) || !seq_lens || !cu_seqlens || num_blocks == 0) return KDA_ERR_INVALID_ARG;

@@ -437,8 +437,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                                 top.x = fmaxf(top.x, s[n][i].x * fac[n].x);
                                 top.y = fmaxf(top.y, s[n][i].y * fac[n].y);
                             }
-                            f[n].x = raise(top.x - F4_LOG_UP, m[n].x, minus_m[n].x, l[n].x);
-                            f[n].y = raise(top.y - F4_LOG_UP, m[n].y, minus_m[n].y, l[n].y);
+                            f[n].x = raise(top.x - Q4_LOG_UP, m[n].x, minus_m[n].x, l[n].x);
+                            f[n].y = raise(top.y - Q4_LOG_UP, m[n].y, minus_m[n].y, l[n].y);
                         }
                         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -454,8 +454,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     }
 #pragma unroll
                     for (int n = 0; n < TILES; ++n) l[n] = __fadd2_rn(l[n], sum[n]);
-                    // ---- outputs: 2^-23 n s as bf16 (exact) from codes in place.  Bits 0 .. 7 of a bf16 alone are an integer times
-                    // 2^-133, below the normal numbers and in the first ones alike: 2^-133 c, or 2^-129 c from bits 4 .. 7.
+                    // ---- outputs
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
                         uint32_t bq[TILES][2];
@@ -464,7 +463,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             bq[n][0] = transpose_8x8(pk[n][2 * mt]);
                             bq[n][1] = transpose_8x8(pk[n][2 * mt + 1]);
                         }
-                        uint32_t s_even[2], s_odd[2], off[2];   // 2^110 s, 2^106 s, -8 2^-23 s
+                        Q4Scale scale[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             uint32_t x;
@@ -474,9 +473,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             } else {
                                 x = __byte_perm(word(v_scales + (16 * mt + 8 * i) * 2), 0, sel) & 0x00ff00ffu;
                             }
-                            s_even[i] = x * p.two4 + 0x6f006f00u;
-                            s_odd[i] = x * p.two4 + 0x6d006d00u;
-                            off[i] = x * p.two4 + 0xae00ae00u;
+                            scale[i] = q4_scales(x, p.two4);
                         }
                         uint32_t v[4][D / 64];
 #pragma unroll
@@ -495,11 +492,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             const uint32_t lo23 = __byte_perm(v[2][x], v[3][x], 0x5410), hi23 = __byte_perm(v[2][x], v[3][x], 0x7632);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                auto value = [&](uint32_t word, int pair) {
-                                    const uint32_t x = (j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
-                                    return q4_value(x, j & 1 ? s_odd[pair] : s_even[pair], off[pair]);
-                                };
-                                const uint32_t a0 = value(lo01, 0), a1 = value(hi01, 0), a2 = value(lo23, 1), a3 = value(hi23, 1);
+                                const uint32_t a0 = q4_pair(lo01, j, scale[0]), a1 = q4_pair(hi01, j, scale[0]);
+                                const uint32_t a2 = q4_pair(lo23, j, scale[1]), a3 = q4_pair(hi23, j, scale[1]);
 #pragma unroll
                                 for (int n = 0; n < TILES; ++n) mma_bf16(o[4 * x + j][n], a0, a1, a2, a3, bq[n][0], bq[n][1]);
                             }
@@ -524,8 +518,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                         float y[D / 8];   // channels (D / 8) g ..
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            y[2 * i] = o[i][n][x] * F4_UP;
-                            y[2 * i + 1] = o[i][n][2 + x] * F4_UP;
+                            y[2 * i] = o[i][n][x] * Q4_UP;
+                            y[2 * i + 1] = o[i][n][2 + x] * Q4_UP;
                         }
                         if (!whole) {
                             if (g == 0) sts_f2(sbase + L::ML + ((warp * 2 + part) * ROWS + row) * 8, make_float2(ref, sum));

@@ -11,8 +11,7 @@ constexpr long long F4_MAX_KEYS = 0x7fffff00;
 constexpr int F4_SHARE = 4;            // chunks a CTA has at least
 constexpr int F4_MAX_CTAS = 160;
 constexpr int F4_MAX_ROWS = 16;        // rows a unit can have
-constexpr float F4_LOG_UP = 23.f, F4_UP = 8388608.f;   // weights are 2^23 and more, values 2^-23 of what they are
-constexpr float F4_MOST = 65536.f * F4_UP;             // sum of a lane's weights that makes a warp look at its maximum
+constexpr float F4_MOST = 65536.f * Q4_UP;   // sum of a lane's weights (2^23 for 1) that makes a warp look at its maximum
 
 // Rows a unit has at most, and how a CTA is made for them
 template <int D, int ROWS>

@@ -38,30 +38,28 @@ __device__ __forceinline__ float q4_inverse(float s) {
     return y * (1.f + 0x1p-12f);
 }
 
-// Pair j (channels 2j, 2j + 1) of a word as bf16 16 + c: the code below the leading bit of 16's mantissa
-__device__ __forceinline__ uint32_t q4_raw(uint32_t word, int j) {
-    const uint32_t x = j == 0 ? word << 3 : word >> (4 * j - 3);
-    return (x & 0x00780078u) | 0x41804180u;
-}
-// (x & mask) | bit in one instruction: with a mask and a bit that the compiler knows it makes two, so they are arguments
-// of the kernels
-__device__ __forceinline__ uint32_t q4_masked(uint32_t x, uint32_t mask, uint32_t bit) {
+// (x s + d) for bf16 pairs, with one rounding
+__device__ __forceinline__ uint32_t q4_fma(uint32_t x, uint32_t s, uint32_t d) {
     uint32_t y;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(y) : "r"(x), "r"(mask), "r"(bit));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(s), "r"(d));
     return y;
 }
-// (raw - 24) s with one rounding, which there is none of: s and 24 s as bf16 pairs, both exact
-__device__ __forceinline__ uint32_t q4_value(uint32_t raw, uint32_t s2, uint32_t minus24s2) {
-    uint32_t y;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(raw), "r"(s2), "r"(minus24s2));
-    return y;
+
+// Values as bf16 pairs, 2^-23 of what they are, from codes in place.  Bits 0 .. 7 of a bf16 number alone are an integer
+// times 2^-133, below the normal numbers and among the first of them alike: pair j of a word (channels 2j, 2j + 1) is
+// 2^-133 c from bits 0 .. 3 or 2^-129 c from bits 4 .. 7, times 2^110 s or 2^106 s less 8 2^-23 s, all without a rounding.
+// Nothing larger than 2^110 will do, as 2^110 times the largest s is near the largest number there is.
+constexpr float Q4_UP = 8388608.f, Q4_LOG_UP = 23.f;
+struct Q4Scale {
+    uint32_t even, odd, off;
+};
+// ... of scale bytes in bytes 0 and 2 of `two`; two4 is 16, from memory: a product for the multiplier, which has room, not
+// a shift
+__device__ __forceinline__ Q4Scale q4_scales(uint32_t two, uint32_t two4) {
+    return {two * two4 + 0x6f006f00u, two * two4 + 0x6d006d00u, two * two4 + 0xae00ae00u};
 }
-// Scale bytes b (in byte 0 and byte 2 of `two`, the others ignored) as a bf16 pair, and -24 times it
-__device__ __forceinline__ uint32_t q4_scale2(uint32_t two) { return (two & 0x00ff00ffu) * 16u + 0x38003800u; }
-__device__ __forceinline__ uint32_t q4_offset2(uint32_t s2) {
-    uint32_t y;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(s2), "r"(0xc1c0c1c0u));   // -24
-    return y;
+__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int j, const Q4Scale &s) {
+    return q4_fma((j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu), j & 1 ? s.odd : s.even, s.off);
 }
 
 }  // namespace kda

@@ -120,11 +120,10 @@ __global__ __launch_bounds__(Q4_THREADS) void kv_write_q4_kernel(const Q4CacheAr
 
 namespace {
 // Word x of a row as 8 bf16 values
-template <int D>
 __device__ __forceinline__ uint4 values_of(uint32_t word, uint32_t b) {
-    const uint32_t s2 = q4_scale2(b * 0x00010001u), o2 = q4_offset2(s2);
-    return make_uint4(q4_value(q4_raw(word, 0), s2, o2), q4_value(q4_raw(word, 1), s2, o2),
-                      q4_value(q4_raw(word, 2), s2, o2), q4_value(q4_raw(word, 3), s2, o2));
+    const Q4Scale s = q4_scales(b * 0x00010001u, 16u);
+    auto pair = [&](int j) { return q4_fma(q4_pair(word, j, s), 0x4b004b00u, 0u); };   // 2^23
+    return make_uint4(pair(0), pair(1), pair(2), pair(3));
 }
 
 }  // namespace
@@ -142,8 +141,8 @@ __global__ __launch_bounds__(Q4_THREADS) void kv_read_q4_kernel(const Q4CacheArg
         const Q4Place at = q4_place<D>(slot, h, p.H_kv, p.block_log2);
         const uint32_t wk = reinterpret_cast<const uint32_t *>(p.k_cache + at.codes)[x];
         const uint32_t wv = reinterpret_cast<const uint32_t *>(p.v_cache + at.codes)[x];
-        a = values_of<D>(wk, p.k_cache[at.scales + x / 4]);
-        b = values_of<D>(wv, p.v_cache[at.scales + x / 4]);
+        a = values_of(wk, p.k_cache[at.scales + x / 4]);
+        b = values_of(wv, p.v_cache[at.scales + x / 4]);
     }
     __stcs(reinterpret_cast<uint4 *>(p.k_out) + (size_t)row * L + x, a);
     __stcs(reinterpret_cast<uint4 *>(p.v_out) + (size_t)row * L + x, b);

@@ -533,7 +533,7 @@ int kda_kv_read_q4(const uint8_t *k_cache, const uint8_t *v_cache, const int32_t
 
 /*
  * kda_attn_paged over such a cache: the attention of q over the values that the cache stands for, with the same
- * arguments, masks, precision and errors.
+ * arguments, masks, precision and errors; |scale| is at most 2^100.
  */
 int kda_attn_paged_q4(const kda_bf16_t *q, const uint8_t *k_cache, const uint8_t *v_cache, float scale,
                       const int32_t *block_table, const int32_t *seq_lens, const int32_t *cu_seqlens, int N,

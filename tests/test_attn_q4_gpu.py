@@ -134,6 +134,13 @@ def test_scales(scale):
         A.check(out[rows], lse[rows], Q.reference(q, c.ks[n], c.vs[n], abs(scale), first=cached))
 
 
+@pytest.mark.parametrize("power", [100, -100])
+def test_scales_far_from_one(power):
+    c = Q.PagedQ4([77, 200], [1, 20], 8, 2, 128, 16, seed=2)
+    c.scale, c.q = 0.09 * 2.0 ** power, c.q * 2.0 ** -power
+    c.check(*c.run())
+
+
 def test_nan_scale():
     c = Q.PagedQ4([20, -2], [1, 3], 2, 1, 64, 16)
     c.scale = math.nan

@@ -103,6 +103,8 @@ def test_attn_q4_refusals(lib):
         assert paged(**full, size=0) == WS and paged(**full, ws=FAKE, size=kda.kda_attn_q4_workspace_size(128) - 1) == WS
         assert paged(**full, ws=ctypes.c_void_p(FAKE.value + 16), size=1 << 30) == WS
     assert kda.kda_attn_q4_workspace_size(96) == 0
+    for scale, rc in ((2.0 ** 100, OK), (1.3e30, BAD), (-1.3e30, BAD), (float("inf"), BAD), (float("nan"), OK)):
+        assert lib.kda_attn_paged_q4(*[None] * 3, scale, *[None] * 3, 0, 0, 2, 1, 128, 4, 16, 4, None, None, None) == rc, scale
 
 
 def test_binding_refusals():
