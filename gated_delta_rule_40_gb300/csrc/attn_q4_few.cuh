@@ -16,7 +16,7 @@ constexpr float F4_MOST = 65536.f * Q4_UP;   // sum of a lane's weights (2^23 fo
 // Rows a unit has at most, and how a CTA is made for them
 template <int D, int ROWS>
 struct F4Layout {
-    static constexpr int WARPS = ROWS == 16 ? 8 : 12;
+    static constexpr int WARPS = ROWS == 16 && D == 128 ? 8 : 12;   // by registers
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int STAGES = 2;                              // a warp's ring of chunks
     static constexpr int TILES = ROWS / 8;                        // of 8 queries, the columns of a product
