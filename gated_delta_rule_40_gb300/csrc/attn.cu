@@ -50,10 +50,11 @@
 // which the start and the joining take 10 us.  The ring's 160 KiB (heads of 128) cover DRAM's latency at the 45 GB/s
 // that an SM gets of its bandwidth.  Decode with heads of 64 (a ring of 128 KiB): 256 requests, 16 heads over 8, with
 // 1.1 GB in 0.208 ms, 5.3 TB/s.
-// 4-bit pages: 24 requests with chunks of up to 512 tokens among single ones, 28 heads over 4, blocks of 16, in 142 us for
-// the chunks, where bf16 pages take 117 us: the expanding warps take issue slots and shared-memory bandwidth from the
-// softmax.  (Expanding warps that load codes into registers themselves: 187 us; by cp.async: 163 us; with fewer
-// instructions 147 us.)
+// 4-bit pages: 2 x 1024 tokens over 8192 keys, 32 heads over 8, in 201 us, where bf16 pages take 165: the expansion costs 9
+// us, the idle kernel for few rows before it 4 to 9, and 128 instead of 168 registers a thread another 9 (bf16 pages with
+// 512 threads: 175 us).  Handing registers over between warps (setmaxnreg) is ignored in relocatable device code; in a
+// module of its own, 152 and 104, the call took 193 us.  (Expanding warps that load codes into registers themselves: 187 us
+// instead of 163 by cp.async for the mixed call of 24 requests, at the time.)
 //
 // Every wait is bounded; a timeout records KDA_ERR_DEVICE_TIMEOUT and all roles stop.
 #include "attn.h"
@@ -492,12 +493,6 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
         return ok = false;
     };
 
-    if constexpr (Q4) {
-        // The softmax warps take registers over from the others: 256 threads of 168 and 256 of 88 are the launch's
-        // 512 of 128 (which the host checks).
-        if (warp < AT_ISSUER) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-    }
     if (Q4 && warp >= AT_THREADS / 32) {
         // ------------------------------------------------------------ expander (4-bit pages)
         // 4 warps write 2^-23 of a tile's values as bf16, exactly, into the ring.  A lane takes 16 bytes of codes, 32
@@ -1117,11 +1112,6 @@ cudaError_t run(const AttnParams &p, const F4Params *few, int few_rows, int grid
     if (!ready[dev & 63]) {
         e = cudaFuncSetAttribute(attn_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
         if (e != cudaSuccess) return e;
-        if (MODE == AT_PAGES_Q4) {   // its warps share out 512 x 128 registers
-            cudaFuncAttributes f;
-            if ((e = cudaFuncGetAttributes(&f, attn_kernel<D, MODE>)) != cudaSuccess) return e;
-            if (f.numRegs != 128) return cudaErrorLaunchOutOfResources;
-        }
         // the same split of an SM's memory for both kernels, so that it is not rearranged between them
         e = cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e == cudaSuccess && MODE == AT_PAGES_Q4)

@@ -4,17 +4,18 @@
 // cache's bytes, the others (prompts' chunks) by the products.  Two kernels, each of which finds its own requests
 // among the lengths on the device: attn_q4_few.cu expands codes in registers, as operands of small products, and
 // attn.cu's attn_kernel expands tiles of 128 keys into shared memory for tcgen05.  The second is launched while the
-// first runs and takes over its SMs as they become free; where it finds nothing to do it costs 2 to 4 us.  One more kernel
-// joins what both have cut.
+// first runs and takes over its SMs as they become free (in turn: 43.2 against 40.9 us for 100 decoded tokens with heads
+// of 64, 165 against 162 us for a mixed call, but 197 against 201 us for chunks alone); where it finds nothing to do it costs 1
+// to 4 us.  One more kernel joins what both have cut.
 #include "attn.h"
 #include "attn_q4_few.cuh"
 
 namespace kda {
 namespace {
 // Rows of a request up to which it is one with few.  The kernel for few takes as long for each 16 rows more, the other
-// one as long for any number up to 128.  128 requests over 4096 keys, 32 heads over 8, with 16 rows 188 against 340 us,
-// with 32 350 against 342, with 64 674 against 348; over 1024 keys with 32 rows 110 against 143 us, with 64 194 against
-// 145; a single request over 131072 keys with 32 rows 93 against 105 us, with 64 176 against 106.
+// one as long for any number up to 128.  128 requests over 4096 keys, 32 heads over 8, with 16 rows 174 against 327 us,
+// with 32 324 against 328, with 64 623 against 335; over 1024 keys with 32 rows 101 against 142 us, with 64 176 against
+// 146; a single request over 131072 keys with 32 rows 86 against 100 us, with 64 165 against 101.
 constexpr int F4_MOST_ROWS = 32;
 }  // namespace
 

@@ -24,15 +24,17 @@
 //            does not hold (tried with bf16 for what it does not: the same time)
 // Lanes read what they expand from 16-byte pieces that are exchanged by the row's place, without bank conflicts.
 //
-// What bounds it, and what it measured on the GPU.  256 decoded tokens with 0.59 GB of cache in 130 us, 4.5 TB/s: expanding
-// and multiplying take 120 us by themselves, the loads 100 us (the floor is 87 us).  A chunk costs an SM 246 cycles and 604
-// instructions, 285 of them on the logic and shift units (148 cycles at their rate) and 34 products (69); without the
-// outputs, or the scores, the loads bound it (102, 106 us), without the products themselves 128 us.  12 warps of 168
-// registers beat 16 of 128 (126.8 against 135.5 us for 128 tokens over 4096 keys; 54.6 against 55.4 with heads of 64, which
-// lose no register to memory), so that it is not latency, and 8 of 255, whose outputs and next scores were interleaved (154
-// against 136 us at the time).  8-bit products (e4m3 holds a code as it is) turn their operands into fp16 first on this chip.
-// 4 drafted tokens over 131072 keys, 16 rows: 51 us; 100 decoded tokens with heads of 64 35 us (the smaller chunks' own
-// cost); 4 decoded tokens over up to 1000 keys 8.5 us, all latency.
+// What bounds it, and what it measured on the GPU.  256 decoded tokens with 0.59 GB of cache in 117 us, 5.0 TB/s: expanding
+// and multiplying take 107 us by themselves, the loads 100 us (the floor is 87 us).  A chunk costs an SM 227 cycles, where
+// its bytes need 190, and 604 instructions, 270 of them on the logic and shift units (135 cycles at their rate) and 32
+// products (60).  12 warps of 168 registers beat 16 of 128 (115.6 against 122.2 us for 128 tokens over 4096 keys; 51.4
+// against 52.2 with heads of 64, which lose no register to memory), so that it is not latency, and 8 of 255, whose outputs
+// and next scores were interleaved (154 against 136 us at the time).  Three stages, a block's addresses once for its
+// chunks, and shifts as products (more of them for the multiplier, less for the shifter) change nothing or cost 2 to 5 %.
+// 8-bit products (e4m3 holds a code as it is) turn their operands into fp16 first on this chip.
+// 4 drafted tokens over 131072 keys, 16 rows: 48 us (two warps a scheduler, all that their registers leave room for, issue
+// in 45 % of the cycles); 100 decoded tokens with heads of 64 34 us (the smaller chunks' own cost); 4 decoded tokens over
+// up to 1000 keys 8.5 us, all latency.
 #include "attn_q4_few.cuh"
 
 namespace kda {
@@ -655,8 +657,8 @@ cudaError_t join(const F4Params &p, int rows, int grid, cudaStream_t stream) {
 
 // Rows a unit has, 8 or 16: those that a request has on average, or a single token's where the average is the other
 // kernel's.  A key's codes are expanded once a unit, but tiles of 16 columns leave registers for fewer warps.  128
-// requests over 4096 keys, 8 and 16: with 8 rows over 4 heads 77 and 102 us, with 9 131 and 103, with 12 over 8 heads 242
-// and 187, with 32 460 and 350.
+// requests over 4096 keys, 8 and 16: with 8 rows over 4 heads 67 and 94 us, with 9 116 and 94, with 12 over 8 heads 215
+// and 172, with 32 412 and 325.
 int attn_q4_few_rows(const AttnQ4Args &a, int most_rows) {
     const int G = a.H_q / a.H_kv;
     const long long rows = ((long long)a.T + a.N - 1) / a.N * G;
@@ -676,8 +678,8 @@ F4Params attn_q4_few_params(const AttnQ4Args &a, int most_rows, void *ws) {
     p.G = a.H_q / a.H_kv;
     p.over_g = (65536u + p.G - 1) / p.G;
     p.most_rows = most_rows;
-    // About 4000 cycles of a warp, whose chunks take 3100.  0, 2 and 4: 256 decoded tokens over 300 keys 39.7, 38.7 and 38.4
-    // us, over 1040 81.2, 80.2 and 80.3; 128 x 16 rows over 1024 67.5, 66.8 and 68.4
+    // About 4000 cycles of a warp, whose chunks take 2700.  0, 2 and 4: 256 decoded tokens over 300 keys 34.2, 32.6 and 32.3
+    // us, 64 over 4096 65.7, 66.2 and 67.5; 128 x 16 rows over 1024 60.7, 60.5 and 61.3
     p.unit_cost = 2;
     p.two20 = 1u << 20;
     p.two4 = 1u << 4;

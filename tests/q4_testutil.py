@@ -69,12 +69,10 @@ def bf16_values(x):
 def reference(q, k, v, scale, first=0):
     """A.reference, with room for what computing with the codes themselves adds:
 
-    * A block's product of q with codes 1024 + c and 64 + c, less what the 1024 + 8 and 64 + 8 add: at most three
-      roundings of 2^-24 (two products of 16 channels, the difference), of at most 1039 sum|q|.  A score is off by
-      e = scale 2^-22 1039 sum over blocks of s sum|q|, a weight by a factor of 2 e more.  A block's s is at most a sixth
-      of its largest value (its largest n is 6 or 7, as scales are 1.125 apart or less), or 2^-15 for a block of zeros.
-    * The sums over codes c = 8 + n, less 8 times the sum of p s, are off by 2^-19 of 16 sum p s (chains of up to 32
-      fp32 additions, 2^-24 each).
+    * A block's product of q with codes c = 8 + n, less 8 times q's sum: at most four roundings of 2^-24 (two products of
+      16 channels, the sum, the difference) of at most 15 + 8 times sum|q|.  A score is off by e = scale 2^-22 23 sum over
+      blocks of s sum|q|, a weight by a factor of 2 e more.  A block's s is at most a sixth of its largest value (its
+      largest n is 6 or 7, as scales are 1.125 apart or less), or 2^-15 for a block of zeros.
     * An exponential below 2^-126 of the largest may become 0, which takes at most 2^-126 |v_j| from a sum of which
       the largest term's weight is 1: 2^-126 L max |v| over L keys.  It shows where v is 0 in every key of weight,
       which values rounded to 4 bits often are.  bf16's smallest step is 2^-133."""
@@ -87,12 +85,10 @@ def reference(q, k, v, scale, first=0):
     s = torch.einsum("ahd,lhd->ahl", q, k.repeat_interleave(G, 1)) * scale
     p = torch.where(seen[:, None, :], torch.exp(s - torch.where(torch.isfinite(l), l, 0.0)[..., None]), 0.0)
     ks = torch.where(seen[:, :, None, None], (k.unflatten(-1, (-1, 32)).abs().amax(-1) / 6 + 2.0 ** -15)[None], 0.0).amax(1)
-    e = scale * 2.0 ** -22 * 1039 * (ks.repeat_interleave(G, 1) * q.unflatten(-1, (-1, 32)).abs().sum(-1)).sum(-1)
-    steps = v.unflatten(-1, (-1, 32)).abs().amax(-1) / 6 + 2.0 ** -15
-    ps = torch.einsum("ahl,lhb->ahb", p, steps.repeat_interleave(G, 1)).repeat_interleave(32, -1)
+    e = scale * 2.0 ** -22 * 23 * (ks.repeat_interleave(G, 1) * q.unflatten(-1, (-1, 32)).abs().sum(-1)).sum(-1)
     sums = torch.einsum("ahl,lhd->ahd", p, v.abs().repeat_interleave(G, 1))
     tiny = 2.0 ** -126 * k.shape[0] * float(v.abs().max()) + 2.0 ** -133
-    return o, l, to + torch.expm1(2 * e)[..., None] * sums + 2.0 ** -19 * 16 * ps + tiny, tl + e
+    return o, l, to + torch.expm1(2 * e)[..., None] * sums + tiny, tl + e
 
 
 class PagedQ4(A.Paged):
