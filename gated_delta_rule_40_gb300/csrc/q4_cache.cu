@@ -1,8 +1,9 @@
 // The paged key/value cache held in 4 bits: the quantising store of new keys and values, and rows read back.
 //
 // Both are one pass over rows, lanes on neighbouring 32 (store) or 16 (read) bytes, codes and bf16 rows in whole
-// sectors.  On the GPU, 32768 tokens x 8 heads of 128: store 30 us, 5.6 TB/s, bound by instructions (with one word a
-// lane, and rounding by conversions to integers, 52 us); read 25 us, 6.7 TB/s, DRAM.  64 tokens: 2 us each.
+// sectors.  On the GPU, 32768 tokens x 8 heads of 128, back to back: store 28 us, 6.0 TB/s (with one word a lane, and
+// rounding by conversions to integers, 52 us; with five instead of six blocks an SM 28.9 us); read 27.4 us, 6.2 TB/s
+// (one row a lane 32.6, four 28.1; blocks of 256 threads 30.2 us).  64 tokens: 2 us each.
 #include "attn_q4.h"
 #include "q4.cuh"
 
@@ -10,6 +11,7 @@ namespace kda {
 namespace {
 
 constexpr int Q4_THREADS = 256;
+constexpr int Q4_READ_THREADS = 128, Q4_READS = 2;   // rows that a lane reads
 
 // Byte offsets of a row's codes and scales in a cache
 struct Q4Place {
@@ -63,7 +65,7 @@ __device__ __forceinline__ uint32_t no_nan(uint32_t w) {
 
 // A lane takes 16 channels of a (token, head) of k and the same ones of v: two words, half a block of 32.
 template <int D>
-__global__ __launch_bounds__(Q4_THREADS) void kv_write_q4_kernel(const Q4CacheArgs p, uint32_t rows) {
+__global__ __launch_bounds__(Q4_THREADS, 6) void kv_write_q4_kernel(const Q4CacheArgs p, uint32_t rows) {
     constexpr uint32_t L = D / 16;
     const uint32_t row = blockIdx.x * (Q4_THREADS / L) + threadIdx.x / L, x = threadIdx.x % L;
     const bool on = row < rows;
@@ -128,44 +130,62 @@ __device__ __forceinline__ uint4 values_of(uint32_t word, uint32_t b) {
 
 }  // namespace
 
+// A lane takes 8 channels of Q4_READS rows, whose loads are in flight together.
 template <int D>
-__global__ __launch_bounds__(Q4_THREADS) void kv_read_q4_kernel(const Q4CacheArgs p, uint32_t rows) {
-    constexpr uint32_t L = D / 8;
-    const uint32_t row = blockIdx.x * (Q4_THREADS / L) + threadIdx.x / L, x = threadIdx.x % L;
-    if (row >= rows) return;
-    const uint32_t t = row / (uint32_t)p.H_kv, h = row - t * (uint32_t)p.H_kv;
-    const long long slot = p.slots[t];
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (slot >= p.num_slots) set_status(KDA_ERR_BAD_PAGES);
-    if (slot >= 0 && slot < p.num_slots) {
-        const Q4Place at = q4_place<D>(slot, h, p.H_kv, p.block_log2);
-        const uint32_t wk = reinterpret_cast<const uint32_t *>(p.k_cache + at.codes)[x];
-        const uint32_t wv = reinterpret_cast<const uint32_t *>(p.v_cache + at.codes)[x];
-        a = values_of(wk, p.k_cache[at.scales + x / 4]);
-        b = values_of(wv, p.v_cache[at.scales + x / 4]);
+__global__ __launch_bounds__(Q4_READ_THREADS) void kv_read_q4_kernel(const Q4CacheArgs p, uint32_t rows) {
+    constexpr uint32_t L = D / 8, STEP = Q4_READ_THREADS / L;
+    const uint32_t row0 = blockIdx.x * (Q4_READS * STEP) + threadIdx.x / L, x = threadIdx.x % L;
+    long long slot[Q4_READS];
+    uint32_t head[Q4_READS], k[Q4_READS], v[Q4_READS], ks[Q4_READS], vs[Q4_READS];
+#pragma unroll
+    for (int i = 0; i < Q4_READS; ++i) {
+        const uint32_t row = row0 + i * STEP, t = row / (uint32_t)p.H_kv;
+        head[i] = row - t * (uint32_t)p.H_kv;
+        slot[i] = row < rows ? p.slots[t] : -1;
+        if (slot[i] >= p.num_slots) {
+            set_status(KDA_ERR_BAD_PAGES);
+            slot[i] = -1;
+        }
     }
-    __stcs(reinterpret_cast<uint4 *>(p.k_out) + (size_t)row * L + x, a);
-    __stcs(reinterpret_cast<uint4 *>(p.v_out) + (size_t)row * L + x, b);
+#pragma unroll
+    for (int i = 0; i < Q4_READS; ++i) {
+        k[i] = v[i] = 0x88888888u;   // zeros
+        ks[i] = vs[i] = 0;
+        if (slot[i] < 0) continue;
+        const Q4Place at = q4_place<D>(slot[i], head[i], p.H_kv, p.block_log2);
+        k[i] = reinterpret_cast<const uint32_t *>(p.k_cache + at.codes)[x];
+        v[i] = reinterpret_cast<const uint32_t *>(p.v_cache + at.codes)[x];
+        ks[i] = p.k_cache[at.scales + x / 4];
+        vs[i] = p.v_cache[at.scales + x / 4];
+    }
+#pragma unroll
+    for (int i = 0; i < Q4_READS; ++i) {
+        const uint32_t row = row0 + i * STEP;
+        if (row >= rows) continue;
+        __stcs(reinterpret_cast<uint4 *>(p.k_out) + (size_t)row * L + x, values_of(k[i], ks[i]));
+        __stcs(reinterpret_cast<uint4 *>(p.v_out) + (size_t)row * L + x, values_of(v[i], vs[i]));
+    }
 }
+
 namespace {
-// Blocks for rows of which a lane takes `channels`
-unsigned grid_of(const Q4CacheArgs &a, int channels) {
-    const unsigned rows = Q4_THREADS / (a.D / channels);   // a block
+// Blocks of `threads` lanes that take `channels` of `each` rows
+unsigned grid_of(const Q4CacheArgs &a, int threads, int channels, int each) {
+    const unsigned rows = threads / (a.D / channels) * each;   // a block
     return (unsigned)(((long long)a.T * a.H_kv + rows - 1) / rows);
 }
 }  // namespace
 
 cudaError_t launch_kv_write_q4(const Q4CacheArgs &a, cudaStream_t stream) {
     const uint32_t rows = (uint32_t)a.T * (uint32_t)a.H_kv;   // below 2^31, as the entry point checks
-    if (a.D == 64) kv_write_q4_kernel<64><<<grid_of(a, 16), Q4_THREADS, 0, stream>>>(a, rows);
-    else kv_write_q4_kernel<128><<<grid_of(a, 16), Q4_THREADS, 0, stream>>>(a, rows);
+    if (a.D == 64) kv_write_q4_kernel<64><<<grid_of(a, Q4_THREADS, 16, 1), Q4_THREADS, 0, stream>>>(a, rows);
+    else kv_write_q4_kernel<128><<<grid_of(a, Q4_THREADS, 16, 1), Q4_THREADS, 0, stream>>>(a, rows);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read_q4(const Q4CacheArgs &a, cudaStream_t stream) {
     const uint32_t rows = (uint32_t)a.T * (uint32_t)a.H_kv;
-    if (a.D == 64) kv_read_q4_kernel<64><<<grid_of(a, 8), Q4_THREADS, 0, stream>>>(a, rows);
-    else kv_read_q4_kernel<128><<<grid_of(a, 8), Q4_THREADS, 0, stream>>>(a, rows);
+    if (a.D == 64) kv_read_q4_kernel<64><<<grid_of(a, Q4_READ_THREADS, 8, Q4_READS), Q4_READ_THREADS, 0, stream>>>(a, rows);
+    else kv_read_q4_kernel<128><<<grid_of(a, Q4_READ_THREADS, 8, Q4_READS), Q4_READ_THREADS, 0, stream>>>(a, rows);
     return cudaGetLastError();
 }
 
