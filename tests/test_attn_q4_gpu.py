@@ -198,6 +198,20 @@ def test_bad_blocks_count_as_zeros():
         c.check(out, lse)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("entry", [0, 1, 5, 6])
+def test_bad_blocks_of_a_pair(entry, D):
+    """Blocks of 16 rows, of which a chunk of 32 keys takes two: the first, the second, one in the last chunk."""
+    kda = _kda()
+    c = Q.PagedQ4([100, 90], [1, 3], 4, 2, D, 16, seed=entry)
+    c.table[0, entry] = -7
+    c.ks[0][entry * 16:(entry + 1) * 16] = 0
+    c.vs[0][entry * 16:(entry + 1) * 16] = 0
+    out, lse = c.run()
+    assert kda.kda_get_status() == kda.KDA_ERR_BAD_PAGES
+    c.check(out, lse)
+
+
 def test_nothing_to_do():
     kda = _kda()
     c = Q.PagedQ4([], [], 4, 2, 128, 16, pad=3)
