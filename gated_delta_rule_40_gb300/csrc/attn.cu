@@ -159,7 +159,7 @@ struct Request {
     __host__ __device__ void load(const AttnParams &p, int n) {
         if (p.a.cu) {
             row0 = p.a.cu[n];
-            fresh = p.a.cu[n + 1] - row0;
+            fresh = (int)((uint32_t)p.a.cu[n + 1] - (uint32_t)row0);   // (offsets that fall are found by comparing them)
             keys = p.a.lens ? p.a.lens[n] : fresh;
         } else {
             row0 = n * p.a.T;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
     grid_dep_launch();   // the joining kernel may come as soon as CTAs leave
     if (Q4 && p.few_tokens > 0) {   // all requests with few tokens, as when decoding: 1 us sooner than by the sums below
         bool any = false;
-        for (int n = tid; n < p.a.N; n += THREADS) any |= p.a.cu[n + 1] - p.a.cu[n] > p.few_tokens;
+        for (int n = tid; n < p.a.N; n += THREADS) any |= (long long)p.a.cu[n + 1] - p.a.cu[n] > p.few_tokens;
         if (!__syncthreads_or(any)) {
             if (tid == 0) p.join[blockIdx.x].pieces = 0;
             grid_dep_wait();   // (lengths are checked by the kernel for few)

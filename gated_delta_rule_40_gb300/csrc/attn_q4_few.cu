@@ -97,7 +97,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
         F4Request r;
         for (int n = n0; n < n1; ++n) {
             r.load(p, n, ROWS);
-            if (r.fresh < 0 || r.keys < 0 || r.keys > most) bad = true;
+            // offsets that fall, by more than 2^31 too, which their difference does not show
+            if (p.a.cu[n + 1] < r.row0 || r.keys < 0 || r.keys > most) bad = true;
             else mine += r.length(p, ROWS) * p.a.H_kv;
         }
         long long before = mine;

@@ -62,7 +62,7 @@ struct F4Request {
     int row0, fresh, keys, rows, units;
     __device__ void load(const F4Params &p, int n, int R) {
         row0 = p.a.cu[n];
-        fresh = p.a.cu[n + 1] - row0;
+        fresh = (int)((uint32_t)p.a.cu[n + 1] - (uint32_t)row0);   // (offsets that fall are found by comparing them)
         keys = p.a.lens[n];
         const long long r = (long long)fresh * p.G;
         rows = fresh > 0 && r <= p.most_rows ? (int)r : 0;
