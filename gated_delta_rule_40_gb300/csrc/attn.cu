@@ -62,6 +62,8 @@
 #include "kda_tma.cuh"
 #include "attn_q4_few.cuh"
 
+#include <cfloat>
+
 namespace kda {
 
 constexpr int AT_KEYS = 128;                 // keys a tile
@@ -791,6 +793,9 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
         constexpr bool FOLD = D == 64;
         constexpr float UP = Q4 ? Q4_LOG_UP : 0.f;   // 4-bit values are 2^-23 of themselves, weights 2^23
         const float c = p.c, factor = FOLD && p.neg ? -c : c;
+        // What a row's exponents are taken from: m c, or the lowest number where that is below it, so that such scores
+        // weigh nothing (m c = -infinity would make them NaN) and the first one in range makes a step look.
+        auto base_of = [&](float m) { return (m == -INFINITY ? 0.f : fmaxf(m * c, -FLT_MAX)) - UP; };
         const uint32_t sign = FOLD && p.neg ? 0x80000000u : 0u, nothing = 0xff800000u ^ sign;   // -infinity
         while (ok && w.next(p)) {
             const bool closed = w.a == 0 && w.b == w.all;
@@ -836,7 +841,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                                 if (32 * b + j >= seen) x[b][j] = nothing;
                     }
                     auto weights = [&]() {
-                        const float base = (m == -INFINITY ? 0.f : m * c) - UP;
+                        const float base = base_of(m);
                         const float2 c2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
                         float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -913,7 +918,7 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                 const bool any = w.active(i);
                 if (limit <= 0) l = 0.f;   // no key: 0 and -infinity, under a NaN scale too
                 const float inv = (l != 0.f ? 1.f / l : 0.f) * (Q4 ? Q4_UP : 1.f);
-                const float base = (m == -INFINITY ? 0.f : m * c) - UP;
+                const float base = base_of(m);
 #pragma unroll
                 for (int b = 0; b < D / 64; ++b) {
                     uint32_t y[2][32];

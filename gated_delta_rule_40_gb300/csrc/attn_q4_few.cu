@@ -37,6 +37,8 @@
 // up to 1000 keys 8.5 us, all latency.
 #include "attn_q4_few.cuh"
 
+#include <cfloat>
+
 namespace kda {
 namespace {
 
@@ -303,7 +305,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                 // each block of 32.  Codes come as 2^-24 c and 2^-20 c = 2^-24 (c 2^4), whose queries are 2^-4 of the others,
                 // and c is 8 + n: a block's product is off by 2^-24 8 times the queries' sum.
                 uint32_t q[TILES][BLOCKS][4];
-                float2 excess[TILES][BLOCKS], m[TILES], minus_m[TILES], l[TILES], factor[TILES];   // minus_m: 0 for -infinity
+                float2 excess[TILES][BLOCKS], m[TILES], minus_m[TILES], l[TILES], factor[TILES];
                 int limit[TILES][2];
                 float o[MT][TILES][4];
 #pragma unroll
@@ -342,8 +344,10 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
                         limit[n][x] = w.r.keys - w.r.fresh + f4_token(p, min(w.first + 8 * n + 2 * t + x, w.first + w.rows - 1)) + 1;
+                    // -m, finite: without a reference yet, scores of -infinity weigh nothing and any other makes a chunk look
                     m[n] = make_float2(-INFINITY, -INFINITY);
-                    minus_m[n] = l[n] = make_float2(0.f, 0.f);
+                    minus_m[n] = make_float2(FLT_MAX, FLT_MAX);
+                    l[n] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -433,7 +437,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             }
                         }
                     };
-                    // A row that sees no key of the piece's first chunk sees none of the piece: its reference stays -infinity
+                    // A row that sees no key of the piece's first chunk sees none of the piece: its reference stays -infinity.  (So it
+                    // does, until a chunk has another, where all scores are below the lowest number.)
                     bool look = c == w.a;
                     if (!look) {
                         weights();
