@@ -22,6 +22,7 @@
 // them cost more moves than they save.  A call of 64 tokens takes 3.1 us, and the host 17.
 #include "qk_rope.h"
 #include "kda_common.cuh"
+#include "launch.h"
 
 #include <type_traits>
 
@@ -29,6 +30,7 @@ namespace kda {
 namespace {
 
 constexpr int QR_THREADS = 256, QR_WARPS = QR_THREADS / 32;
+constexpr int QR_FWD_CTAS = 3, QR_BWD_CTAS = 2;   // of an SM at once, by registers
 
 // 1 / (2 pi), the first 128 bits after the binary point
 constexpr unsigned long long INV_2PI_HI = 0x28be60db9391054aull, INV_2PI_LO = 0x7f09d5f47d4d3770ull;
@@ -143,7 +145,7 @@ __device__ __forceinline__ void load_weight(const float *w, const Lane &x, float
 
 // ---------------------------------------------------------------- forward
 template <int D, bool NORM, bool PAIRS>
-__global__ __launch_bounds__(QR_THREADS, 3) void qk_rope_kernel(const QkRopeArgs p, int per, int chunks) {
+__global__ __launch_bounds__(QR_THREADS, QR_FWD_CTAS) void qk_rope_kernel(const QkRopeArgs p, int per, int chunks) {
     constexpr int L = D / 8, ROWS = 32 / L, EACH = 4 / ROWS, UNROLL = 4;
     const int lane = threadIdx.x & 31, row = lane / L, l = lane - row * L;
     const Lane x = lane_of<D>(p, l);
@@ -216,7 +218,7 @@ __global__ __launch_bounds__(QR_THREADS, 3) void qk_rope_kernel(const QkRopeArgs
 // Each warp walks tokens with a fixed stride and keeps the weights' gradients of its rows in registers; a CTA
 // adds its warps' up in a fixed order, and qk_rope_dw_kernel the CTAs', so that bits repeat.
 template <int D, bool NORM, bool PAIRS>
-__global__ __launch_bounds__(QR_THREADS, 2) void qk_rope_bwd_kernel(const QkRopeArgs p, int per, int chunks, float *partial) {
+__global__ __launch_bounds__(QR_THREADS, QR_BWD_CTAS) void qk_rope_bwd_kernel(const QkRopeArgs p, int per, int chunks, float *partial) {
     constexpr int L = D / 8, ROWS = 32 / L, EACH = 4 / ROWS, UNROLL = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane / L, l = lane - row * L;
     grid_dep_launch();   // the sum of the weights' gradients may come as soon as CTAs leave
@@ -344,7 +346,6 @@ __global__ __launch_bounds__(256) void qk_rope_dw_kernel(const float *partial, i
 }
 
 namespace {
-constexpr int QR_FWD_CTAS = 152 * 3, QR_BWD_CTAS = 152 * 2;   // resident at once
 constexpr int QR_MAX_CHUNKS = 32;   // looked at
 constexpr int QR_ITEM_COST = 8, QR_LEAST = 4;
 
@@ -371,19 +372,23 @@ void split(const QkRopeArgs &a, int warps, int *per, int *chunks) {
 
 template <int D, bool NORM, bool PAIRS>
 cudaError_t forward(const QkRopeArgs &a, cudaStream_t stream) {
+    const int resident = sm_count() * QR_FWD_CTAS;
+    if (resident == 0) return cudaErrorInvalidDevice;
     int per, chunks;
-    split(a, QR_FWD_CTAS * QR_WARPS, &per, &chunks);
-    const long long want = ((long long)a.T * chunks + QR_WARPS - 1) / QR_WARPS, grid = want < QR_FWD_CTAS ? want : QR_FWD_CTAS;
+    split(a, resident * QR_WARPS, &per, &chunks);
+    const long long want = ((long long)a.T * chunks + QR_WARPS - 1) / QR_WARPS, grid = want < resident ? want : resident;
     qk_rope_kernel<D, NORM, PAIRS><<<(unsigned)grid, QR_THREADS, 0, stream>>>(a, per, chunks);
     return cudaGetLastError();
 }
 
 template <int D, bool NORM, bool PAIRS>
 cudaError_t backward(const QkRopeArgs &a, float *partial, int *n, cudaStream_t stream) {
+    const int resident = sm_count() * QR_BWD_CTAS;
+    if (resident == 0) return cudaErrorInvalidDevice;
     int per, chunks;
-    split(a, QR_BWD_CTAS * QR_WARPS, &per, &chunks);
+    split(a, resident * QR_WARPS, &per, &chunks);
     const long long want = ((long long)a.T * chunks + QR_WARPS - 1) / QR_WARPS;
-    *n = (int)(want < QR_BWD_CTAS ? want : QR_BWD_CTAS);
+    *n = (int)(want < resident ? want : resident);
     qk_rope_bwd_kernel<D, NORM, PAIRS><<<(unsigned)*n, QR_THREADS, 0, stream>>>(a, per, chunks, partial);
     return cudaGetLastError();
 }
@@ -399,7 +404,7 @@ cudaError_t dispatch(const QkRopeArgs &a, bool bwd, float *partial, int *n, cuda
 }
 }  // namespace
 
-size_t qk_rope_bwd_workspace_bytes(int D) { return sizeof(float) * 2 * D * QR_BWD_CTAS; }
+size_t qk_rope_bwd_workspace_bytes(int D) { return sizeof(float) * 2 * D * MAX_SMS * QR_BWD_CTAS; }
 
 cudaError_t launch_qk_rope(const QkRopeArgs &a, cudaStream_t stream) {
     return a.D == 64 ? dispatch<64>(a, false, nullptr, nullptr, stream) : dispatch<128>(a, false, nullptr, nullptr, stream);
