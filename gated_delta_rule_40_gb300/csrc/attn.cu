@@ -60,6 +60,7 @@
 #include "attn.h"
 #include "kda_common.cuh"
 #include "kda_tma.cuh"
+#include "launch.h"
 #include "attn_q4_few.cuh"
 
 #include <cfloat>
@@ -315,9 +316,6 @@ __device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t *w, boo
     }
 }
 
-__device__ __forceinline__ void copy_16_bytes(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
-}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
 template <int D, int MODE>
@@ -591,9 +589,9 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
                     for (int c = 0; c < COPIES; ++c) {
                         const int h = c * ROWS_AT_ONCE / 16;
                         const size_t from = __shfl_sync(0xffffffffu, codes_at, h) + in_codes + (c * ROWS_AT_ONCE - 16 * h) * (D / 2);
-                        if (good >> h & 1u) copy_16_bytes(to + at + c * 512, cache + from);
+                        if (good >> h & 1u) cp_async16(to + at + c * 512, cache + from);
                     }
-                    if (has_piece) copy_16_bytes(scales_to + at, cache + piece);
+                    if (has_piece) cp_async16(scales_to + at, cache + piece);
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar + 8 * (L::CF + slot)) : "memory");
                     if (lane == 0) {
                         *reinterpret_cast<volatile uint32_t *>(sm + L::GOOD + 4 * slot) = good;
@@ -1044,20 +1042,6 @@ __global__ __launch_bounds__(256, 4) void attn_q4_join_both_kernel(const AttnPar
 
 // ---------------------------------------------------------------- host side
 namespace {
-constexpr int AT_MAX_CTAS = 160;
-
-int sm_count() {
-    static int count[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (!count[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        count[dev] = n < AT_MAX_CTAS ? n : AT_MAX_CTAS;
-    }
-    return count[dev];
-}
-
 // A bf16 tensor of n dimensions, the first of channels, with the others' strides in elements, in 128-byte
 // swizzled boxes
 cudaError_t tensor_map(CUtensorMap *m, const void *base, int n, const long long *sizes, const long long *strides,
@@ -1078,8 +1062,6 @@ cudaError_t tensor_map(CUtensorMap *m, const void *base, int n, const long long 
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-
-size_t align256_at(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <int D, int MODE>
 cudaError_t run(const AttnParams &p, const F4Params *few, int few_rows, int grid, cudaStream_t stream) {
@@ -1165,8 +1147,8 @@ cudaError_t run(const AttnParams &p, const F4Params *few, int few_rows, int grid
 bool attn_may_cut(const AttnArgs &a) { return a.lens || a.T > (2 * AT_LEAST - 1) * AT_KEYS; }
 
 size_t attn_workspace_bytes(int D) {
-    return align256_at(sizeof(JoinDesc) * AT_MAX_CTAS) + align256_at(sizeof(float2) * 256 * 2 * AT_MAX_CTAS) +
-           sizeof(float) * 256 * D * 2 * AT_MAX_CTAS;
+    return align256(sizeof(JoinDesc) * MAX_SMS) + align256(sizeof(float2) * 256 * 2 * MAX_SMS) +
+           sizeof(float) * 256 * D * 2 * MAX_SMS;
 }
 
 static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, const F4Params *few, int few_rows, void *ws,
@@ -1178,9 +1160,9 @@ static cudaError_t launch(const AttnArgs &a, bool q4, int few_tokens, const F4Pa
     const bool cut = attn_may_cut(a);
     char *base = static_cast<char *>(ws);
     p.join = cut ? reinterpret_cast<JoinDesc *>(base) : nullptr;
-    base += align256_at(sizeof(JoinDesc) * AT_MAX_CTAS);
+    base += align256(sizeof(JoinDesc) * MAX_SMS);
     p.ml = reinterpret_cast<float2 *>(base);
-    base += align256_at(sizeof(float2) * 256 * 2 * AT_MAX_CTAS);
+    base += align256(sizeof(float2) * 256 * 2 * MAX_SMS);
     p.o = reinterpret_cast<float *>(base);
     p.neg = a.scale < 0.f;
     p.whole = ((uintptr_t)a.out & 31u) == 0;

@@ -36,6 +36,7 @@
 // in 45 % of the cycles); 100 decoded tokens with heads of 64 34 us (the smaller chunks' own cost); 4 decoded tokens over
 // up to 1000 keys 8.5 us, all latency.
 #include "attn_q4_few.cuh"
+#include "launch.h"
 
 #include <cfloat>
 
@@ -59,9 +60,6 @@ __device__ __forceinline__ float2 lds_f2(uint32_t a) {
 }
 __device__ __forceinline__ void sts_f4(uint32_t a, float4 x) {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
-}
-__device__ __forceinline__ void cp16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
 }
 template <int TO, int FROM>
 __device__ __forceinline__ void cp16_at(uint32_t to, const void *from) {
@@ -217,7 +215,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                 cp16_at<L::CODES + 1024, 1024>(at, v);
                 cp16_at<L::CODES + 1536, 1536>(at, v);
             }
-            if (lane < 2 * scale_lanes) cp16(to + scale_to, scale_from + slab + id_row * (D / 32));
+            if (lane < 2 * scale_lanes) cp_async16(to + scale_to, scale_from + slab + id_row * (D / 32));
         } else if (box != F4_KEYS && (uint32_t)id[0] < blocks && (uint32_t)id[1] < blocks) {
             // two blocks of 16 rows (124 against 151 us in the loop below, 256 decoded tokens over 2040 keys; 118 with larger blocks)
             const size_t slab = (size_t)((uint32_t)id[0] * (uint32_t)p.a.H_kv + (uint32_t)id_hk) * slab_bytes;
@@ -237,7 +235,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
             // (twice the lanes for the scales, each of its block's)
             const bool second = lane >= 2 * scale_lanes;
             if (lane < 4 * scale_lanes)
-                cp16(to + (second ? scale_second : scale_to), (second ? scale_from_second + next : scale_from + slab));
+                cp_async16(to + (second ? scale_second : scale_to), (second ? scale_from_second + next : scale_from + slab));
         } else {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
@@ -251,15 +249,15 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                 const float zeros = __uint_as_float(0x88888888u);   // codes of zeros, for rows without a block
                 for (int i = 0; i < box * PER_ROW / 32; ++i) {
                     if (good) {
-                        cp16(at + 512 * i, k + 512 * i);
-                        cp16(at + 512 * i + L::CODES, v + 512 * i);
+                        cp_async16(at + 512 * i, k + 512 * i);
+                        cp_async16(at + 512 * i + L::CODES, v + 512 * i);
                     } else {
                         sts_f4(at + 512 * i, make_float4(zeros, zeros, zeros, zeros));
                         sts_f4(at + 512 * i + L::CODES, make_float4(zeros, zeros, zeros, zeros));
                     }
                 }
                 if (lane < 2 * scale_lanes) {
-                    if (good) cp16(scales, scale_from + slab + id_row * (D / 32));
+                    if (good) cp_async16(scales, scale_from + slab + id_row * (D / 32));
                     else sts_f4(scales, make_float4(0.f, 0.f, 0.f, 0.f));
                 }
             }
@@ -640,20 +638,6 @@ __global__ __launch_bounds__(256) void attn_q4_join_kernel(const F4Params p) {
 
 // ---------------------------------------------------------------- host side
 namespace {
-int sm_count() {
-    static int count[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (!count[dev]) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        count[dev] = n < F4_MAX_CTAS ? n : F4_MAX_CTAS;
-    }
-    return count[dev];
-}
-
-size_t align256_f4(size_t x) { return (x + 255) & ~(size_t)255; }
-
 template <int D, int ROWS>
 cudaError_t run(const F4Params &p, int grid, cudaStream_t stream) {
     using L = F4Layout<D, ROWS>;
@@ -700,9 +684,9 @@ F4Params attn_q4_few_params(const AttnQ4Args &a, int most_rows, void *ws) {
     p.a = a;
     char *base = static_cast<char *>(ws);
     p.join = reinterpret_cast<F4Join *>(base);
-    base += align256_f4(sizeof(F4Join) * F4_MAX_CTAS);
+    base += align256(sizeof(F4Join) * MAX_SMS);
     p.ml = reinterpret_cast<float2 *>(base);
-    base += align256_f4(sizeof(float2) * 2 * F4_MAX_CTAS * F4_MAX_ROWS);
+    base += align256(sizeof(float2) * 2 * MAX_SMS * F4_MAX_ROWS);
     p.o = reinterpret_cast<float *>(base);
     p.c = a.scale * LOG2E;
     p.G = a.H_q / a.H_kv;
@@ -717,8 +701,8 @@ F4Params attn_q4_few_params(const AttnQ4Args &a, int most_rows, void *ws) {
 }
 
 size_t attn_q4_few_workspace_bytes(int D) {
-    return align256_f4(sizeof(F4Join) * F4_MAX_CTAS) + align256_f4(sizeof(float2) * 2 * F4_MAX_CTAS * F4_MAX_ROWS) +
-           sizeof(float) * 2 * F4_MAX_CTAS * F4_MAX_ROWS * D;
+    return align256(sizeof(F4Join) * MAX_SMS) + align256(sizeof(float2) * 2 * MAX_SMS * F4_MAX_ROWS) +
+           sizeof(float) * 2 * MAX_SMS * F4_MAX_ROWS * D;
 }
 
 cudaError_t launch_attn_q4_few(const F4Params &p, int rows, cudaStream_t stream, int *launches) {

@@ -11,7 +11,6 @@ constexpr long long F4_MAX_KEYS = 0x7fffff00;
 // Chunks a CTA has at least (a token over 1000 keys, 8 heads: 4 10.6 us, 1 11.2, 12 11.3, 24 12.7; four such: 10.9, 10.9,
 // 11.4, 12.8)
 constexpr int F4_SHARE = 4;
-constexpr int F4_MAX_CTAS = 160;
 constexpr int F4_MAX_ROWS = 16;        // rows a unit can have
 constexpr float F4_MOST = 65536.f * Q4_UP;   // sum of a lane's weights (2^23 for 1) that makes a warp look at its maximum
 
