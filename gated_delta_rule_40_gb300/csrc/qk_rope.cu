@@ -6,8 +6,8 @@
 //
 // Angle.  position x f in fp32 is off by radians at far positions, so angles are kept in turns as fixed-point
 // fractions of 64 bits: F = f / (2 pi) 2^64 from f's mantissa times 128 bits of 1 / (2 pi) (Payne and Hanek's
-// reduction), position x F modulo 2^64 is the fraction of a turn to 2^-33 at any int32 position, and the
-// function of pi x takes it from there.
+// reduction), position x F modulo 2^64 is the fraction of a turn to 2^-33 at any int32 position.  It is rounded to fp32,
+// by 2^-26 of a turn at most, which moves a cosine by 2^-23, and the function of pi x takes it from there.
 //
 // Layout.  A row (a head's D channels) is D / 8 lanes with two runs of four channels each: a lane that turns
 // holds both channels of its four pairs (half-split pairs: 4l .. and R / 2 + 4l ..; neighbours: 8l ..), so a

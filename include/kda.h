@@ -469,8 +469,9 @@ int kda_attn_paged_ws(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_
  *                 contiguous, and must not overlap the inputs otherwise
  *
  * D is 64 or 128, rot_dim a multiple of 8 from 0 to D (KDA_ERR_UNSUPPORTED otherwise); eps is not negative.
- * Statistics, angles and products are fp32 or better (the angle is exact to 2^-31 of a turn before its cosine, at
- * any position), rounded once to bf16.  Tensors must be 16-byte aligned, weights, freqs and positions 4-byte.
+ * Statistics, angles and products are fp32 or better, rounded once to bf16.  An angle is a fraction of a turn that is
+ * exact to 2^-33 at any position, and is rounded to fp32, by 2^-26 of a turn at most, before its cosine is taken.
+ * Tensors must be 16-byte aligned, weights, freqs and positions 4-byte.
  */
 int kda_qk_norm_rope(const kda_bf16_t *q, const kda_bf16_t *k, int64_t q_stride, int64_t k_stride,
                      const float *q_weight, const float *k_weight, float eps, int norm, const float *freqs,

@@ -1,7 +1,11 @@
-"""GPU tests of the query/key norms with rotation: the workspace's size, whatever the device's number of SMs."""
+"""GPU tests of the query/key norms with rotation: the workspace's size, whatever the device's number of SMs, and the angles
+by themselves."""
+from fractions import Fraction
+
 import pytest
 import torch
 
+from qk_rope_testutil import _PI as PI
 from qk_rope_testutil import freqs_of, grad_bounds, gradients
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +42,28 @@ def test_the_workspace_holds_what_is_written(T, D):
         _, dw = gradients(x, pos, freqs, weight, 1e-6, True, False, d)
         _, tol = grad_bounds(x, pos, freqs, weight, 1e-6, True, False, d)
         assert ((got[name].double().cpu() - dw).abs() - tol).max() <= 0
+
+
+@pytest.mark.parametrize("far", [1, 4000, 1 << 24, (1 << 31) - 1])
+def test_angles(far):
+    """cos and sin of the angles themselves: the gradients of (1, 0) pairs, which are fp32.  The fraction of a turn is
+    rounded to fp32 once, 2^-26 of a turn at most beside the 2^-33 of its own, and the function is off by 2^-24 (an
+    ulp) of at most 1, with room for another."""
+    from gated_delta_rule_40_gb300 import kda
+    g = torch.Generator().manual_seed(far & 1023)
+    pos = torch.randint(0, far + 1, (300,), generator=g).to(torch.int32)
+    pos[0] = far
+    freqs = freqs_of(128)
+    freqs[:6] = torch.tensor([3.0, 6.2831855, 100.25, -0.7, 1e-6, 1e7])
+    x = torch.zeros((300, 1, 128), dtype=torch.bfloat16, device="cuda")
+    x[..., :64] = 1.0
+    got = kda.kda_qk_norm_rope_bwd(x, x, pos.cuda(), freqs.cuda(), x, x, norm=False)["dq"][:, 0].double().cpu()
+    turn = 2 * PI
+    ang = torch.empty((300, 64), dtype=torch.float64)   # reduced in exact arithmetic, near positions too
+    for j, f in enumerate(Fraction(float(f)) for f in freqs):
+        for i, p in enumerate(pos.tolist()):
+            a = p * f
+            ang[i, j] = float(a - turn * round(a / turn))
+    bound = 2 * 3.1416 * (2.0 ** -26 + 2.0 ** -33) + 2.0 ** -23
+    assert (got[:, :64] - torch.cos(ang)).abs().max() <= bound
+    assert (got[:, 64:] + torch.sin(ang)).abs().max() <= bound
