@@ -469,6 +469,8 @@ int kda_attn_paged_ws(const kda_bf16_t *q, const kda_bf16_t *k_cache, const kda_
  *                 contiguous, and must not overlap the inputs otherwise
  *
  * D is 64 or 128, rot_dim a multiple of 8 from 0 to D (KDA_ERR_UNSUPPORTED otherwise); eps is not negative.
+ * The squares are summed in fp32: a row whose sum is above its range (channels past 10^18) becomes zeros, and with eps = 0
+ * a row's mean square has to be 2^-126 or more (a row of zeros gives NaN).
  * Statistics, angles and products are fp32 or better, rounded once to bf16.  An angle is a fraction of a turn that is
  * exact to 2^-33 at any position, and is rounded to fp32, by 2^-26 of a turn at most, before its cosine is taken.
  * Tensors must be 16-byte aligned, weights, freqs and positions 4-byte.

@@ -1,5 +1,5 @@
-"""GPU tests of the query/key norms with rotation: the workspace's size, whatever the device's number of SMs, and the angles
-by themselves."""
+"""GPU tests of the query/key norms with rotation: the workspace's size, whatever the device's number of SMs, the angles
+by themselves, and rows whose mean square has no fp32 number."""
 from fractions import Fraction
 
 import pytest
@@ -67,3 +67,35 @@ def test_angles(far):
     bound = 2 * 3.1416 * (2.0 ** -26 + 2.0 ** -33) + 2.0 ** -23
     assert (got[:, :64] - torch.cos(ang)).abs().max() <= bound
     assert (got[:, 64:] + torch.sin(ang)).abs().max() <= bound
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pairs", [False, True])
+def test_rows_out_of_the_range_of_their_mean_square(D, pairs):
+    """Squares are summed in fp32: rows whose sum is above its range become zeros, with gradients of 0, and without eps a
+    row of zeros is 0 / 0.  Other rows are as they are alone."""
+    from gated_delta_rule_40_gb300 import kda
+    g = torch.Generator().manual_seed(D)
+    q, k, dq, dk = (torch.randn((6, h, D), generator=g).to(torch.bfloat16) for h in (4, 2, 4, 2))
+    w, pos, freqs = 1.0 + 0.3 * torch.randn((2, D), generator=g), torch.arange(6, dtype=torch.int32) + 50, freqs_of(D)
+    args = [x.cuda() for x in (pos, freqs, dq, dk, w[0], w[1])]
+    run = lambda q, **kw: (*kda.kda_qk_norm_rope(q, k.cuda(), *args[:2], *args[4:], interleaved=pairs, **kw),  # noqa: E731
+                           kda.kda_qk_norm_rope_bwd(q, k.cuda(), *args, interleaved=pairs, **kw))
+    keep, keepk, grads = run(q.cuda())
+    big = q.clone()
+    big[2, 1] *= 2.0 ** 70   # the squares' sum is 2^140 or more
+    big[4, 3] *= 2.0 ** 50   # 2^107: within the range
+    out, outk, got = run(big.cuda())
+    assert not out[2, 1].any() and not got["dq"][2, 1].any()
+    same = torch.ones((6, 4), dtype=torch.bool)
+    same[2, 1] = same[4, 3] = False
+    assert torch.equal(out.cpu()[same], keep.cpu()[same]) and torch.equal(got["dq"].cpu()[same], grads["dq"].cpu()[same])
+    assert torch.equal(outk, keepk) and torch.equal(got["dk"], grads["dk"]) and torch.equal(got["dk_weight"], grads["dk_weight"])
+    # (eps, 1e-6 of a mean square of 1, is 2^-21 of the root)
+    off = (out[4, 3].double() - keep[4, 3].double()).abs().cpu()
+    assert (off <= 2.0 ** -8 * 2 * keep[4, 3].double().abs().cpu() + 2.0 ** -18 * 4).all()
+    assert torch.isfinite(got["dq_weight"]).all()
+    big[2, 1] = 0
+    out, _, got = run(big.cuda(), eps=0.0)
+    assert torch.isnan(out[2, 1]).all() and torch.isnan(got["dq"][2, 1]).all()
+    assert torch.isfinite(out.cpu()[same]).all() and torch.isfinite(got["dq"].cpu()[same]).all()
