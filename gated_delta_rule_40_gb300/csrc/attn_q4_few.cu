@@ -5,7 +5,8 @@
 // of 32 keys that its last row sees.  The chunks of all units, and a constant for each unit's own cost, form one line, cut
 // into equal shares: one a warp, so that few units are shared at all.  (With the warps of a CTA all on one unit, every one
 // of them pays for every unit's beginning and end: 518 against 166 us for 256 decoded tokens, at the time.)  What a share's
-// ends cut is joined in shared memory among a CTA's warps, and by attn_q4_join_kernel among CTAs, in a fixed order.
+// ends cut is joined in shared memory among a CTA's warps, and among CTAs by attn_q4_join_kernel, or by
+// attn_q4_join_both_kernel (attn.cu) where the kernel for chunks runs too, in a fixed order.
 //
 // A warp by itself, with no barrier until the end: cp.async of a chunk into one of two stages, the next but one in flight
 // while it works.  Both products are small ones (mma.sync) with the keys as rows: 16 keys x 16 channels times 8 queries
@@ -13,8 +14,8 @@
 // registers.  tcgen05, whose rows are 128, would take operands from shared or tensor memory, which costs more here than
 // what they compute.
 //   scores   codes as fp16 in place, without an exponent (2^-24 c or 2^-20 c), one mask each and one shift a word of 8; q as
-//            fp16 times a power of two, which keeps every channel; 8 times the sum of q is taken off, and the keys' scale
-//            is applied, for each block of 32 channels in fp32.  (With an exponent, 1024 + c and 64 + c, the sums are
+//            fp16 times a power of two, which keeps every channel down to 2^-27 of the row's largest (and 2^-35 of that of a
+//            smaller one); 8 times the sum of q is taken off, and the keys' scale is applied, for each block of 32 channels in fp32.  (With an exponent, 1024 + c and 64 + c, the sums are
 //            exact to 2^-22 of 1039 instead of 15 times the queries' sum: lse was 1e-4 off.)
 //   weights  2^(s c - m), c = scale log2(e), with the reference m of the piece's first chunk, which moves when a sum of
 //            weights passes 2^16; rounded to bf16 as operands, like attn.cu's
@@ -27,10 +28,14 @@
 // What bounds it, and what it measured on the GPU.  256 decoded tokens with 0.59 GB of cache in 117 us, 5.0 TB/s: expanding
 // and multiplying take 107 us by themselves, the loads 100 us (the floor is 87 us).  A chunk costs an SM 227 cycles, where
 // its bytes need 190, and 604 instructions, 270 of them on the logic and shift units (135 cycles at their rate) and 32
-// products (60).  12 warps of 168 registers beat 16 of 128 (115.6 against 122.2 us for 128 tokens over 4096 keys; 51.4
-// against 52.2 with heads of 64, which lose no register to memory), so that it is not latency, and 8 of 255, whose outputs
-// and next scores were interleaved (154 against 136 us at the time).  Three stages, a block's addresses once for its
-// chunks, and shifts as products (more of them for the multiplier, less for the shifter) change nothing or cost 2 to 5 %.
+// products (60).  No unit is at its limit: instructions issue in 62 % of the cycles, the logic unit is busy 55 %, the
+// tensor cores 26 %, DRAM 64 % of its peak, and what warps wait for most is their own last instruction (1.43 an issue), with
+// three warps a scheduler.  So it is chains of dependent instructions, and their number.  More warps are no way out: 12 of 168
+// registers beat 16 of 128 (115.6 against 122.2 us for 128 tokens over 4096 keys; 51.4 against 52.2 with heads of 64,
+// which lose no register to memory), and 8 of 255, whose outputs and next scores were interleaved (154 against 136 us at
+// the time).  Products that start at the offsets, two additions less in a score's chain (118.8 against 118.0 us), three
+// stages, a block's addresses once for its chunks, and shifts as products (more of them for the multiplier, less for
+// the shifter) change nothing or cost up to 5 %.
 // 8-bit products (e4m3 holds a code as it is) turn their operands into fp16 first on this chip.
 // 4 drafted tokens over 131072 keys, 16 rows: 48 us (two warps a scheduler, all that their registers leave room for, issue
 // in 45 % of the cycles); 100 decoded tokens with heads of 64 34 us (the smaller chunks' own cost); 4 decoded tokens over
@@ -435,8 +440,8 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                             }
                         }
                     };
-                    // A row that sees no key of the piece's first chunk sees none of the piece: its reference stays -infinity.  (So it
-                    // does, until a chunk has another, where all scores are below the lowest number.)
+                    // A row that sees no key of the piece's first chunk sees none of the piece: its reference stays -infinity.  (It also
+                    // does where all that it sees scores below the lowest number, until another score makes a chunk look.)
                     bool look = c == w.a;
                     if (!look) {
                         weights();

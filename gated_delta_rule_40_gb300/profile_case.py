@@ -25,8 +25,10 @@ bwdc_gradk_kernel, bwdc_jacobian_kernel and bwdc_dalog_kernel; one for ``kda_dec
 ``--bf16-state``; one for ``kda_decode_step``; two for ``kda_attn_fwd`` and ``kda_attn_paged``:
 attn_kernel and attn_join_kernel, with a key/value head to four query heads; ``attn_decode``
 gives each of ``--B`` requests one token over a cache of ``--T``, ``attn_decode_q4`` over one held in 4 bits,
-``attn_chunk_q4`` a chunk of 1024 tokens; four with the 4-bit cache: attn_q4_few_kernel, attn_kernel,
-attn_join_kernel and attn_q4_join_kernel).  A profiler then selects launches by kernel name and index (e.g.
+``attn_chunk_q4`` a chunk of 1024 tokens; three with the 4-bit cache: attn_q4_few_kernel, attn_kernel and
+attn_q4_join_both_kernel, or two where all tokens together make 32 rows or fewer: attn_q4_few_kernel and
+attn_q4_join_kernel; one for ``rope``: qk_rope_kernel; two for ``rope_bwd``: qk_rope_bwd_kernel and
+qk_rope_dw_kernel).  A profiler then selects launches by kernel name and index (e.g.
 ``ncu -k regex:intra_kernel -s 2 -c 1``).  ``--kernel-times`` (kda and bwd) times the
 last iteration's kernels with the library's CUDA events instead and prints them.
 """
