@@ -791,9 +791,10 @@ __global__ __launch_bounds__(AttnLayout<D, MODE>::THREADS, 1) void attn_kernel(c
         constexpr bool FOLD = D == 64;
         constexpr float UP = Q4 ? Q4_LOG_UP : 0.f;   // 4-bit values are 2^-23 of themselves, weights 2^23
         const float c = p.c, factor = FOLD && p.neg ? -c : c;
-        // What a row's exponents are taken from: m c, or the lowest number where that is below it, so that such scores
-        // weigh nothing (m c = -infinity would make them NaN) and the first one in range makes a step look.
-        auto base_of = [&](float m) { return (m == -INFINITY ? 0.f : fmaxf(m * c, -FLT_MAX)) - UP; };
+        // What a row's exponents are taken from: m c, or the lowest or largest number where that is past it.  So scores below
+        // the range weigh nothing (m c = -infinity would make them NaN) and the first one in range makes a step look, and
+        // scores above it weigh infinitely, which ends as NaN (m c = infinity would make them nothing).
+        auto base_of = [&](float m) { return (m == -INFINITY ? 0.f : fminf(fmaxf(m * c, -FLT_MAX), FLT_MAX)) - UP; };
         const uint32_t sign = FOLD && p.neg ? 0x80000000u : 0u, nothing = 0xff800000u ^ sign;   // -infinity
         while (ok && w.next(p)) {
             const bool closed = w.a == 0 && w.b == w.all;

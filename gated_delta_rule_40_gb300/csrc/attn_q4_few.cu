@@ -14,8 +14,8 @@
 // registers.  tcgen05, whose rows are 128, would take operands from shared or tensor memory, which costs more here than
 // what they compute.
 //   scores   codes as fp16 in place, without an exponent (2^-24 c or 2^-20 c), one mask each and one shift a word of 8; q as
-//            fp16 times a power of two, which keeps every channel down to 2^-27 of the row's largest (and 2^-35 of that of a
-//            smaller one); 8 times the sum of q is taken off, and the keys' scale is applied, for each block of 32 channels in fp32.  (With an exponent, 1024 + c and 64 + c, the sums are
+//            fp16 times a power of two, which keeps every channel down to 2^-27 of the row's largest (a smaller one is off by
+//            2^-35 of that at most); 8 times the sum of q is taken off, and the keys' scale is applied, for each block of 32 channels in fp32.  (With an exponent, 1024 + c and 64 + c, the sums are
 //            exact to 2^-22 of 1039 instead of 15 times the queries' sum: lse was 1e-4 off.)
 //   weights  2^(s c - m), c = scale log2(e), with the reference m of the piece's first chunk, which moves when a sum of
 //            weights passes 2^16; rounded to bf16 as operands, like attn.cu's
@@ -461,7 +461,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                                 if (!(top > m + 8.f)) return 1.f;
                                 const float f = ex2(m - top);
                                 m = top;
-                                minus_m = -top;
+                                minus_m = -fminf(top, FLT_MAX);   // (a score above the range weighs infinitely: NaN in the end)
                                 l *= f;
                                 move = true;
                                 return f;

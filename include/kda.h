@@ -401,7 +401,7 @@ int kda_kv_write(const kda_bf16_t *k, const kda_bf16_t *v, const int32_t *slots,
  * KDA_ERR_BAD_SEQLENS and writes nothing.  Scores, the softmax's statistics and the
  * output sums are fp32; the weights exp(s - a reference of the row) enter the second product rounded to bf16.
  * A score below fp32's range weighs nothing (a row of such scores alone: out = 0, lse = -infinity); one above it
- * gives NaN.
+ * makes its row's out NaN (and lse NaN or infinity).
  * The values a query may not see are multiplied by an exact 0, so a NaN or infinity
  * in v of a later token of the same prompt reaches earlier tokens, as it does in a masked matrix
  * product; tokens of other prompts never do.

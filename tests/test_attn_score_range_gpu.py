@@ -1,5 +1,5 @@
 """GPU tests of attention where the range of scores ends: those that fall below the smallest fp32 number weigh
-nothing, and what follows them counts."""
+nothing, and what follows them counts; those past the largest make their rows NaN."""
 import math
 
 import pytest
@@ -80,3 +80,46 @@ def test_bf16_scores_below_the_smallest_number(paged, D, sign):
     got = out[150:].double().cpu().unflatten(1, (Hkv, H // Hkv))
     assert ((got - want[:, :, None]).abs() - 2.0 ** -8 * (want.abs() + 1.02 * size)[:, :, None]).max() <= 0
     assert (lse[150:].double().cpu() - n.log()[:, None]).abs().max() <= 2.0 ** -20 * 8
+
+
+@pytest.mark.parametrize("form", ["decode", "drafted", "chunk", "pages", "prompt"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("at", [0, 5, 70, 290])
+def test_scores_above_the_largest_number(at, sign, D, form):
+    """One key that scores past fp32's range among others of score 0: NaN for the tokens that see it, not a plain mean or
+    nothing.  Rows that do not see it are as they are without it."""
+    from gated_delta_rule_40_gb300 import kda
+    H, Hkv, L, bs = 8, 2, 300, 16
+    new = {"decode": 1, "drafted": 4, "chunk": 250}.get(form, L)
+    q4 = form in ("decode", "drafted", "chunk")
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    g = torch.Generator().manual_seed(at)
+    big = 2.0 ** 120 if q4 else 2.0 ** 60
+    q = torch.full((40 * new if form == "decode" else new, H, D), big, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros((304, Hkv, D), dtype=torch.bfloat16)
+    k[at] = sign * (12000.0 if q4 else 2.0 ** 59)
+    v = torch.randn((304, Hkv, D), generator=g).to(torch.bfloat16)
+    scale = sign * (D ** -0.5 if q4 else 64.0)
+    N = q.shape[0] // new
+    lens, cu, table = ints([L] * N), ints([new * n for n in range(N + 1)]), ints([list(range(19))] * N)
+
+    def run(k):
+        if form == "prompt":
+            return (x[0] for x in kda.kda_attn_fwd(q[None], k[None, :L].cuda(), v[None, :L].cuda(), scale))
+        if form == "pages":
+            pages = [x.cuda().unflatten(0, (19, bs)).transpose(1, 2).contiguous() for x in (k, v)]
+            return kda.kda_attn_paged(q, *pages, table, lens, cu, scale)
+        cache = [torch.zeros((19, Hkv, bs, kda.q4_row_bytes(D)), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        kda.kda_kv_write_q4(k.cuda(), v.cuda(), torch.arange(304, dtype=torch.int32, device="cuda"), *cache)
+        return kda.kda_attn_paged_q4(q, *cache, table, lens, cu, scale)
+
+    out, lse = run(k)
+    plain, plain_lse = run(torch.zeros_like(k))
+    first = L - new   # position of a request's first token
+    sees = torch.tensor([first + i >= at for _ in range(N) for i in range(new)])
+    assert torch.isnan(out[sees.cuda()]).all()
+    l = lse[sees.cuda()]
+    assert (torch.isnan(l) | (l == math.inf)).all()
+    assert torch.equal(out[~sees.cuda()], plain[~sees.cuda()]) and torch.equal(lse[~sees.cuda()], plain_lse[~sees.cuda()])
+    assert torch.isfinite(plain).all()
