@@ -329,8 +329,10 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     const uint32_t e = most ? min(268u - (most >> 23), 253u) : 127u;
                     const float up = __uint_as_float(e << 23);
                     const float down = most >= 0x7f800000u ? NAN : __uint_as_float((254u - e) << 23);
-                    // queries 2t and 2t + 1 are the columns of this lane's scores
-                    factor[n] = make_float2(p.c * __shfl_sync(0xffffffffu, down, 8 * t), p.c * __shfl_sync(0xffffffffu, down, 8 * t + 4));
+                    // queries 2t and 2t + 1 are the columns of this lane's scores.  (A factor past the range would make a score of
+                    // 0 NaN, and at the range's end any other is past it as it should.)
+                    const float mine = p.c * down, f = fabsf(mine) == INFINITY ? copysignf(FLT_MAX, mine) : mine;
+                    factor[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
 #pragma unroll
                     for (int b = 0; b < BLOCKS; ++b) {
                         float sum = 0.f;

@@ -123,3 +123,28 @@ def test_scores_above_the_largest_number(at, sign, D, form):
     assert (torch.isnan(l) | (l == math.inf)).all()
     assert torch.equal(out[~sees.cuda()], plain[~sees.cuda()]) and torch.equal(lse[~sees.cuda()], plain_lse[~sees.cuda()])
     assert torch.isfinite(plain).all()
+
+
+@pytest.mark.parametrize("new", [1, 4, 30])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale", [2.0 ** 60, -2.0 ** 60, 2.0 ** 100])
+def test_large_queries_under_a_large_scale(scale, D, new):
+    """Queries times the scale past fp32's range: scores of exactly 0 stay, lower ones vanish."""
+    from gated_delta_rule_40_gb300 import kda
+    H, Hkv, L, bs = 8, 2, 200, 16
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    g = torch.Generator().manual_seed(new)
+    k = torch.zeros((208, Hkv, D), dtype=torch.bfloat16)
+    k[1:120:2] = -1.0 if scale > 0 else 1.0
+    v = torch.randn((208, Hkv, D), generator=g).to(torch.bfloat16)
+    cache = [torch.zeros((13, Hkv, bs, kda.q4_row_bytes(D)), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    kda.kda_kv_write_q4(k.cuda(), v.cuda(), torch.arange(208, dtype=torch.int32, device="cuda"), *cache)
+    q = torch.full((new, H, D), 2.0 ** 110, dtype=torch.bfloat16, device="cuda")
+    out, lse = kda.kda_attn_paged_q4(q, *cache, ints([list(range(13))]), ints([L]), ints([0, new]), scale)
+    values = Q.bf16_values(v).double()
+    for i in range(new):
+        rows = torch.cat([values[0:120:2], values[120:L - new + 1 + i]])
+        want, size = rows.mean(0), rows.abs().mean(0)
+        got = out[i].double().cpu().unflatten(0, (Hkv, H // Hkv))
+        assert ((got - want[:, None]).abs() - 2.0 ** -8 * (want.abs() + 1.02 * size)[:, None]).max() <= 0
+        assert (lse[i].double().cpu() - math.log(len(rows))).abs().max() <= 2.0 ** -20 * 8
