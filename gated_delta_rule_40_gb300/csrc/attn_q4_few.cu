@@ -15,8 +15,9 @@
 // what they compute.
 //   scores   codes as fp16 in place, without an exponent (2^-24 c or 2^-20 c), one mask each and one shift a word of 8; q as
 //            fp16 times a power of two, which keeps every channel down to 2^-27 of the row's largest (a smaller one is off by
-//            2^-35 of that at most); 8 times the sum of q is taken off, and the keys' scale is applied, for each block of 32 channels in fp32.  (With an exponent, 1024 + c and 64 + c, the sums are
-//            exact to 2^-22 of 1039 instead of 15 times the queries' sum: lse was 1e-4 off.)
+//            2^-35 of that at most); 8 times the sum of q is taken off, and the keys' scale is applied, for each block of
+//            32 channels in fp32.  (With an exponent, 1024 + c and 64 + c, the sums are exact to 2^-22 of 1039 instead of
+//            15 times the queries' sum: lse was 1e-4 off.)
 //   weights  2^(s c - m), c = scale log2(e), with the reference m of the piece's first chunk, which moves when a sum of
 //            weights passes 2^16; rounded to bf16 as operands, like attn.cu's
 //   outputs  codes of two keys in the halves of a register, as bf16 without an exponent, times the keys' scales less 8 of
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(F4Layout<D, ROWS>::THREADS, 1) void attn_q4_few_ker
                     const float up = __uint_as_float(e << 23);
                     const float down = most >= 0x7f800000u ? NAN : __uint_as_float((254u - e) << 23);
                     // queries 2t and 2t + 1 are the columns of this lane's scores.  (A factor past the range would make a score of
-                    // 0 NaN, and at the range's end any other is past it as it should.)
+                    // 0 NaN; under one at the range's end any other is still too far away to share the weight.)
                     const float mine = p.c * down, f = fabsf(mine) == INFINITY ? copysignf(FLT_MAX, mine) : mine;
                     factor[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
 #pragma unroll
